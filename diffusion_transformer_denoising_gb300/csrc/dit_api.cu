@@ -15,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/dit.h"
+#include "api_common.h"
 #include "kernels.h"
 
 using namespace dit;
@@ -23,7 +24,9 @@ using namespace dit;
 static thread_local char g_last_error[512] = "";
 static int g_fail_alloc_after = 0;  // test hook: fail the n-th next allocation
 
-static dit_status fail(dit_status s, const char* fmt, ...) {
+namespace dit {
+
+dit_status fail(dit_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -31,16 +34,9 @@ static dit_status fail(dit_status s, const char* fmt, ...) {
   return s;
 }
 
-#define CU_TRY(expr)                                                                                    \
-  do {                                                                                                  \
-    cudaError_t e_ = (expr);                                                                            \
-    if (e_ != cudaSuccess) return fail(DIT_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString(e_)); \
-  } while (0)
-#define DIT_TRY(expr)                 \
-  do {                                \
-    dit_status s_ = (expr);           \
-    if (s_ != DIT_OK) return s_;      \
-  } while (0)
+void clear_last_error() { g_last_error[0] = 0; }
+
+}  // namespace dit
 
 static dit_status dev_alloc(void** p, size_t bytes) {
   *p = nullptr;

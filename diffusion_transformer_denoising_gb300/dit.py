@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -21,7 +22,11 @@ LIB_PATH = os.environ.get("DIT_LIB") or os.path.join(_PKG, "libdit.so")
 DIT_OK, DIT_ERR_INVALID_ARG, DIT_ERR_SHAPE, DIT_ERR_NOT_LOADED, DIT_ERR_OOM, DIT_ERR_CUDA, DIT_ERR_TIMEOUT = range(7)
 PREC_BF16, PREC_F32, PREC_FP8 = 0, 1, 2
 COND_CROSS, COND_JOINT = 0, 1
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_SPLIT = 0, 1
+ROPE_MAX_AXES, ROPE_MAX_HEAD_DIM = 4, 256
+POS_I32, POS_F32 = 0, 1
+ACT_NONE, ACT_SILU = 0, 1
 LOOP_PARTIAL_SCHEDULE = 1
 LOOP_CUDA_GRAPH = 2
 
@@ -30,7 +35,8 @@ EXPORTS = ["dit_create", "dit_load_weights", "dit_num_params", "dit_param_info",
            "dit_patch_embed", "dit_block_forward", "dit_final_layer", "cfg_combine", "flow_euler_step",
            "dit_denoise_loop", "dit_synchronize", "dit_device_bytes", "dit_destroy", "dit_status_string",
            "dit_last_error", "dit_debug_fail_alloc_after", "dit_debug_gemm_cta_pairs", "dit_debug_stall", "dit_profile_start", "dit_profile_stop",
-           "dit_timestep_modulation_noalloc"]
+           "dit_timestep_modulation_noalloc", "dit_rope_forward", "dit_rope_backward", "dit_rope_workspace_bytes",
+           "dit_group_norm_forward", "dit_group_norm_backward", "dit_group_norm_workspace_bytes"]
 NOALLOC_MAX_BATCH, NOALLOC_MAX_HIDDEN = 64, 262144
 
 KERNEL_KINDS = ["gemm_qkv", "gemm_out", "gemm_cross_q", "gemm_cross_kv", "gemm_ffn1", "gemm_ffn2", "gemm_embed",
@@ -94,6 +100,12 @@ def lib():
         "dit_debug_stall": ([vp, vp], C.c_int),
         "dit_profile_start": ([vp, C.c_int], C.c_int),
         "dit_profile_stop": ([vp, C.POINTER(i64), C.POINTER(C.c_double)], C.c_int),
+        "dit_rope_forward": ([vp, vp], C.c_int),
+        "dit_rope_backward": ([vp, vp, i64, vp], C.c_int),
+        "dit_rope_workspace_bytes": ([vp], i64),
+        "dit_group_norm_forward": ([vp, vp, i64, vp], C.c_int),
+        "dit_group_norm_backward": ([vp, vp, i64, vp], C.c_int),
+        "dit_group_norm_workspace_bytes": ([vp, C.c_int], i64),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -163,6 +175,232 @@ def cfg_combine(vc, vu, g: float, v, n: int, stream=None):
 
 def flow_euler_step(x, v, sigma: float, sigma_next: float, n: int, stream=None):
     _check(lib().flow_euler_step(_ptr(x), _ptr(v), sigma, sigma_next, n, _stream(stream)))
+
+
+# ------------------------------------------------------------- operators
+# dit_rope_args and dit_group_norm_args of include/dit.h, packed in one go
+_ROPE_ARGS = struct.Struct("<2q8i2fQ2q2i" + 2 * "2iQ3qQ3qQ3q2Q")
+_GN_ARGS = struct.Struct("<2q4ifiQ2qQ2qQ2q6Q")
+_NO_VIEW = (0, 0, 0, 0)
+_dtype_codes = None
+
+
+def _dtype_code(t):
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    try:
+        return _dtype_codes[t.dtype]
+    except KeyError:
+        raise DitError(DIT_ERR_INVALID_ARG, f"unsupported dtype {t.dtype}") from None
+
+
+def _refuse(status, msg):
+    raise DitError(status, msg)
+
+
+def _param(name, t, shape, device):
+    """Pointer of an optional contiguous float32 tensor of this shape."""
+    if t is None:
+        return 0
+    if t.device != device:
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} is on {t.device}, not {device}")
+    if t.element_size() != 4 or not t.is_floating_point():
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} must be float32")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        _refuse(DIT_ERR_SHAPE, f"{name} must be contiguous {list(shape)}")
+    return t.data_ptr()
+
+
+def _launch_on(device, workspace, stream, need, args):
+    """(workspace pointer, bytes, stream) of a call on `device`."""
+    import torch
+    if device.type != "cuda":
+        _refuse(DIT_ERR_INVALID_ARG, f"tensors are on {device}, not on a CUDA device")
+    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+    if need is None:
+        return 0, 0, s
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            _refuse(DIT_ERR_INVALID_ARG, f"the workspace must be contiguous memory on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), s
+    n = need(args)
+    if n < 0:
+        raise DitError(DIT_ERR_INVALID_ARG, lib().dit_last_error().decode())
+    if n == 0:
+        return 0, 0, s
+    if stream is not None:
+        _refuse(DIT_ERR_INVALID_ARG, "a call on an explicit stream needs its workspace passed in")
+    # torch's allocator hands the block out in the order of the current stream, which is the call's
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws.data_ptr(), n, s
+
+
+def _heads_view(name, t, like):
+    """(pointer, batch, token and head strides) of a [batch, tokens, heads, head_dim] view."""
+    if t.shape != like.shape:
+        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(like.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} has another dtype or device")
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1 and t.numel():
+        _refuse(DIT_ERR_SHAPE, f"{name}: the channels of a head must be contiguous")
+    return t.data_ptr(), sb, st, sh
+
+
+def _rope_heads(tag, x, dy, out, weight, dweight, ref):
+    """Packed dit_rope_heads of one tensor; ref is (batch, tokens, head_dim, dtype, device)."""
+    if out is None:
+        if x is not None or dy is not None or weight is not None or dweight is not None:
+            _refuse(DIT_ERR_INVALID_ARG, f"{tag} is given without its output")
+        return (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
+    if out.dim() != 4 or (out.shape[0], out.shape[1], out.shape[3]) != ref[:3]:
+        _refuse(DIT_ERR_SHAPE, f"{tag} is {list(out.shape)}: [{ref[0]}, {ref[1]}, heads, {ref[2]}] is wanted")
+    if out.dtype != ref[3] or out.device != ref[4]:
+        _refuse(DIT_ERR_INVALID_ARG, f"{tag} has another dtype or device")
+    return (out.shape[2], 0,
+            *(_NO_VIEW if x is None else _heads_view(f"{tag} input", x, out)),
+            *(_NO_VIEW if dy is None else _heads_view(f"{tag} gradient", dy, out)),
+            *_heads_view(f"{tag} output", out, out),
+            _param(f"{tag}_weight", weight, (ref[2],), ref[4]), _param(f"d{tag}_weight", dweight, (ref[2],), ref[4]))
+
+
+def _rope_args(pos, axes, theta, style, eps, first, q, k):
+    import torch
+    B, N, _, d = first.shape if first.dim() == 4 else _refuse(DIT_ERR_SHAPE, "q must be [batch, tokens, heads, head_dim]")
+    n = len(axes)
+    if not 1 <= n <= ROPE_MAX_AXES:
+        _refuse(DIT_ERR_INVALID_ARG, f"1 to {ROPE_MAX_AXES} axes are supported")
+    if pos.dim() not in (2, 3) or tuple(pos.shape[-2:]) != (N, n) or (pos.dim() == 3 and pos.shape[0] != B):
+        _refuse(DIT_ERR_SHAPE, f"positions are {list(pos.shape)}: [{N}, {n}] or [{B}, {N}, {n}] is wanted")
+    if pos.dtype not in (torch.int32, torch.float32) or pos.device != first.device:
+        _refuse(DIT_ERR_INVALID_ARG, "positions must be int32 or float32 on the tensors' device")
+    ps = pos.stride()
+    if n > 1 and ps[-1] != 1 and pos.numel():
+        _refuse(DIT_ERR_SHAPE, "the axes of a position must be contiguous")
+    ref = (B, N, d, first.dtype, first.device)
+    return _ROPE_ARGS.pack(B, N, d, _dtype_code(first), style, n, *axes, *(0,) * (4 - n), theta, eps, pos.data_ptr(),
+                           ps[0] if pos.dim() == 3 else 0, ps[-2], POS_F32 if pos.is_floating_point() else POS_I32, 0,
+                           *_rope_heads("q", *q, ref), *_rope_heads("k", *k, ref))
+
+
+def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, style=ROPE_INTERLEAVED, q_weight=None,
+                     k_weight=None, eps=1e-6, stream=None):
+    """Turn q (and k) [batch, tokens, heads, head_dim] by positions with
+    several axes, behind a per-head RMS norm where a weight is given.
+
+    pos: int32 or float32 [tokens, len(axes)], or [batch, tokens, len(axes)];
+    axes: rotary channels per axis; q_out / k_out may be q / k themselves.
+    Views may have any strides with contiguous heads; k may have its own
+    number of heads (see dit_rope_forward in include/dit.h)."""
+    args = _rope_args(pos, axes, theta, style, eps, q, (q, None, q_out, q_weight, None),
+                      (k, None, k_out, k_weight, None))
+    _check(lib().dit_rope_forward(args, _launch_on(q.device, None, stream, None, args)[2]))
+
+
+def dit_rope_backward(pos, dq_out, dq, dk_out=None, dk=None, *, axes, theta=1e4, style=ROPE_INTERLEAVED, q=None,
+                      k=None, q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, eps=1e-6, workspace=None,
+                      stream=None):
+    """Gradient of dit_rope_forward: dq (and dk) from dq_out (and dk_out);
+    with a weight the forward's input q (k) is read, and d{q,k}_weight
+    (float32 [head_dim], overwritten) is computed where given.  workspace: a
+    contiguous tensor of dit_rope_workspace_bytes, or None to take one from
+    torch's allocator (only on torch's current stream)."""
+    args = _rope_args(pos, axes, theta, style, eps, dq_out, (q, dq_out, dq, q_weight, dq_weight),
+                      (k, dk_out, dk, k_weight, dk_weight))
+    L = lib()
+    ws, n, s = _launch_on(dq_out.device, workspace, stream,
+                          None if dq_weight is None and dk_weight is None else L.dit_rope_workspace_bytes, args)
+    _check(L.dit_rope_backward(args, ws, n, s))
+
+
+def dit_rope_workspace_bytes(head_dim: int) -> int:
+    """Workspace of dit_rope_backward when weight gradients are wanted."""
+    heads = (1, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 16, 32)
+    none = (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
+    n = lib().dit_rope_workspace_bytes(_ROPE_ARGS.pack(1, 1, head_dim, DTYPE_F32, 0, 1, 0, 0, 0, 0, 1e4, 0.0, 0, 0, 0,
+                                                       POS_I32, 0, *heads, *none))
+    if n < 0:
+        raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
+    return n
+
+
+def _pixel_view(name, t, like):
+    """(pointer, batch stride, pixel stride) of a [batch, ..., channels] view."""
+    if t.shape != like.shape:
+        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(like.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} has another dtype or device")
+    shape, stride = t.shape, t.stride()
+    if t.numel() == 0:
+        return 0, 0, 0
+    if stride[-1] != 1 and shape[-1] > 1:
+        _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous (channels last)")
+    step, span = 0, 0
+    for i in range(t.dim() - 2, 0, -1):  # the middle axes as one axis of pixels
+        if shape[i] == 1:
+            continue
+        if not step:
+            step = stride[i]
+        elif stride[i] != span:
+            _refuse(DIT_ERR_SHAPE, f"{name}: the axes between batch and channels must have one common stride")
+        span = stride[i] * shape[i]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else 0, step
+
+
+def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, act):
+    if x.dim() < 3:
+        _refuse(DIT_ERR_SHAPE, "x must be [batch, ..., channels]")
+    B, C = x.shape[0], x.shape[-1]
+    P = 1
+    for v in x.shape[1:-1]:
+        P *= v
+    dev = x.device
+    return _GN_ARGS.pack(B, P, C, groups, _dtype_code(x), act, eps, 0, *_pixel_view("x", x, x),
+                         *((0, 0, 0) if dy is None else _pixel_view("dy", dy, x)), *_pixel_view("out", out, x),
+                         _param("weight", weight, (C,), dev), _param("bias", bias, (C,), dev),
+                         _param("mean", mean, (B, groups), dev), _param("rstd", rstd, (B, groups), dev),
+                         _param("dweight", dweight, (C,), dev), _param("dbias", dbias, (C,), dev))
+
+
+def dit_group_norm_forward(x, y, groups: int, *, weight=None, bias=None, mean=None, rstd=None, eps=1e-6, act=ACT_NONE,
+                           workspace=None, stream=None):
+    """Group norm of x [batch, ..., channels] (channels last) with an
+    activation, into y (which may be x).  mean / rstd: float32 [batch, groups]
+    written for the backward call, or None.  workspace: a contiguous tensor of
+    dit_group_norm_workspace_bytes, or None to take one from torch's allocator
+    (only on torch's current stream)."""
+    args = _gn_args(x, None, y, groups, weight, bias, mean, rstd, None, None, eps, act)
+    L = lib()
+    ws, n, s = _launch_on(x.device, workspace, stream, lambda a: L.dit_group_norm_workspace_bytes(a, 0), args)
+    _check(L.dit_group_norm_forward(args, ws, n, s))
+
+
+def dit_group_norm_backward(x, dy, mean, rstd, dx, groups: int, *, weight=None, bias=None, dweight=None, dbias=None,
+                            act=ACT_NONE, workspace=None, stream=None):
+    """Gradient of dit_group_norm_forward: dx (which may be dy or x), and
+    dweight / dbias (float32 [channels], overwritten) where given.  mean and
+    rstd are what the forward call wrote."""
+    args = _gn_args(x, dy, dx, groups, weight, bias, mean, rstd, dweight, dbias, 0.0, act)
+    L = lib()
+    ws, n, s = _launch_on(x.device, workspace, stream, lambda a: L.dit_group_norm_workspace_bytes(a, 1), args)
+    _check(L.dit_group_norm_backward(args, ws, n, s))
+
+
+def dit_group_norm_workspace_bytes(x, groups: int, backward: bool) -> int:
+    """Workspace of a group-norm call on tensors like x (the same strides and
+    alignment in every argument)."""
+    view = _pixel_view("x", x, x)
+    P = 1
+    for v in x.shape[1:-1]:
+        P *= v
+    n = lib().dit_group_norm_workspace_bytes(
+        _GN_ARGS.pack(x.shape[0], P, x.shape[-1], groups, _dtype_code(x), ACT_NONE, 0.0, 0, *view, *view, *view,
+                      0, 0, 0, 0, 0, 0), 1 if backward else 0)
+    if n < 0:
+        raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
+    return n
 
 
 def dit_debug_fail_alloc_after(n: int):

@@ -35,9 +35,10 @@
  *     Calls of one model on two unordered streams race on the workspace.
  *     Separate models share nothing and may run concurrently.
  *   - Floating-point tensors crossing the ABI are float32, row-major, densely
- *     packed, in the layouts given per call.  B is the batch of network
- *     passes; in the loop B = 2 x requests with CFG (conditional passes
- *     first, then unconditional ones).
+ *     packed, in the layouts given per call (dit_rope_* and dit_group_norm_*
+ *     take strided views of float32, bfloat16 or float16 activations).  B is
+ *     the batch of network passes; in the loop B = 2 x requests with CFG
+ *     (conditional passes first, then unconditional ones).
  */
 #ifndef DIT_H
 #define DIT_H
@@ -61,7 +62,9 @@ typedef enum {
 
 enum { DIT_PREC_BF16 = 0, DIT_PREC_F32 = 1, DIT_PREC_FP8 = 2 };
 enum { DIT_COND_CROSS = 0, DIT_COND_JOINT = 1 };
-enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1 };
+/* DIT_DTYPE_F16 is a type of the rotation and group-norm operators only:
+ * dit_load_weights takes the other two. */
+enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1, DIT_DTYPE_F16 = 2 };
 /* dit_denoise_loop flags */
 enum {
   DIT_LOOP_PARTIAL_SCHEDULE = 1, /* allow sigmas[0] != 1 or sigmas[n] != 0                     */
@@ -227,6 +230,123 @@ dit_status cfg_combine(const float* vc, const float* vu, float g, float* v, int6
  * sigma: DIT_ERR_INVALID_ARG. */
 dit_status flow_euler_step(float* x, const float* v, float sigma, float sigma_next, int64_t n,
                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators beside the model: what a block around the denoiser's own needs on
+ * its token grids and latents, forward and gradient.  They hold no state and
+ * allocate nothing; scratch is the caller's `workspace` (device memory,
+ * 16-byte aligned, its size from the ..._workspace_bytes call, contents
+ * meaningless before and after).  Calls that share a workspace must be
+ * ordered on the GPU, captured graphs among them.  Every pointer is a device
+ * pointer of one device; the launch goes to that device whichever is current,
+ * and `stream` must belong to it.  Results are the same bits from run to run.
+ * An output may be the very view of an input (same pointer, same strides) and
+ * otherwise overlaps none.  A size of zero is a valid call.
+ */
+
+/* Rotary position embedding of q and k over 1 to 4 position axes (time,
+ * height, width, ...), with an optional RMS norm of every head in front of it.
+ * The rotary shape and style are named among the failure points of
+ * SGLang-Diffusion "Support New Diffusion Models", "Verify the Port".
+ *
+ * R = axes[0] + ... channels of each head are turned as R / 2 pairs; axis a
+ * owns axes[a] / 2 consecutive pairs, and its j-th pair of a token at
+ * position pos[a] turns by pos[a] * theta^(-2 j / axes[a]).  Pair p is
+ * channels (2p, 2p + 1) with DIT_ROPE_INTERLEAVED, (p, p + R / 2) with
+ * DIT_ROPE_SPLIT; (a, b) -> (a cos - b sin, a sin + b cos).  Channels from R
+ * on are not turned.  Angles are reduced exactly (64-bit fixed-point turns),
+ * so far positions lose nothing.  With a weight w[head_dim] the head x is
+ * first x * w / sqrt(mean(x^2) + eps), the mean over the whole head.
+ * Arithmetic is fp32, rounded once to the activation type.  */
+enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_SPLIT = 1 };
+enum { DIT_ROPE_MAX_AXES = 4, DIT_ROPE_MAX_HEAD_DIM = 256 };
+enum { DIT_POS_I32 = 0, DIT_POS_F32 = 1 };
+
+/* One of the two tensors turned, as views [batch, tokens, heads, head_dim]
+ * whose last axis is contiguous; strides in elements, of the batch, token and
+ * head axes.  Inputs may have strides of 0 (expanded views). */
+typedef struct {
+  int32_t heads;         /* 0: tensor absent                                            */
+  int32_t reserved;      /* 0                                                           */
+  const void* x;         /* forward input (backward: needed with a weight, else unread) */
+  int64_t x_stride[3];
+  const void* dy;        /* backward: gradient of the forward output                    */
+  int64_t dy_stride[3];
+  void* out;             /* forward: output; backward: gradient of x                    */
+  int64_t out_stride[3];
+  const float* weight;   /* device float[head_dim] of the head norm, or NULL: no norm   */
+  float* dweight;        /* backward: device float[head_dim], or NULL: not wanted       */
+} dit_rope_heads;
+
+typedef struct {
+  int64_t batch;
+  int64_t tokens;
+  int32_t head_dim;      /* even, at most DIT_ROPE_MAX_HEAD_DIM                          */
+  int32_t dtype;         /* DIT_DTYPE_* of x, dy and out                                */
+  int32_t style;         /* DIT_ROPE_*                                                  */
+  int32_t n_axes;        /* 1 .. DIT_ROPE_MAX_AXES                                      */
+  int32_t axes[4];       /* channels per axis: even, >= 0, at most head_dim in all      */
+  float theta;           /* >= 1                                                        */
+  float eps;             /* >= 0                                                        */
+  const void* pos;       /* device [batch, tokens, n_axes], last axis contiguous        */
+  int64_t pos_stride[2]; /* batch (0: shared by the batch) and token strides, elements  */
+  int32_t pos_dtype;     /* DIT_POS_I32, or DIT_POS_F32 (exact for any finite value)    */
+  int32_t reserved;      /* 0                                                           */
+  dit_rope_heads q, k;   /* their head counts are independent                           */
+} dit_rope_args;
+
+dit_status dit_rope_forward(const dit_rope_args* a, void* stream);
+/* out = the gradient of x; dweight = the gradient of the weight, summed over
+ * batch, tokens and heads in fp32 (overwritten; all zero for no tokens).
+ * Needs workspace when a dweight is wanted. */
+dit_status dit_rope_backward(const dit_rope_args* a, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes dit_rope_backward needs (host-only query; pointers are read as
+ * present or NULL only); -1 for arguments the call would refuse. */
+int64_t dit_rope_workspace_bytes(const dit_rope_args* a);
+
+/* Group norm of channels-last activations with an activation behind it: the
+ * normalisation of the latent encoders and decoders on either side of the
+ * denoiser (SGLang-Diffusion "Disaggregated Diffusion Pipeline", Quick Start,
+ * role table: encoder, decoder).  x is a view [batch, pixels, channels] whose
+ * last axis is contiguous (pixels = H W or T H W); strides in elements, of
+ * the batch and pixel axes.  Each batch element's `groups` groups of
+ * channels / groups consecutive channels are normalised over all pixels with
+ * their mean and population variance, then y = act(xhat * weight + bias) per
+ * channel.  Statistics and arithmetic are fp32, rounded once to the type.  */
+enum { DIT_ACT_NONE = 0, DIT_ACT_SILU = 1 };
+typedef struct {
+  int64_t batch;
+  int64_t pixels;
+  int32_t channels;
+  int32_t groups;       /* divides channels                                               */
+  int32_t dtype;        /* DIT_DTYPE_* of x, dy and out                                  */
+  int32_t act;          /* DIT_ACT_*                                                     */
+  float eps;            /* >= 0; forward only                                            */
+  int32_t reserved;     /* 0                                                             */
+  const void* x;
+  int64_t x_stride[2];
+  const void* dy;       /* backward: gradient of the forward output                      */
+  int64_t dy_stride[2];
+  void* out;            /* forward: y; backward: gradient of x                           */
+  int64_t out_stride[2];
+  const float* weight;  /* device float[channels], or NULL: 1                            */
+  const float* bias;    /* device float[channels], or NULL: 0                            */
+  float* mean;          /* device float[batch, groups]: forward writes them (NULL: not   */
+  float* rstd;          /*   wanted); backward reads what the forward wrote              */
+  float* dweight;       /* backward: device float[channels], or NULL: not wanted         */
+  float* dbias;         /* backward: device float[channels], or NULL: not wanted         */
+} dit_group_norm_args;
+
+/* With no pixels, mean is 0 and rstd 1 / sqrt(eps). */
+dit_status dit_group_norm_forward(const dit_group_norm_args* a, void* workspace, int64_t workspace_bytes,
+                                  void* stream);
+/* dweight and dbias are sums over batch and pixels in fp32 (overwritten). */
+dit_status dit_group_norm_backward(const dit_group_norm_args* a, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+/* Bytes of workspace of the forward (backward == 0) or the backward call
+ * (host-only query, from the sizes, type, strides and alignment); -1 for
+ * arguments the call would refuse. */
+int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backward);
 
 /* The whole denoiser stage for `batch` requests: the denoiser role of
  * SGLang-Diffusion "Disaggregated Diffusion Pipeline" (Quick Start, role

@@ -1,0 +1,161 @@
+"""Refusals of the rotation and group-norm operators that need no GPU: the
+library's checks come before any launch (pointers here are never read), and
+the binding's before the library."""
+import pytest
+import torch
+
+from diffusion_transformer_denoising_gb300 import dit
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(dit.LIB_PATH):
+        from diffusion_transformer_denoising_gb300 import build
+        build.build()
+    return dit.lib()
+
+
+HEADS = dict(heads=2, reserved=0, x=4096, xs=(512, 64, 32), dy=0, ds=(0, 0, 0), out=8192, os=(512, 64, 32), weight=0,
+             dweight=0)
+NONE = dict(HEADS, heads=0, x=0, out=0)
+
+
+def rope_args(q=HEADS, k=NONE, **kw):
+    a = dict(batch=2, tokens=8, head_dim=32, dtype=dit.DTYPE_F32, style=0, n_axes=2, axes=(16, 16, 0, 0), theta=1e4,
+             eps=1e-6, pos=1024, ps=(0, 2), pos_dtype=0, reserved=0)
+    a.update(kw)
+    heads = [v for h in (q, k) for v in (h["heads"], h["reserved"], h["x"], *h["xs"], h["dy"], *h["ds"], h["out"],
+                                         *h["os"], h["weight"], h["dweight"])]
+    return dit._ROPE_ARGS.pack(a["batch"], a["tokens"], a["head_dim"], a["dtype"], a["style"], a["n_axes"], *a["axes"],
+                               a["theta"], a["eps"], a["pos"], *a["ps"], a["pos_dtype"], a["reserved"], *heads)
+
+
+INVALID, SHAPE = dit.DIT_ERR_INVALID_ARG, dit.DIT_ERR_SHAPE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), SHAPE), (dict(tokens=-1), SHAPE), (dict(batch=1 << 20, tokens=1 << 20), SHAPE),
+    (dict(head_dim=0), SHAPE), (dict(head_dim=31), SHAPE), (dict(head_dim=258), SHAPE),
+    (dict(dtype=3), INVALID), (dict(style=2), INVALID), (dict(pos_dtype=2), INVALID),
+    (dict(n_axes=0), INVALID), (dict(n_axes=5), INVALID), (dict(axes=(15, 16, 0, 0)), INVALID),
+    (dict(axes=(-2, 16, 0, 0)), INVALID), (dict(axes=(18, 16, 0, 0)), INVALID),
+    (dict(theta=0.5), INVALID), (dict(theta=float("nan")), INVALID), (dict(theta=float("inf")), INVALID),
+    (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(reserved=1), INVALID),
+    (dict(pos=0), INVALID), (dict(pos=1026), INVALID), (dict(ps=(-16, 2)), SHAPE), (dict(ps=(0, 1 << 60)), SHAPE),
+    (dict(q=NONE), SHAPE), (dict(q=dict(HEADS, heads=-1)), SHAPE), (dict(q=dict(HEADS, heads=1 << 17)), SHAPE),
+    (dict(q=dict(HEADS, x=0)), INVALID), (dict(q=dict(HEADS, out=0)), INVALID), (dict(q=dict(HEADS, x=4097)), INVALID),
+    (dict(q=dict(HEADS, xs=(-1, 64, 32))), SHAPE), (dict(q=dict(HEADS, xs=(1 << 58, 64, 32))), SHAPE),
+    (dict(q=dict(HEADS, os=(512, 64, 31))), SHAPE),     # heads of the output overlap
+    (dict(q=dict(HEADS, os=(0, 64, 32))), SHAPE),       # an expanded output
+    (dict(q=dict(HEADS, os=(512, 32, 32))), SHAPE),
+    (dict(q=dict(HEADS, out=4096, os=(1024, 64, 32))), INVALID),   # in place with other strides
+    (dict(q=dict(HEADS, dweight=64)), INVALID), (dict(q=dict(HEADS, weight=66)), INVALID),
+    (dict(k=dict(NONE, weight=64)), INVALID), (dict(k=dict(HEADS, reserved=1)), INVALID),
+    (dict(k=HEADS), INVALID),                            # q and k with one output
+])
+def test_rope_forward_refuses(L, kw, status):
+    with pytest.raises(dit.DitError) as e:
+        dit._check(L.dit_rope_forward(rope_args(**kw), None))
+    assert e.value.status == status, e.value
+
+
+def test_rope_backward_refuses(L):
+    g = dict(HEADS, dy=2048, ds=(512, 64, 32))
+    for q, ws, n in ((dict(g, dy=0), 0, 0),                                     # no gradient
+                     (dict(g, x=0, weight=64), 0, 0),                           # the norm's gradient needs x
+                     (dict(g, weight=0, dweight=64), 0, 0),                     # a gradient of no weight
+                     (dict(g, weight=64, dweight=128), 0, 0),                   # no workspace
+                     (dict(g, weight=64, dweight=128), 1024, 16),               # too little
+                     (dict(g, weight=64, dweight=128), 1032, 1 << 30)):         # not aligned
+        with pytest.raises(dit.DitError) as e:
+            dit._check(L.dit_rope_backward(rope_args(q=q), ws, n, None))
+        assert e.value.status == INVALID, e.value
+    two = dict(g, weight=64, dweight=128)
+    with pytest.raises(dit.DitError):
+        dit._check(L.dit_rope_backward(rope_args(q=two, k=dict(two, out=16384)), 1024, 1 << 30, None))
+    assert L.dit_rope_workspace_bytes(rope_args(q=dict(two, heads=-3))) == -1
+
+
+def gn_args(**kw):
+    a = dict(batch=2, pixels=9, channels=12, groups=3, dtype=dit.DTYPE_F32, act=0, eps=1e-6, reserved=0, x=4096,
+             xs=(108, 12), dy=0, ds=(0, 0), out=16384, os=(108, 12), weight=0, bias=0, mean=0, rstd=0, dweight=0,
+             dbias=0)
+    a.update(kw)
+    return dit._GN_ARGS.pack(a["batch"], a["pixels"], a["channels"], a["groups"], a["dtype"], a["act"], a["eps"],
+                             a["reserved"], a["x"], *a["xs"], a["dy"], *a["ds"], a["out"], *a["os"], a["weight"],
+                             a["bias"], a["mean"], a["rstd"], a["dweight"], a["dbias"])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), SHAPE), (dict(pixels=-1), SHAPE), (dict(pixels=1 << 31), SHAPE), (dict(batch=1 << 21), SHAPE),
+    (dict(channels=0), SHAPE), (dict(channels=1 << 21, groups=1), SHAPE), (dict(groups=0), SHAPE), (dict(groups=5), SHAPE),
+    (dict(dtype=5), INVALID), (dict(act=2), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(reserved=1), INVALID), (dict(x=0), INVALID), (dict(out=0), INVALID), (dict(x=4098), INVALID),
+    (dict(xs=(-1, 12)), SHAPE), (dict(os=(0, 12)), SHAPE), (dict(os=(108, 11)), SHAPE), (dict(os=(12, 12)), SHAPE),
+    (dict(out=4096, os=(216, 24)), INVALID), (dict(dweight=64, weight=128), INVALID), (dict(dbias=64, bias=128), INVALID),
+    (dict(mean=64, rstd=64), INVALID), (dict(weight=66), INVALID),
+])
+def test_group_norm_forward_refuses(L, kw, status):
+    with pytest.raises(dit.DitError) as e:
+        dit._check(L.dit_group_norm_forward(gn_args(**kw), 1024, 1 << 30, None))
+    assert e.value.status == status, e.value
+
+
+def test_group_norm_refuses_bad_workspace_and_missing_statistics(L):
+    big = dict(pixels=1 << 20, xs=(12 << 20, 12), os=(12 << 20, 12))
+    need = L.dit_group_norm_workspace_bytes(gn_args(**big), 0)
+    assert need > 0
+    for ws, n in ((0, 1 << 40), (1024, need - 1), (1032, need)):
+        with pytest.raises(dit.DitError) as e:
+            dit._check(L.dit_group_norm_forward(gn_args(**big), ws, n, None))
+        assert e.value.status == INVALID
+    back = dict(dy=2048, ds=(108, 12))
+    for kw in (dict(mean=64), dict(rstd=64), dict(mean=64, rstd=128, dy=0), dict(mean=64, rstd=128, dweight=256),
+               dict(mean=64, rstd=128, weight=192, bias=224, dweight=256, dbias=256)):
+        with pytest.raises(dit.DitError) as e:
+            dit._check(L.dit_group_norm_backward(gn_args(**{**back, **kw}), 1024, 1 << 30, None))
+        assert e.value.status == INVALID
+    assert L.dit_group_norm_workspace_bytes(gn_args(groups=5), 1) == -1
+
+
+def test_empty_calls_are_no_ops(L):
+    dit._check(L.dit_rope_forward(rope_args(tokens=0, pos=0, q=dict(HEADS, x=0, out=0)), None))
+    dit._check(L.dit_group_norm_forward(gn_args(batch=0, x=0, out=0), 0, 0, None))
+
+
+def test_binding_refuses():
+    z = torch.zeros
+    pos, q = z(8, 2, dtype=torch.int32), z(2, 8, 3, 32)
+    ok = dict(axes=(16, 16))
+    for status, pos_, q_, out, kw in (
+            (INVALID, pos, q, q, ok),                                       # host tensors
+            (SHAPE, pos, q[0], q[0], ok), (SHAPE, pos[:7], q, q, ok), (SHAPE, pos[:, :1], q, q, ok),
+            (INVALID, pos.long(), q, q, ok), (INVALID, pos, q, q.bfloat16(), ok), (SHAPE, pos, q, q[:, :, :2], ok),
+            (SHAPE, pos, q, z(2, 8, 3, 64)[..., ::2], ok), (INVALID, pos, q.double(), q.double(), ok),
+            (INVALID, pos, q, q, dict(axes=())), (INVALID, pos, q, q, dict(axes=(8,) * 5)),
+            (INVALID, pos, q, q, dict(ok, q_weight=z(32, dtype=torch.bfloat16))), (SHAPE, pos, q, q, dict(ok, q_weight=z(31))),
+            (INVALID, pos, q, q, dict(ok, k=q))):
+        with pytest.raises(dit.DitError) as e:
+            dit.dit_rope_forward(pos_, q_, out, **kw)
+        assert e.value.status == status, (e.value, pos_.shape, kw)
+    x = z(2, 4, 5, 12)
+    for status, x_, y, kw in ((INVALID, x, x, {}), (SHAPE, x[0, 0], x[0, 0], {}), (SHAPE, x, x[:, :3], {}),
+                              (SHAPE, z(2, 12, 4, 5).permute(0, 2, 3, 1), z(2, 12, 4, 5).permute(0, 2, 3, 1), {}),
+                              (SHAPE, x, z(2, 4, 7, 12)[:, :, :5], {}), (INVALID, x, x.half(), {}),
+                              (SHAPE, x, x, dict(weight=z(11))), (SHAPE, x, x, dict(mean=z(2, 4))),
+                              (INVALID, x, x, dict(bias=z(12, dtype=torch.int32)))):
+        with pytest.raises(dit.DitError) as e:
+            dit.dit_group_norm_forward(x_, y, 3, **kw)
+        assert e.value.status == status, (e.value, x_.shape, kw)
+
+
+def test_workspace_sizes():
+    assert dit.dit_rope_workspace_bytes(128) >= 128 * 4
+    with pytest.raises(dit.DitError):
+        dit.dit_rope_workspace_bytes(257)
+    x = torch.zeros(2, 8, 8, 64)
+    for backward in (False, True):
+        assert dit.dit_group_norm_workspace_bytes(x, 32, backward) >= 0
+    with pytest.raises(dit.DitError):
+        dit.dit_group_norm_workspace_bytes(x, 48, False)
