@@ -137,10 +137,10 @@ struct SplitV {
 
 // Any style, width, stride and alignment: a warp a row, pairs lane + 32 i,
 // element accesses.
-template <typename T>
+template <typename T, int N>
 struct AnyPairs {
   using Elem = T;
-  static constexpr int NP = 4;
+  static constexpr int NP = N;
   struct RowRaw {
     T a[NP], b[NP];
   };
@@ -186,8 +186,8 @@ struct RopeSeg {
   void* out;
   int64_t xs[3], ds[3], os[3];
   const float* w;
-  float* part;  // ROPE_NORM_GRAD: [blocks of this segment][head_dim] partial dweight, or NULL
-  int heads, slice, nslice;
+  float* part;  // ROPE_NORM_GRAD: [blocks][head_dim] partial dweight, or NULL
+  int heads;
 };
 
 struct RopeParams {
@@ -201,45 +201,42 @@ struct RopeParams {
   uint64_t turn[DIT_ROPE_MAX_HEAD_DIM / 2];
 };
 
-// blockIdx.y: head slice (q's, then k's); blockIdx.x strides over tokens.  A
-// group of 2^group_log2 lanes takes one token at a time and walks the heads of
-// the slice HU at a time.
+// blockIdx.y of gridDim.y: a slice of q's heads and of k's; blockIdx.x strides
+// over tokens.  A group of 2^group_log2 lanes takes one token at a time: its
+// angles once, then the slice's heads HU at a time.  A row's turn is
+// ya = a k0 + b k1, yb = a k2 + b k3 with (k0, k1, k2, k3) = (c, -s, s, c), or
+// with the norm's weights in them, on column pairs (fma.rn.f32x2).
 template <class L, int MODE, int HU>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) rope_kernel(const __grid_constant__ RopeParams P) {
   using T = typename L::Elem;
-  constexpr int NP = L::NP;
-  const int which = blockIdx.y >= (unsigned)P.seg[0].nslice;
-  const RopeSeg& S = P.seg[which];
-  const int h0 = (blockIdx.y - (which ? P.seg[0].nslice : 0)) * S.slice;
-  const int h1 = min(h0 + S.slice, S.heads);
+  constexpr int NP = L::NP, N2 = NP / 2;
   const int lanes = 1 << P.group_log2;
   const int lane = threadIdx.x & (lanes - 1);
   const int groups = kRopeThreads >> P.group_log2;
   const int group = threadIdx.x >> P.group_log2;
+  const bool partial = 2 * P.half < P.d;
 
   L lay;
   lay.init(lane, P.d, P.half, P.split);
-  uint64_t turn[NP];
-  int axis[NP];
-  bool turned[NP];
-  float wa[NP], wb[NP], da[NP], db[NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int p = lay.pair(i);
-    turned[i] = lay.has(i) && p < P.half;
-    turn[i] = turned[i] ? P.turn[p] : 0;
-    axis[i] = 0;
-    for (int a = 0; a + 1 < P.n_axes; ++a) axis[i] += p >= P.ends[a];
-    if constexpr (MODE != ROPE_TURN) {
-      wa[i] = lay.has(i) ? S.w[lay.chan_a(i)] : 0.f;
-      wb[i] = lay.has_b(i) ? S.w[lay.chan_b(i)] : 0.f;
-    }
-    da[i] = db[i] = 0.f;
+  // every pair's frequency and axis
+  __shared__ uint64_t turn[DIT_ROPE_MAX_HEAD_DIM / 2];
+  __shared__ int axis[DIT_ROPE_MAX_HEAD_DIM / 2];
+  if (threadIdx.x < P.half) {
+    turn[threadIdx.x] = P.turn[threadIdx.x];
+    int on = 0;
+    for (int a = 0; a + 1 < P.n_axes; ++a) on += (int)threadIdx.x >= P.ends[a];
+    axis[threadIdx.x] = on;
   }
+  __syncthreads();
+  bool turned[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) turned[i] = lay.has(i) && lay.pair(i) < P.half;
+  float2 da[2][N2], db[2][N2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int i = 0; i < N2; ++i) da[g][i] = db[g][i] = make_float2(0.f, 0.f);
 
-  const T* x = static_cast<const T*>(S.x);
-  const T* dy = static_cast<const T*>(S.dy);
-  T* out = static_cast<T*>(S.out);
   const uint32_t step = gridDim.x * groups;
   // the loop runs while any group of the block has a row: lanes of a warp stay
   // together for the shuffles
@@ -248,99 +245,151 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const bool ok = row < P.rows;
     const uint32_t b = ok ? row / P.tokens : 0, t = ok ? row - b * P.tokens : 0;
     float c[NP], s[NP];
-    const int64_t po = b * P.ps[0] + t * P.ps[1];
-    const int64_t xo = b * S.xs[0] + t * S.xs[1], oo = b * S.os[0] + t * S.os[1], go = b * S.ds[0] + t * S.ds[1];
-    for (int h = h0; h < h1; h += HU) {
-      typename L::RowRaw rx[HU], rg[MODE == ROPE_NORM_GRAD ? HU : 1];
 #pragma unroll
-      for (int u = 0; u < HU; ++u) {
-        lay.load(rx[u], x + xo + (h + u) * S.xs[2], ok && h + u < h1);
-        if constexpr (MODE == ROPE_NORM_GRAD) lay.load(rg[u], dy + go + (h + u) * S.ds[2], ok && h + u < h1);
-      }
-      if (h == h0) {
+    for (int i = 0; i < NP; ++i) c[i] = 1.f, s[i] = 0.f;
+    if (ok) {
+      const int64_t po = b * P.ps[0] + t * P.ps[1];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          c[i] = 1.f, s[i] = 0.f;
-          if (!turned[i] || !ok) continue;
-          if (P.pos_f32) {
-            const float pos = static_cast<const float*>(P.pos)[po + axis[i]];
-            turns_sincos(turns_of(pos, turn[i]), c[i], s[i]);
-            if (!finite_bits(pos)) c[i] = s[i] = __int_as_float(0x7FFFFFFF);
-          } else {
-            const int32_t pos = static_cast<const int32_t*>(P.pos)[po + axis[i]];
-            turns_sincos((uint64_t)(int64_t)pos * turn[i], c[i], s[i]);
-          }
-          if (P.negate) s[i] = -s[i];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < HU; ++u) {
-        float a[NP], e[NP];
-        lay.values(rx[u], a, e);
-        if constexpr (MODE == ROPE_NORM) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < NP; ++i) ss = fmaf(a[i], a[i], fmaf(e[i], e[i], ss));
-          for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-          const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
-#pragma unroll
-          for (int i = 0; i < NP; ++i) a[i] *= r * wa[i], e[i] *= r * wb[i];
-        }
-        if constexpr (MODE != ROPE_NORM_GRAD) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const float ya = fmaf(a[i], c[i], -e[i] * s[i]), yb = fmaf(a[i], s[i], e[i] * c[i]);
-            a[i] = turned[i] ? ya : a[i];
-            e[i] = turned[i] ? yb : e[i];
-          }
+      for (int i = 0; i < NP; ++i) {
+        if (!turned[i]) continue;
+        const int p = lay.pair(i);
+        if (P.pos_f32) {
+          const float pos = static_cast<const float*>(P.pos)[po + axis[p]];
+          turns_sincos(turns_of(pos, turn[p]), c[i], s[i]);
+          if (!finite_bits(pos)) c[i] = s[i] = __int_as_float(0x7FFFFFFF);
         } else {
-          float ga[NP], gb[NP], ss = 0.f, dot = 0.f;
-          lay.values(rg[u], ga, gb);
+          const int32_t pos = static_cast<const int32_t*>(P.pos)[po + axis[p]];
+          turns_sincos((uint64_t)(int64_t)pos * turn[p], c[i], s[i]);
+        }
+        if (P.negate) s[i] = -s[i];
+      }
+    }
+#pragma unroll(MODE == ROPE_NORM_GRAD ? 2 : 1)  // the gradient's sums are registers of their own for q and k
+    for (int g = 0; g < 2; ++g) {
+      const RopeSeg& S = P.seg[g];
+      const int h0 = S.heads * blockIdx.y / gridDim.y, h1 = S.heads * (blockIdx.y + 1) / gridDim.y;
+      if (h0 >= h1) continue;
+      float2 k0[N2], k1[N2], k2[N2], k3[N2], wa[N2], wb[N2];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const float ya = fmaf(ga[i], c[i], gb[i] * s[i]), yb = fmaf(gb[i], c[i], -ga[i] * s[i]);
-            ga[i] = turned[i] ? ya : ga[i];
-            gb[i] = turned[i] ? yb : gb[i];
-            ss = fmaf(a[i], a[i], fmaf(e[i], e[i], ss));
-            dot = fmaf(ga[i] * wa[i], a[i], fmaf(gb[i] * wb[i], e[i], dot));
-          }
-          for (int o = lanes >> 1; o; o >>= 1) {
-            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-          }
-          const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
-          const float m = dot * r * P.inv_d;
+      for (int i = 0; i < NP; ++i) {
+        float va = 1.f, vb = 1.f;
+        if constexpr (MODE != ROPE_TURN) {
+          va = lay.has(i) ? S.w[lay.chan_a(i)] : 0.f;
+          vb = lay.has_b(i) ? S.w[lay.chan_b(i)] : 0.f;
+        }
+        const float m0 = MODE == ROPE_NORM ? c[i] * va : c[i], m1 = MODE == ROPE_NORM ? -s[i] * vb : -s[i];
+        const float m2 = MODE == ROPE_NORM ? s[i] * va : s[i], m3 = MODE == ROPE_NORM ? c[i] * vb : c[i];
+        if (i & 1) k0[i / 2].y = m0, k1[i / 2].y = m1, k2[i / 2].y = m2, k3[i / 2].y = m3, wa[i / 2].y = va, wb[i / 2].y = vb;
+        else k0[i / 2].x = m0, k1[i / 2].x = m1, k2[i / 2].x = m2, k3[i / 2].x = m3, wa[i / 2].x = va, wb[i / 2].x = vb;
+      }
+      const T* x = static_cast<const T*>(S.x) + b * S.xs[0] + t * S.xs[1] + h0 * S.xs[2];
+      const T* dy = MODE == ROPE_NORM_GRAD ? static_cast<const T*>(S.dy) + b * S.ds[0] + t * S.ds[1] + h0 * S.ds[2] : nullptr;
+      T* out = static_cast<T*>(S.out) + b * S.os[0] + t * S.os[1] + h0 * S.os[2];
+      for (int h = h0; h < h1; h += HU) {
+        typename L::RowRaw rx[HU], rg[MODE == ROPE_NORM_GRAD ? HU : 1];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const float xa = a[i] * r, xb = e[i] * r;
-            if (ok && h + u < h1) {
-              da[i] = fmaf(ga[i], xa, da[i]);
-              db[i] = fmaf(gb[i], xb, db[i]);
+        for (int u = 0; u < HU; ++u) {
+          lay.load(rx[u], x + u * S.xs[2], ok && h + u < h1);
+          if constexpr (MODE == ROPE_NORM_GRAD) lay.load(rg[u], dy + u * S.ds[2], ok && h + u < h1);
+        }
+#pragma unroll
+        for (int u = 0; u < HU; ++u) {
+          const bool on = ok && h + u < h1;
+          float af[NP], bf[NP];
+          float2 a[N2], e[N2], ya[N2], yb[N2];
+          lay.values(rx[u], af, bf);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) a[i] = make_float2(af[2 * i], af[2 * i + 1]), e[i] = make_float2(bf[2 * i], bf[2 * i + 1]);
+          if constexpr (MODE != ROPE_NORM_GRAD) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              ya[i] = ffma2(a[i], k0[i], fmul2(e[i], k1[i]));
+              yb[i] = ffma2(a[i], k2[i], fmul2(e[i], k3[i]));
             }
-            a[i] = r * fmaf(-xa, m, ga[i] * wa[i]);
-            e[i] = r * fmaf(-xb, m, gb[i] * wb[i]);
+            if (partial) {  // channels that are not turned do not meet their neighbours (0 * inf)
+#pragma unroll
+              for (int i = 0; i < N2; ++i) {
+                if (!turned[2 * i]) ya[i].x = a[i].x * k0[i].x, yb[i].x = e[i].x * k3[i].x;
+                if (!turned[2 * i + 1]) ya[i].y = a[i].y * k0[i].y, yb[i].y = e[i].y * k3[i].y;
+              }
+            }
+            if constexpr (MODE == ROPE_NORM) {
+              float2 q = fmul2(a[0], a[0]);
+              q = ffma2(e[0], e[0], q);
+#pragma unroll
+              for (int i = 1; i < N2; ++i) q = ffma2(e[i], e[i], ffma2(a[i], a[i], q));
+              float ss = q.x + q.y;
+              for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+              const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
+              const float2 r2 = make_float2(r, r);
+#pragma unroll
+              for (int i = 0; i < N2; ++i) ya[i] = fmul2(ya[i], r2), yb[i] = fmul2(yb[i], r2);
+            }
+          } else {
+            float gaf[NP], gbf[NP];
+            float2 ga[N2], gb[N2], q = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f);
+            lay.values(rg[u], gaf, gbf);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              const float2 va = make_float2(gaf[2 * i], gaf[2 * i + 1]), vb = make_float2(gbf[2 * i], gbf[2 * i + 1]);
+              ga[i] = ffma2(va, k0[i], fmul2(vb, k2[i]));
+              gb[i] = ffma2(va, k1[i], fmul2(vb, k3[i]));
+              if (partial) {
+                if (!turned[2 * i]) ga[i].x = va.x, gb[i].x = vb.x;
+                if (!turned[2 * i + 1]) ga[i].y = va.y, gb[i].y = vb.y;
+              }
+              q = ffma2(e[i], e[i], ffma2(a[i], a[i], q));
+              dt = ffma2(fmul2(ga[i], wa[i]), a[i], dt);
+              dt = ffma2(fmul2(gb[i], wb[i]), e[i], dt);
+            }
+            float ss = q.x + q.y, dot = dt.x + dt.y;
+            for (int o = lanes >> 1; o; o >>= 1) {
+              ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+              dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+            }
+            const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
+            const float m = -dot * r * r * P.inv_d;  // dx = r (g w) + x r m
+            const float2 r2 = make_float2(r, r), m2 = make_float2(r * m, r * m);
+            const float2 on2 = on ? r2 : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              ya[i] = ffma2(a[i], m2, fmul2(fmul2(ga[i], wa[i]), r2));
+              yb[i] = ffma2(e[i], m2, fmul2(fmul2(gb[i], wb[i]), r2));
+              da[g][i] = ffma2(fmul2(ga[i], on2), a[i], da[g][i]);
+              db[g][i] = ffma2(fmul2(gb[i], on2), e[i], db[g][i]);
+            }
+          }
+          if (on) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) af[2 * i] = ya[i].x, af[2 * i + 1] = ya[i].y, bf[2 * i] = yb[i].x, bf[2 * i + 1] = yb[i].y;
+            lay.store(out + u * S.os[2], af, bf);
           }
         }
-        if (ok && h + u < h1) lay.store(out + oo + (h + u) * S.os[2], a, e);
+        x += HU * S.xs[2];
+        dy += HU * S.ds[2];
+        out += HU * S.os[2];
       }
     }
   }
 
   if constexpr (MODE == ROPE_NORM_GRAD) {
     // the block's dweight: groups in order, through shared memory
-    if (S.part) {
-      extern __shared__ float sm[];  // [groups][d]
+    extern __shared__ float sm[];  // [groups][d]
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (!P.seg[g].part) continue;
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = da[i];
-        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = db[i];
+        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[g][i / 2].y : da[g][i / 2].x;
+        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = i & 1 ? db[g][i / 2].y : db[g][i / 2].x;
       }
       __syncthreads();
-      const int64_t block = (int64_t)(blockIdx.y - (which ? P.seg[0].nslice : 0)) * gridDim.x + blockIdx.x;
+      const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
       for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
         float v = 0.f;
-        for (int g = 0; g < groups; ++g) v += sm[g * P.d + ch];
-        S.part[block * P.d + ch] = v;
+        for (int j = 0; j < groups; ++j) v += sm[j * P.d + ch];
+        P.seg[g].part[block * P.d + ch] = v;
       }
     }
   }
@@ -370,22 +419,26 @@ __global__ void __launch_bounds__(1024) rope_dweight_kernel(const float* p0, int
 }
 
 // ---------------------------------------------------------------- launch
-// How one segment's rows are read: 8-channel runs where the widths, strides
-// and pointers are multiples of what they need, else element by element.
-enum RopeLayout { LAYOUT_ANY = 0, LAYOUT_RUNS = 1 };
+// How one tensor's rows are read: in runs of 8 (interleaved pairs) or twice 4
+// channels (split pairs) a lane where the widths, strides and pointers are multiples of what those need,
+// else element by element.
+enum RopeLayout { LAYOUT_ANY = 0, LAYOUT_RUNS4 = 4, LAYOUT_RUNS8 = 8 };
 
-bool aligned16(const void* p, const int64_t st[3], int elem) {
+bool aligned(const void* p, const int64_t st[3], int elem, int to) {
   return !p || (((uintptr_t)p | (uintptr_t)(st[0] * elem) | (uintptr_t)(st[1] * elem) | (uintptr_t)(st[2] * elem)) &
-                15) == 0;
+                (to - 1)) == 0;
 }
 
 int elem_bytes(int dtype) { return dtype == DIT_DTYPE_F32 ? 4 : 2; }
 
 RopeLayout layout_of(const dit_rope_args& a, const dit_rope_heads& h, int half) {
   const int e = elem_bytes(a.dtype);
-  const bool ok = aligned16(h.x, h.x_stride, e) && aligned16(h.dy, h.dy_stride, e) && aligned16(h.out, h.out_stride, e);
-  if (!ok || a.head_dim % 8 || (a.style == DIT_ROPE_SPLIT && half % 8)) return LAYOUT_ANY;
-  return LAYOUT_RUNS;
+  auto ok = [&](int to) {
+    return aligned(h.x, h.x_stride, e, to) && aligned(h.dy, h.dy_stride, e, to) && aligned(h.out, h.out_stride, e, to);
+  };
+  if (a.style == DIT_ROPE_INTERLEAVED) return a.head_dim % 8 == 0 && ok(16) ? LAYOUT_RUNS8 : LAYOUT_ANY;
+  if (a.head_dim % 4 == 0 && half % 4 == 0 && ok(4 * e)) return LAYOUT_RUNS4;
+  return LAYOUT_ANY;
 }
 
 int log2_ceil(int v) {
@@ -401,18 +454,20 @@ cudaError_t launch(const RopeParams& P, dim3 grid, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class L>
+// HU rows in flight a group: 64 bytes of each lane (element accesses: 2 rows)
+template <class L, int HU>
 cudaError_t launch_mode(const RopeParams& P, int mode, dim3 grid, cudaStream_t s) {
-  if (mode == ROPE_TURN) return launch<L, ROPE_TURN, 4>(P, grid, s);
-  if (mode == ROPE_NORM) return launch<L, ROPE_NORM, 4>(P, grid, s);
-  return launch<L, ROPE_NORM_GRAD, 2>(P, grid, s);
+  if (mode == ROPE_TURN) return launch<L, ROPE_TURN, HU>(P, grid, s);
+  if (mode == ROPE_NORM) return launch<L, ROPE_NORM, HU>(P, grid, s);
+  return launch<L, ROPE_NORM_GRAD, HU / 2>(P, grid, s);
 }
 
 template <typename T>
 cudaError_t launch_layout(const RopeParams& P, int layout, int mode, dim3 grid, cudaStream_t s) {
-  if (layout == LAYOUT_ANY) return launch_mode<AnyPairs<T>>(P, mode, grid, s);
-  if (P.split) return launch_mode<SplitV<T, 8>>(P, mode, grid, s);
-  return launch_mode<Interleaved8<T>>(P, mode, grid, s);
+  if (layout == LAYOUT_RUNS4) return launch_mode<SplitV<T, 4>, 8 / sizeof(T)>(P, mode, grid, s);
+  if (layout == LAYOUT_RUNS8) return launch_mode<Interleaved8<T>, 8 / sizeof(T)>(P, mode, grid, s);
+  if (P.d <= 128) return launch_mode<AnyPairs<T, 2>, 2>(P, mode, grid, s);
+  return launch_mode<AnyPairs<T, 4>, 2>(P, mode, grid, s);
 }
 
 }  // namespace
@@ -451,24 +506,15 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       const int last = together ? 1 : first;
       RopeParams Q = P;
       Q.group_log2 = 5;
-      if (layout[first] == LAYOUT_RUNS)
-        Q.group_log2 = log2_ceil(P.split ? P.half / 8 + (P.d - 2 * P.half + 15) / 16 : P.d / 8);
+      const int v = layout[first];
+      if (v) Q.group_log2 = log2_ceil(P.split ? P.half / v + (P.d - 2 * P.half + 2 * v - 1) / (2 * v) : P.d / v);
       Q.negate = backward && mode[first] == ROPE_TURN;
-      const int heads = h[first]->heads + (together ? h[1]->heads : 0);
-      if (!heads) continue;
-      const int64_t row_blocks = ((int64_t)P.rows + (kRopeThreads >> Q.group_log2) - 1) >> (8 - Q.group_log2);
-      // heads a group takes one after the other: as many as leave blocks for
-      // every SM (they share the token's cos and sin), 12 at most
-      int slice = heads < 12 ? heads : 12;
-      while (slice > 1 && row_blocks * ((heads + slice - 1) / slice) < 608) slice = (slice + 1) / 2;
-      while ((heads + slice - 1) / slice > kRopeGradBlocks / 4) slice *= 2;
-      int ny = 0;
+      const int hmax = together && h[1]->heads > h[first]->heads ? h[1]->heads : h[first]->heads;
+      if (!hmax) continue;
       for (int i = first; i <= last; ++i) {
         RopeSeg& S = Q.seg[i - first];
         const dit_rope_heads& H = *h[i];
         S.heads = H.heads;
-        S.slice = slice;
-        S.nslice = (H.heads + slice - 1) / slice;
         S.w = H.weight;
         const bool turn_grad = Q.negate;
         S.x = turn_grad ? H.dy : H.x;
@@ -479,18 +525,20 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
           S.ds[k] = H.dy_stride[k];
           S.os[k] = H.out_stride[k];
         }
-        ny += S.nslice;
       }
-      int64_t nx = row_blocks;
-      if (mode[first] == ROPE_NORM_GRAD && nx > kRopeGradBlocks / 2 / ny) nx = kRopeGradBlocks / 2 / ny;
-      for (int i = first; i <= last; ++i) {
-        RopeSeg& S = Q.seg[i - first];
+      // one slice of all heads shares the token's cos and sin best; as many as
+      // it takes to give every SM four blocks otherwise
+      int64_t nx = ((int64_t)P.rows + (kRopeThreads >> Q.group_log2) - 1) >> (8 - Q.group_log2);
+      int64_t ny = (608 + nx - 1) / nx;
+      if (ny > hmax) ny = hmax;
+      if (ny > 256) ny = 256;
+      if (mode[first] == ROPE_NORM_GRAD && nx * ny > kRopeGradBlocks / 2) nx = kRopeGradBlocks / 2 / ny;
+      for (int i = first; i <= last; ++i)
         if (mode[i] == ROPE_NORM_GRAD && h[i]->dweight) {
-          blocks[i] = (int)nx * S.nslice;
+          blocks[i] = (int)(nx * ny);
           if (i == 1) part[1] = part[0] + (int64_t)blocks[0] * P.d;
-          S.part = part[i];
+          Q.seg[i - first].part = part[i];
         }
-      }
       const dim3 grid((unsigned)nx, (unsigned)ny);
       cudaError_t e;
       if (a.dtype == DIT_DTYPE_F32) e = launch_layout<float>(Q, layout[first], mode[first], grid, stream);

@@ -39,76 +39,75 @@ DIT_DEV uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// N elements of T as raw 16-byte words (N * sizeof(T) a multiple of 16), and
-// N = 1 as the element itself.
+// N elements of T as they lie in memory: 16-byte words, one word of 8 or 4
+// bytes, or a single element.  A pointer to them is aligned to the word.
 template <typename T, int N>
 struct Raw {
-  uint4 v[N * sizeof(T) / 16];
-};
-template <typename T>
-struct Raw<T, 1> {
-  T v;
+  static constexpr int kBytes = N * sizeof(T);
+  static constexpr int kWords = kBytes / 4 > 0 ? kBytes / 4 : 1;
+  uint32_t w[kWords];
 };
 
 template <typename T, int N>
 DIT_DEV Raw<T, N> load_raw(const T* p) {
   Raw<T, N> r;
-  if constexpr (N == 1) {
-    r.v = *p;
-  } else {
+  constexpr int B = Raw<T, N>::kBytes;
+  if constexpr (B >= 16) {
 #pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < B / 16; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (B == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else if constexpr (B == 4) {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
   }
   return r;
 }
 template <typename T, int N>
 DIT_DEV Raw<T, N> zero_raw() {
   Raw<T, N> r;
-  if constexpr (N == 1) {
-    r.v = from_f32<T>(0.f);
-  } else {
 #pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r.v[i] = make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < Raw<T, N>::kWords; ++i) r.w[i] = 0;
   return r;
 }
 template <typename T, int N>
 DIT_DEV void unpack(const Raw<T, N>& r, float (&f)[N]) {
-  if constexpr (N == 1) {
-    f[0] = to_f32(r.v);
-  } else {
 #pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) {
-      const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 4) {
-          f[4 * i + j] = __uint_as_float(w[j]);
-        } else {
-          const float2 t = unpack2<T>(w[j]);
-          f[8 * i + 2 * j] = t.x;
-          f[8 * i + 2 * j + 1] = t.y;
-        }
-      }
+  for (int i = 0; i < Raw<T, N>::kWords; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(r.w[i]);
+    } else {
+      const float2 t = unpack2<T>(r.w[i]);
+      f[2 * i] = t.x;
+      if constexpr (N > 1) f[2 * i + 1] = t.y;
     }
   }
 }
 template <typename T, int N>
 DIT_DEV void store_f32(T* p, const float (&f)[N]) {
+  constexpr int B = Raw<T, N>::kBytes;
   if constexpr (N == 1) {
     *p = from_f32<T>(f[0]);
   } else {
+    uint32_t w[Raw<T, N>::kWords];
 #pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) {
-      uint4 v;
-      if constexpr (sizeof(T) == 4) {
-        v = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                       __float_as_uint(f[4 * i + 3]));
-      } else {
-        v = make_uint4(pack2<T>(f[8 * i], f[8 * i + 1]), pack2<T>(f[8 * i + 2], f[8 * i + 3]),
-                       pack2<T>(f[8 * i + 4], f[8 * i + 5]), pack2<T>(f[8 * i + 6], f[8 * i + 7]));
-      }
-      reinterpret_cast<uint4*>(p)[i] = v;
+    for (int i = 0; i < Raw<T, N>::kWords; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+      else w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    }
+    if constexpr (B >= 16) {
+#pragma unroll
+      for (int i = 0; i < B / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (B == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
     }
   }
 }
