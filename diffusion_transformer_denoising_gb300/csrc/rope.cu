@@ -12,12 +12,21 @@
 // dx = r (h - xhat mean(h xhat)); the two row sums (x^2 and h x) are taken
 // together, so a row costs one round of shuffles either way.
 //
-// What bounds it: HBM.  Every row is read once and written once.  A group of
-// 4 to 32 lanes holds one row in registers (8 channels or more a lane, 128-bit
-// accesses), keeps its pairs' cos and sin for all the heads of a slice, and
-// has several rows' loads in flight.
+// What bounds it: HBM, once the latency is covered.  Every row is read once
+// and written once.  A group of 2 to 32 lanes holds one row in registers (8
+// channels a lane, 128-bit accesses), forms its pairs' cos and sin once for
+// all the token's heads, and always has the next batch of rows (64 bytes a
+// lane), of the next tensor or token too, and the next token's positions on
+// their way.  Measured on one GB300 (bf16, 128-wide heads, 44/42/42): q and k
+// of 2 x 32760 tokens x 12 heads 122 us = 6.60 TB/s (0.99 of the copy
+// bandwidth); 32760 tokens with the norm, out of a packed projection, 70.5 us
+// = 5.72 TB/s; its gradient 115 us = 5.27 TB/s (without the loads ahead 151 us;
+// with the positions not among them 146 us).
 #include <math.h>
 
+#include <type_traits>
+
+#include "launch.cuh"
 #include "operators.h"
 #include "vec.cuh"
 
@@ -201,18 +210,45 @@ struct RopeParams {
   uint64_t turn[DIT_ROPE_MAX_HEAD_DIM / 2];
 };
 
+// 4 bytes to shared memory in the background (zeros unless `some`), and the
+// wait for all of the thread's.
+DIT_DEV void cp_async4(void* dst, const void* src, bool some) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(some ? 4 : 0) : "memory");
+}
+DIT_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Two pairs turned; MIX: the first (tx) or second (ty) of them may be a pair
+// of channels that are not turned, which must not meet (0 * inf).
+template <bool MIX>
+DIT_DEV void turn_pair(float2 a, float2 b, float2 k0, float2 k1, float2 k2, float2 k3, bool tx, bool ty, float2& ya,
+                       float2& yb) {
+  ya = ffma2(a, k0, fmul2(b, k1));
+  yb = ffma2(a, k2, fmul2(b, k3));
+  if constexpr (MIX) {
+    const float2 pa = fmul2(a, k0), pb = fmul2(b, k3);
+    ya = make_float2(tx ? ya.x : pa.x, ty ? ya.y : pa.y);
+    yb = make_float2(tx ? yb.x : pb.x, ty ? yb.y : pb.y);
+  }
+}
+
 // blockIdx.y of gridDim.y: a slice of q's heads and of k's; blockIdx.x strides
 // over tokens.  A group of 2^group_log2 lanes takes one token at a time: its
-// angles once, then the slice's heads HU at a time.  A row's turn is
-// ya = a k0 + b k1, yb = a k2 + b k3 with (k0, k1, k2, k3) = (c, -s, s, c), or
-// with the norm's weights in them, on column pairs (fma.rn.f32x2).
+// angles once, then the slice's heads in batches of HU rows, the next batch's
+// loads (of the next tensor or token, too) in flight while one is worked on.
+// A row's turn is ya = a k0 + b k1, yb = a k2 + b k3 with (k0, k1, k2, k3) =
+// (c, -s, s, c), or with the norm's weights in them, on column pairs
+// (fma.rn.f32x2).
 template <class L, int MODE, int HU>
 __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) rope_kernel(const __grid_constant__ RopeParams P) {
   using T = typename L::Elem;
   constexpr int NP = L::NP, N2 = NP / 2;
+  constexpr bool GRAD = MODE == ROPE_NORM_GRAD;
   const int lanes = 1 << P.group_log2;
   const int lane = threadIdx.x & (lanes - 1);
-  const int groups = kRopeThreads >> P.group_log2;
+  const uint32_t groups = kRopeThreads >> P.group_log2;
   const int group = threadIdx.x >> P.group_log2;
   const bool partial = 2 * P.half < P.d;
 
@@ -227,169 +263,249 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
     for (int a = 0; a + 1 < P.n_axes; ++a) on += (int)threadIdx.x >= P.ends[a];
     axis[threadIdx.x] = on;
   }
+  // each tensor's weights of the pairs (a, b), as the lanes hold them
+  __shared__ float2 weight[MODE == ROPE_TURN ? 1 : 2][MODE == ROPE_TURN ? 1 : DIT_ROPE_MAX_HEAD_DIM / 2];
+  if constexpr (MODE != ROPE_TURN) {
+    if (group < 2 && P.seg[group].heads)
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (lay.has(i))
+          weight[group][lay.pair(i)] = make_float2(P.seg[group].w[lay.chan_a(i)], lay.has_b(i) ? P.seg[group].w[lay.chan_b(i)] : 0.f);
+  }
   __syncthreads();
   bool turned[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) turned[i] = lay.has(i) && lay.pair(i) < P.half;
-  float2 da[2][N2], db[2][N2];
+  float2 da[N2], db[N2];  // the gradient's sums: a block takes one tensor only
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
-#pragma unroll
-    for (int i = 0; i < N2; ++i) da[g][i] = db[g][i] = make_float2(0.f, 0.f);
+  for (int i = 0; i < N2; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
 
+  // the slice's heads of each tensor
+  const auto first_head = [&](int g) { return (int)(P.seg[g].heads * blockIdx.y / gridDim.y); };
+  const auto end_head = [&](int g) {
+    return GRAD && g != blockIdx.z ? first_head(g) : (int)(P.seg[g].heads * (blockIdx.y + 1) / gridDim.y);
+  };
+  const int g_first = first_head(0) < end_head(0) ? 0 : 1, g_last = first_head(1) < end_head(1) ? 1 : 0;
   const uint32_t step = gridDim.x * groups;
-  // the loop runs while any group of the block has a row: lanes of a warp stay
-  // together for the shuffles
-  for (uint32_t base = blockIdx.x * groups; base < P.rows; base += step) {
-    const uint32_t row = base + group;
-    const bool ok = row < P.rows;
-    const uint32_t b = ok ? row / P.tokens : 0, t = ok ? row - b * P.tokens : 0;
-    float c[NP], s[NP];
+
+  // the next batch: the block's token base, the tensor, its heads, its rows
+  uint32_t base = blockIdx.x * groups, b, t;
+  int g = g_first, h, h1;
+  bool ok;
+  const T* x;
+  const T* dy = nullptr;
+  T* out;
+  // what a lane keeps for itself outside the registers: the next token's
+  // position on every pair's axis (on its way), and the token's cos and sin
+  __shared__ int32_t where[NP][kRopeThreads];
+  __shared__ float2 spin[NP][kRopeThreads];
+  auto token = [&] {
+    ok = base + group < P.rows;
+    b = ok ? (base + group) / P.tokens : 0;
+    t = ok ? base + group - b * P.tokens : 0;
+    const int32_t* pos = static_cast<const int32_t*>(P.pos) + b * P.ps[0] + t * P.ps[1];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) c[i] = 1.f, s[i] = 0.f;
-    if (ok) {
-      const int64_t po = b * P.ps[0] + t * P.ps[1];
+    for (int i = 0; i < NP; ++i)
+      if (turned[i]) cp_async4(&where[i][threadIdx.x], pos + axis[lay.pair(i)], ok);
+  };
+  auto tensor = [&] {
+    const RopeSeg& S = P.seg[g];
+    h = first_head(g);
+    h1 = end_head(g);
+    x = static_cast<const T*>(S.x) + b * S.xs[0] + t * S.xs[1] + h * S.xs[2];
+    if constexpr (GRAD) dy = static_cast<const T*>(S.dy) + b * S.ds[0] + t * S.ds[1] + h * S.ds[2];
+    out = static_cast<T*>(S.out) + b * S.os[0] + t * S.os[1] + h * S.os[2];
+  };
+  typename L::RowRaw rx[HU], rg[GRAD ? HU : 1];
+  auto load = [&] {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (!turned[i]) continue;
-        const int p = lay.pair(i);
-        if (P.pos_f32) {
-          const float pos = static_cast<const float*>(P.pos)[po + axis[p]];
-          turns_sincos(turns_of(pos, turn[p]), c[i], s[i]);
-          if (!finite_bits(pos)) c[i] = s[i] = __int_as_float(0x7FFFFFFF);
-        } else {
-          const int32_t pos = static_cast<const int32_t*>(P.pos)[po + axis[p]];
-          turns_sincos((uint64_t)(int64_t)pos * turn[p], c[i], s[i]);
-        }
-        if (P.negate) s[i] = -s[i];
+    for (int u = 0; u < HU; ++u) {
+      lay.load(rx[u], x, ok && h + u < h1);
+      x += P.seg[g].xs[2];
+      if constexpr (GRAD) {
+        lay.load(rg[u], dy, ok && h + u < h1);
+        dy += P.seg[g].ds[2];
       }
     }
-#pragma unroll(MODE == ROPE_NORM_GRAD ? 2 : 1)  // the gradient's sums are registers of their own for q and k
-    for (int g = 0; g < 2; ++g) {
-      const RopeSeg& S = P.seg[g];
-      const int h0 = S.heads * blockIdx.y / gridDim.y, h1 = S.heads * (blockIdx.y + 1) / gridDim.y;
-      if (h0 >= h1) continue;
-      float2 k0[N2], k1[N2], k2[N2], k3[N2], wa[N2], wb[N2];
+  };
+
+  float2 k0[N2], k1[N2], k2[N2], k3[N2], wa[N2], wb[N2];
+  bool new_token = true, new_tensor = true;
+  token();
+  tensor();
+  if (h < h1) load();
+  else base = P.rows;
+  // the loop runs while any group of the block has a row: lanes of a warp stay
+  // together for the shuffles
+  while (base < P.rows) {
+    if (new_token) {
+      cp_async_wait();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
+        float c = 1.f, s = 0.f;
+        if (turned[i]) {
+          const uint64_t f = turn[lay.pair(i)];
+          const int32_t at = where[i][threadIdx.x];
+          if (P.pos_f32) {
+            turns_sincos(turns_of(__int_as_float(at), f), c, s);
+            if (!finite_bits(__int_as_float(at))) c = s = __int_as_float(0x7FFFFFFF);
+          } else {
+            turns_sincos((uint64_t)(int64_t)at * f, c, s);
+          }
+          if (P.negate) s = -s;
+        }
+        spin[i][threadIdx.x] = make_float2(c, s);
+      }
+    }
+    if (new_tensor) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float2 cs = spin[i][threadIdx.x];
         float va = 1.f, vb = 1.f;
         if constexpr (MODE != ROPE_TURN) {
-          va = lay.has(i) ? S.w[lay.chan_a(i)] : 0.f;
-          vb = lay.has_b(i) ? S.w[lay.chan_b(i)] : 0.f;
+          const float2 w = lay.has(i) ? weight[g][lay.pair(i)] : make_float2(0.f, 0.f);
+          va = w.x, vb = w.y;
         }
-        const float m0 = MODE == ROPE_NORM ? c[i] * va : c[i], m1 = MODE == ROPE_NORM ? -s[i] * vb : -s[i];
-        const float m2 = MODE == ROPE_NORM ? s[i] * va : s[i], m3 = MODE == ROPE_NORM ? c[i] * vb : c[i];
+        const float m0 = MODE == ROPE_NORM ? cs.x * va : cs.x, m1 = MODE == ROPE_NORM ? -cs.y * vb : -cs.y;
+        const float m2 = MODE == ROPE_NORM ? cs.y * va : cs.y, m3 = MODE == ROPE_NORM ? cs.x * vb : cs.x;
         if (i & 1) k0[i / 2].y = m0, k1[i / 2].y = m1, k2[i / 2].y = m2, k3[i / 2].y = m3, wa[i / 2].y = va, wb[i / 2].y = vb;
         else k0[i / 2].x = m0, k1[i / 2].x = m1, k2[i / 2].x = m2, k3[i / 2].x = m3, wa[i / 2].x = va, wb[i / 2].x = vb;
       }
-      const T* x = static_cast<const T*>(S.x) + b * S.xs[0] + t * S.xs[1] + h0 * S.xs[2];
-      const T* dy = MODE == ROPE_NORM_GRAD ? static_cast<const T*>(S.dy) + b * S.ds[0] + t * S.ds[1] + h0 * S.ds[2] : nullptr;
-      T* out = static_cast<T*>(S.out) + b * S.os[0] + t * S.os[1] + h0 * S.os[2];
-      for (int h = h0; h < h1; h += HU) {
-        typename L::RowRaw rx[HU], rg[MODE == ROPE_NORM_GRAD ? HU : 1];
-#pragma unroll
-        for (int u = 0; u < HU; ++u) {
-          lay.load(rx[u], x + u * S.xs[2], ok && h + u < h1);
-          if constexpr (MODE == ROPE_NORM_GRAD) lay.load(rg[u], dy + u * S.ds[2], ok && h + u < h1);
-        }
-#pragma unroll
-        for (int u = 0; u < HU; ++u) {
-          const bool on = ok && h + u < h1;
-          float af[NP], bf[NP];
-          float2 a[N2], e[N2], ya[N2], yb[N2];
-          lay.values(rx[u], af, bf);
-#pragma unroll
-          for (int i = 0; i < N2; ++i) a[i] = make_float2(af[2 * i], af[2 * i + 1]), e[i] = make_float2(bf[2 * i], bf[2 * i + 1]);
-          if constexpr (MODE != ROPE_NORM_GRAD) {
-#pragma unroll
-            for (int i = 0; i < N2; ++i) {
-              ya[i] = ffma2(a[i], k0[i], fmul2(e[i], k1[i]));
-              yb[i] = ffma2(a[i], k2[i], fmul2(e[i], k3[i]));
-            }
-            if (partial) {  // channels that are not turned do not meet their neighbours (0 * inf)
-#pragma unroll
-              for (int i = 0; i < N2; ++i) {
-                if (!turned[2 * i]) ya[i].x = a[i].x * k0[i].x, yb[i].x = e[i].x * k3[i].x;
-                if (!turned[2 * i + 1]) ya[i].y = a[i].y * k0[i].y, yb[i].y = e[i].y * k3[i].y;
-              }
-            }
-            if constexpr (MODE == ROPE_NORM) {
-              float2 q = fmul2(a[0], a[0]);
-              q = ffma2(e[0], e[0], q);
-#pragma unroll
-              for (int i = 1; i < N2; ++i) q = ffma2(e[i], e[i], ffma2(a[i], a[i], q));
-              float ss = q.x + q.y;
-              for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-              const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
-              const float2 r2 = make_float2(r, r);
-#pragma unroll
-              for (int i = 0; i < N2; ++i) ya[i] = fmul2(ya[i], r2), yb[i] = fmul2(yb[i], r2);
-            }
-          } else {
-            float gaf[NP], gbf[NP];
-            float2 ga[N2], gb[N2], q = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f);
-            lay.values(rg[u], gaf, gbf);
-#pragma unroll
-            for (int i = 0; i < N2; ++i) {
-              const float2 va = make_float2(gaf[2 * i], gaf[2 * i + 1]), vb = make_float2(gbf[2 * i], gbf[2 * i + 1]);
-              ga[i] = ffma2(va, k0[i], fmul2(vb, k2[i]));
-              gb[i] = ffma2(va, k1[i], fmul2(vb, k3[i]));
-              if (partial) {
-                if (!turned[2 * i]) ga[i].x = va.x, gb[i].x = vb.x;
-                if (!turned[2 * i + 1]) ga[i].y = va.y, gb[i].y = vb.y;
-              }
-              q = ffma2(e[i], e[i], ffma2(a[i], a[i], q));
-              dt = ffma2(fmul2(ga[i], wa[i]), a[i], dt);
-              dt = ffma2(fmul2(gb[i], wb[i]), e[i], dt);
-            }
-            float ss = q.x + q.y, dot = dt.x + dt.y;
-            for (int o = lanes >> 1; o; o >>= 1) {
-              ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-              dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-            }
-            const float r = rsqrtf(fmaf(ss, P.inv_d, P.eps));
-            const float m = -dot * r * r * P.inv_d;  // dx = r (g w) + x r m
-            const float2 r2 = make_float2(r, r), m2 = make_float2(r * m, r * m);
-            const float2 on2 = on ? r2 : make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < N2; ++i) {
-              ya[i] = ffma2(a[i], m2, fmul2(fmul2(ga[i], wa[i]), r2));
-              yb[i] = ffma2(e[i], m2, fmul2(fmul2(gb[i], wb[i]), r2));
-              da[g][i] = ffma2(fmul2(ga[i], on2), a[i], da[g][i]);
-              db[g][i] = ffma2(fmul2(gb[i], on2), e[i], db[g][i]);
-            }
-          }
-          if (on) {
-#pragma unroll
-            for (int i = 0; i < N2; ++i) af[2 * i] = ya[i].x, af[2 * i + 1] = ya[i].y, bf[2 * i] = yb[i].x, bf[2 * i + 1] = yb[i].y;
-            lay.store(out + u * S.os[2], af, bf);
-          }
-        }
-        x += HU * S.xs[2];
-        dy += HU * S.ds[2];
-        out += HU * S.os[2];
-      }
     }
+    // this batch's rows out of the load registers, and the next batch's loads
+    typename L::RowRaw cx[HU], cg[GRAD ? HU : 1];
+#pragma unroll
+    for (int u = 0; u < HU; ++u) {
+      cx[u] = rx[u];
+      if constexpr (GRAD) cg[u] = rg[u];
+    }
+    const bool row_ok = ok;
+    T* const to = out;
+    const int64_t to_step = P.seg[g].os[2];
+    const int left = min(h1 - h, HU);
+    h += HU;
+    out += HU * to_step;
+    new_tensor = new_token = false;
+    if (h >= h1) {
+      new_tensor = true;
+      if (g == g_last) {
+        new_token = true;
+        base += step;
+        token();
+        g = g_first;
+      } else {
+        g = 1;
+      }
+      tensor();
+    }
+    if (base < P.rows) load();
+    // N rows of the batch at once, their chains of latency side by side; MIX:
+    // some of the lane's channels are not turned
+    auto rows = [&](auto first_, auto n_, auto mix_) {
+      constexpr int N = decltype(n_)::value, first = decltype(first_)::value;
+      constexpr bool MIX = decltype(mix_)::value;
+      [[maybe_unused]] float2 a[N][N2], e[N][N2];
+      float2 ya[N][N2], yb[N][N2];
+      float ss[N], dot[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        float af[NP], bf[NP];
+        lay.values(cx[first + j], af, bf);
+        float2 q = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+          const float2 va = make_float2(af[2 * i], af[2 * i + 1]), vb = make_float2(bf[2 * i], bf[2 * i + 1]);
+          if constexpr (MODE != ROPE_TURN) q = ffma2(vb, vb, ffma2(va, va, q));
+          if constexpr (GRAD) a[j][i] = va, e[j][i] = vb;
+          else turn_pair<MIX>(va, vb, k0[i], k1[i], k2[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
+        }
+        if constexpr (GRAD) {
+          lay.values(cg[first + j], af, bf);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) {
+            const float2 va = make_float2(af[2 * i], af[2 * i + 1]), vb = make_float2(bf[2 * i], bf[2 * i + 1]);
+            turn_pair<MIX>(va, vb, k0[i], k2[i], k1[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
+            dt = ffma2(fmul2(ya[j][i], wa[i]), a[j][i], dt);
+            dt = ffma2(fmul2(yb[j][i], wb[i]), e[j][i], dt);
+          }
+        }
+        ss[j] = q.x + q.y;
+        dot[j] = dt.x + dt.y;
+      }
+      if constexpr (MODE != ROPE_TURN) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          if (o >= lanes) continue;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            ss[j] += __shfl_xor_sync(0xFFFFFFFFu, ss[j], o);
+            if constexpr (GRAD) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float r = rsqrtf(fmaf(ss[j], P.inv_d, P.eps));
+          const float2 r2 = make_float2(r, r);
+          if constexpr (!GRAD) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) ya[j][i] = fmul2(ya[j][i], r2), yb[j][i] = fmul2(yb[j][i], r2);
+          } else {
+            const float m = -dot[j] * r * r * r * P.inv_d;  // dx = r (g w) - x r^3 mean(g w x)
+            const float2 m2 = make_float2(m, m);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              const float2 ga = fmul2(ya[j][i], r2), gb = fmul2(yb[j][i], r2);
+              if (row_ok) da[i] = ffma2(ga, a[j][i], da[i]), db[i] = ffma2(gb, e[j][i], db[i]);
+              ya[j][i] = ffma2(a[j][i], m2, fmul2(ga, wa[i]));
+              yb[j][i] = ffma2(e[j][i], m2, fmul2(gb, wb[i]));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        float af[NP], bf[NP];
+#pragma unroll
+        for (int i = 0; i < N2; ++i)
+          af[2 * i] = ya[j][i].x, af[2 * i + 1] = ya[j][i].y, bf[2 * i] = yb[j][i].x, bf[2 * i + 1] = yb[j][i].y;
+        if (row_ok) lay.store(to + (first + j) * to_step, af, bf);
+      }
+    };
+    // side by side only where two blocks an SM leave the registers for it
+    constexpr int kSide = GRAD && HU > 1 ? 2 : 1;
+    auto batch = [&](auto side_, auto mix, int n) {  // the first n rows, side_ at once
+      constexpr int N = decltype(side_)::value;
+      static_assert(HU <= 4 * N);
+      rows(Int<0>{}, Int<N>{}, mix);
+      if constexpr (HU >= 2 * N)
+        if (n > N) rows(Int<N>{}, Int<N>{}, mix);
+      if constexpr (HU >= 3 * N)
+        if (n > 2 * N) rows(Int<2 * N>{}, Int<N>{}, mix);
+      if constexpr (HU >= 4 * N)
+        if (n > 3 * N) rows(Int<3 * N>{}, Int<N>{}, mix);
+    };
+    if (left < HU) batch(Int<1>{}, std::true_type{}, left);
+    else if (partial) batch(Int<kSide>{}, std::true_type{}, HU);
+    else batch(Int<kSide>{}, std::false_type{}, HU);
   }
 
-  if constexpr (MODE == ROPE_NORM_GRAD) {
+  if constexpr (GRAD) {
     // the block's dweight: groups in order, through shared memory
-    extern __shared__ float sm[];  // [groups][d]
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (!P.seg[g].part) continue;
-      __syncthreads();
+    start_next();
+    float* part = P.seg[blockIdx.z].part;
+    if (part) {
+      extern __shared__ float sm[];  // [groups][d]
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[g][i / 2].y : da[g][i / 2].x;
-        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = i & 1 ? db[g][i / 2].y : db[g][i / 2].x;
+        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[i / 2].y : da[i / 2].x;
+        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = i & 1 ? db[i / 2].y : db[i / 2].x;
       }
       __syncthreads();
       const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
       for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
         float v = 0.f;
-        for (int j = 0; j < groups; ++j) v += sm[j * P.d + ch];
-        P.seg[g].part[block * P.d + ch] = v;
+        for (uint32_t j = 0; j < groups; ++j) v += sm[j * P.d + ch];
+        part[block * P.d + ch] = v;
       }
     }
   }
@@ -406,8 +522,11 @@ __global__ void __launch_bounds__(1024) rope_dweight_kernel(const float* p0, int
   if (!dw) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (ch < d)
+  wait_previous();
+  if (ch < d) {
+#pragma unroll 4
     for (int i = warp; i < n; i += 32) v += p[(int64_t)i * d + ch];
+  }
   sm[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && ch < d) {
@@ -459,7 +578,7 @@ template <class L, int HU>
 cudaError_t launch_mode(const RopeParams& P, int mode, dim3 grid, cudaStream_t s) {
   if (mode == ROPE_TURN) return launch<L, ROPE_TURN, HU>(P, grid, s);
   if (mode == ROPE_NORM) return launch<L, ROPE_NORM, HU>(P, grid, s);
-  return launch<L, ROPE_NORM_GRAD, HU / 2>(P, grid, s);
+  return launch<L, ROPE_NORM_GRAD, (HU > 1 ? HU / 2 : 1)>(P, grid, s);
 }
 
 template <typename T>
@@ -528,18 +647,23 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       }
       // one slice of all heads shares the token's cos and sin best; as many as
       // it takes to give every SM four blocks otherwise
+      const bool grad = mode[first] == ROPE_NORM_GRAD;
+      const int nz = grad && together ? 2 : 1;
       int64_t nx = ((int64_t)P.rows + (kRopeThreads >> Q.group_log2) - 1) >> (8 - Q.group_log2);
-      int64_t ny = (608 + nx - 1) / nx;
+      int64_t ny = (608 + nx * nz - 1) / (nx * nz);
       if (ny > hmax) ny = hmax;
       if (ny > 256) ny = 256;
-      if (mode[first] == ROPE_NORM_GRAD && nx * ny > kRopeGradBlocks / 2) nx = kRopeGradBlocks / 2 / ny;
+      // the gradient keeps its weight sums in registers: as many blocks as run
+      // at once, so few partials are left to join (two per SM: 115 us on the
+      // 32760-token video gradient, 127 us with 1024 blocks a tensor)
+      if (grad && nx * ny > 304 / nz) nx = 304 / nz / ny > 0 ? 304 / nz / ny : 1;
       for (int i = first; i <= last; ++i)
-        if (mode[i] == ROPE_NORM_GRAD && h[i]->dweight) {
+        if (grad && h[i]->dweight) {
           blocks[i] = (int)(nx * ny);
           if (i == 1) part[1] = part[0] + (int64_t)blocks[0] * P.d;
           Q.seg[i - first].part = part[i];
         }
-      const dim3 grid((unsigned)nx, (unsigned)ny);
+      const dim3 grid((unsigned)nx, (unsigned)ny, (unsigned)nz);
       cudaError_t e;
       if (a.dtype == DIT_DTYPE_F32) e = launch_layout<float>(Q, layout[first], mode[first], grid, stream);
       else if (a.dtype == DIT_DTYPE_BF16) e = launch_layout<__nv_bfloat16>(Q, layout[first], mode[first], grid, stream);
@@ -548,11 +672,9 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
     }
   }
   float* dw[2] = {backward ? a.q.dweight : nullptr, backward ? a.k.dweight : nullptr};
-  if (dw[0] || dw[1]) {
-    rope_dweight_kernel<<<dim3((P.d + 31) / 32, 2), 1024, 0, stream>>>(part[0], blocks[0], dw[0], part[1], blocks[1],
-                                                                     dw[1], P.d);
-    return cudaGetLastError();
-  }
+  if (dw[0] || dw[1])
+    return launch_kernel(rope_dweight_kernel, dim3((P.d + 31) / 32, 2), dim3(1024), 0, stream, 1, P.rows != 0, part[0],
+                         blocks[0], dw[0], part[1], blocks[1], dw[1], P.d);
   return cudaSuccess;
 }
 

@@ -182,107 +182,114 @@ def flow_euler_step(x, v, sigma: float, sigma_next: float, n: int, stream=None):
 _ROPE_ARGS = struct.Struct("<2q8i2fQ2q2i" + 2 * "2iQ3qQ3qQ3q2Q")
 _GN_ARGS = struct.Struct("<2q4ifiQ2qQ2qQ2q6Q")
 _NO_VIEW = (0, 0, 0, 0)
-_dtype_codes = None
+_torch = None          # the module, and its dtypes as dit.h names them, on first use
+_dtype_codes = {}
 
 
-def _dtype_code(t):
-    global _dtype_codes
-    if _dtype_codes is None:
+def _use_torch():
+    global _torch
+    if _torch is None:
         import torch
-        _dtype_codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-    try:
-        return _dtype_codes[t.dtype]
-    except KeyError:
-        raise DitError(DIT_ERR_INVALID_ARG, f"unsupported dtype {t.dtype}") from None
+        _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+        _torch = torch
+    return _torch
 
 
 def _refuse(status, msg):
     raise DitError(status, msg)
 
 
-def _param(name, t, shape, device):
+def _dtype_code(dtype):
+    code = _dtype_codes.get(dtype)
+    return _refuse(DIT_ERR_INVALID_ARG, f"unsupported dtype {dtype}") if code is None else code
+
+
+# The library looks up which device owns each pointer and refuses a mixture,
+# so the helpers here compare types and shapes only.
+def _param(name, t, shape):
     """Pointer of an optional contiguous float32 tensor of this shape."""
     if t is None:
         return 0
-    if t.device != device:
-        _refuse(DIT_ERR_INVALID_ARG, f"{name} is on {t.device}, not {device}")
-    if t.element_size() != 4 or not t.is_floating_point():
+    if t.dtype is not _torch.float32:
         _refuse(DIT_ERR_INVALID_ARG, f"{name} must be float32")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         _refuse(DIT_ERR_SHAPE, f"{name} must be contiguous {list(shape)}")
     return t.data_ptr()
 
 
-def _launch_on(device, workspace, stream, need, args):
-    """(workspace pointer, bytes, stream) of a call on `device`."""
-    import torch
-    if device.type != "cuda":
-        _refuse(DIT_ERR_INVALID_ARG, f"tensors are on {device}, not on a CUDA device")
-    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
-    if need is None:
-        return 0, 0, s
+def _raw_stream(t, stream):
+    """cudaStream_t of the call: torch's current stream of the tensor's device unless one is given."""
+    if not t.is_cuda:
+        _refuse(DIT_ERR_INVALID_ARG, f"tensors are on {t.device}, not on a CUDA device")
+    return _torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else _stream(stream)
+
+
+def _workspace(t, workspace, stream, need):
+    """(pointer, bytes, owner) of the caller's workspace, or of one taken from
+    torch's allocator: its owner lives until the launch has been made."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            _refuse(DIT_ERR_INVALID_ARG, f"the workspace must be contiguous memory on {device}")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), s
-    n = need(args)
-    if n < 0:
+        if not workspace.is_contiguous():
+            _refuse(DIT_ERR_INVALID_ARG, "the workspace must be contiguous")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if need < 0:
         raise DitError(DIT_ERR_INVALID_ARG, lib().dit_last_error().decode())
-    if n == 0:
-        return 0, 0, s
+    if need == 0:
+        return 0, 0, None
     if stream is not None:
         _refuse(DIT_ERR_INVALID_ARG, "a call on an explicit stream needs its workspace passed in")
-    # torch's allocator hands the block out in the order of the current stream, which is the call's
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    return ws.data_ptr(), n, s
+    # the allocator hands blocks out in the order of the current stream, which is the call's
+    ws = _torch.empty(need, dtype=_torch.uint8, device=t.device)
+    return ws.data_ptr(), need, ws
 
 
-def _heads_view(name, t, like):
+def _heads_view(name, t, shape, dtype):
     """(pointer, batch, token and head strides) of a [batch, tokens, heads, head_dim] view."""
-    if t.shape != like.shape:
-        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(like.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        _refuse(DIT_ERR_INVALID_ARG, f"{name} has another dtype or device")
+    if t.shape != shape:
+        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(shape)}")
+    if t.dtype is not dtype:
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
     sb, st, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1 and t.numel():
+    if sd != 1 and t.numel():
         _refuse(DIT_ERR_SHAPE, f"{name}: the channels of a head must be contiguous")
     return t.data_ptr(), sb, st, sh
 
 
-def _rope_heads(tag, x, dy, out, weight, dweight, ref):
-    """Packed dit_rope_heads of one tensor; ref is (batch, tokens, head_dim, dtype, device)."""
+def _rope_heads(tag, x, dy, out, weight, dweight, B, N, d, dtype):
+    """Fields of the dit_rope_heads of one tensor."""
     if out is None:
         if x is not None or dy is not None or weight is not None or dweight is not None:
             _refuse(DIT_ERR_INVALID_ARG, f"{tag} is given without its output")
         return (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
-    if out.dim() != 4 or (out.shape[0], out.shape[1], out.shape[3]) != ref[:3]:
-        _refuse(DIT_ERR_SHAPE, f"{tag} is {list(out.shape)}: [{ref[0]}, {ref[1]}, heads, {ref[2]}] is wanted")
-    if out.dtype != ref[3] or out.device != ref[4]:
-        _refuse(DIT_ERR_INVALID_ARG, f"{tag} has another dtype or device")
-    return (out.shape[2], 0,
-            *(_NO_VIEW if x is None else _heads_view(f"{tag} input", x, out)),
-            *(_NO_VIEW if dy is None else _heads_view(f"{tag} gradient", dy, out)),
-            *_heads_view(f"{tag} output", out, out),
-            _param(f"{tag}_weight", weight, (ref[2],), ref[4]), _param(f"d{tag}_weight", dweight, (ref[2],), ref[4]))
+    shape = out.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != N or shape[3] != d:
+        _refuse(DIT_ERR_SHAPE, f"{tag} output is {list(shape)}: [{B}, {N}, heads, {d}] is wanted")
+    return (shape[2], 0,
+            *(_NO_VIEW if x is None else _heads_view(f"{tag} input", x, shape, dtype)),
+            *(_NO_VIEW if dy is None else _heads_view(f"{tag} gradient", dy, shape, dtype)),
+            *_heads_view(f"{tag} output", out, shape, dtype),
+            0 if weight is None else _param(f"{tag}_weight", weight, (d,)),
+            0 if dweight is None else _param(f"d{tag}_weight", dweight, (d,)))
 
 
 def _rope_args(pos, axes, theta, style, eps, first, q, k):
-    import torch
-    B, N, _, d = first.shape if first.dim() == 4 else _refuse(DIT_ERR_SHAPE, "q must be [batch, tokens, heads, head_dim]")
-    n = len(axes)
+    torch = _torch or _use_torch()
+    if first.dim() != 4:
+        _refuse(DIT_ERR_SHAPE, "q must be [batch, tokens, heads, head_dim]")
+    B, N, _, d = first.shape
+    dtype, n, ps, pd = first.dtype, len(axes), pos.shape, pos.dtype
+    code = _dtype_code(dtype)
     if not 1 <= n <= ROPE_MAX_AXES:
         _refuse(DIT_ERR_INVALID_ARG, f"1 to {ROPE_MAX_AXES} axes are supported")
-    if pos.dim() not in (2, 3) or tuple(pos.shape[-2:]) != (N, n) or (pos.dim() == 3 and pos.shape[0] != B):
-        _refuse(DIT_ERR_SHAPE, f"positions are {list(pos.shape)}: [{N}, {n}] or [{B}, {N}, {n}] is wanted")
-    if pos.dtype not in (torch.int32, torch.float32) or pos.device != first.device:
-        _refuse(DIT_ERR_INVALID_ARG, "positions must be int32 or float32 on the tensors' device")
-    ps = pos.stride()
-    if n > 1 and ps[-1] != 1 and pos.numel():
+    if len(ps) not in (2, 3) or ps[-2] != N or ps[-1] != n or (len(ps) == 3 and ps[0] != B):
+        _refuse(DIT_ERR_SHAPE, f"positions are {list(ps)}: [{N}, {n}] or [{B}, {N}, {n}] is wanted")
+    if pd is not torch.int32 and pd is not torch.float32:
+        _refuse(DIT_ERR_INVALID_ARG, "positions must be int32 or float32")
+    st = pos.stride()
+    if st[-1] != 1 and n > 1 and pos.numel():
         _refuse(DIT_ERR_SHAPE, "the axes of a position must be contiguous")
-    ref = (B, N, d, first.dtype, first.device)
-    return _ROPE_ARGS.pack(B, N, d, _dtype_code(first), style, n, *axes, *(0,) * (4 - n), theta, eps, pos.data_ptr(),
-                           ps[0] if pos.dim() == 3 else 0, ps[-2], POS_F32 if pos.is_floating_point() else POS_I32, 0,
-                           *_rope_heads("q", *q, ref), *_rope_heads("k", *k, ref))
+    return _ROPE_ARGS.pack(B, N, d, code, style, n, *axes, *_NO_VIEW[n:], theta, eps, pos.data_ptr(),
+                           st[0] if len(ps) == 3 else 0, st[-2], POS_I32 if pd is torch.int32 else POS_F32, 0,
+                           *_rope_heads("q", *q, B, N, d, dtype), *_rope_heads("k", *k, B, N, d, dtype))
 
 
 def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, style=ROPE_INTERLEAVED, q_weight=None,
@@ -296,7 +303,9 @@ def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, styl
     number of heads (see dit_rope_forward in include/dit.h)."""
     args = _rope_args(pos, axes, theta, style, eps, q, (q, None, q_out, q_weight, None),
                       (k, None, k_out, k_weight, None))
-    _check(lib().dit_rope_forward(args, _launch_on(q.device, None, stream, None, args)[2]))
+    status = lib().dit_rope_forward(args, _raw_stream(q, stream))
+    if status:
+        _check(status)
 
 
 def dit_rope_backward(pos, dq_out, dq, dk_out=None, dk=None, *, axes, theta=1e4, style=ROPE_INTERLEAVED, q=None,
@@ -309,9 +318,9 @@ def dit_rope_backward(pos, dq_out, dq, dk_out=None, dk=None, *, axes, theta=1e4,
     torch's allocator (only on torch's current stream)."""
     args = _rope_args(pos, axes, theta, style, eps, dq_out, (q, dq_out, dq, q_weight, dq_weight),
                       (k, dk_out, dk, k_weight, dk_weight))
-    L = lib()
-    ws, n, s = _launch_on(dq_out.device, workspace, stream,
-                          None if dq_weight is None and dk_weight is None else L.dit_rope_workspace_bytes, args)
+    L, s, ws, n, owner = lib(), _raw_stream(dq_out, stream), 0, 0, None
+    if dq_weight is not None or dk_weight is not None:
+        ws, n, owner = _workspace(dq_out, workspace, stream, L.dit_rope_workspace_bytes(args))
     _check(L.dit_rope_backward(args, ws, n, s))
 
 
@@ -326,42 +335,45 @@ def dit_rope_workspace_bytes(head_dim: int) -> int:
     return n
 
 
-def _pixel_view(name, t, like):
+def _pixel_view(name, t, shape, dtype):
     """(pointer, batch stride, pixel stride) of a [batch, ..., channels] view."""
-    if t.shape != like.shape:
-        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(like.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        _refuse(DIT_ERR_INVALID_ARG, f"{name} has another dtype or device")
-    shape, stride = t.shape, t.stride()
+    if t.shape != shape:
+        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(shape)}")
+    if t.dtype is not dtype:
+        _refuse(DIT_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
+    stride = t.stride()
     if t.numel() == 0:
         return 0, 0, 0
     if stride[-1] != 1 and shape[-1] > 1:
         _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous (channels last)")
-    step, span = 0, 0
-    for i in range(t.dim() - 2, 0, -1):  # the middle axes as one axis of pixels
-        if shape[i] == 1:
-            continue
-        if not step:
-            step = stride[i]
-        elif stride[i] != span:
-            _refuse(DIT_ERR_SHAPE, f"{name}: the axes between batch and channels must have one common stride")
-        span = stride[i] * shape[i]
-    return t.data_ptr(), stride[0] if shape[0] > 1 else 0, step
+    step = stride[-2]
+    if len(shape) > 3:  # the middle axes as one axis of pixels
+        step, span = 0, 0
+        for i in range(len(shape) - 2, 0, -1):
+            if shape[i] == 1:
+                continue
+            if not step:
+                step = stride[i]
+            elif stride[i] != span:
+                _refuse(DIT_ERR_SHAPE, f"{name}: the axes between batch and channels must have one common stride")
+            span = stride[i] * shape[i]
+    return t.data_ptr(), stride[0], step
 
 
 def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, act):
-    if x.dim() < 3:
+    _torch or _use_torch()
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 3:
         _refuse(DIT_ERR_SHAPE, "x must be [batch, ..., channels]")
-    B, C = x.shape[0], x.shape[-1]
-    P = 1
-    for v in x.shape[1:-1]:
+    B, C, P = shape[0], shape[-1], 1
+    for v in shape[1:-1]:
         P *= v
-    dev = x.device
-    return _GN_ARGS.pack(B, P, C, groups, _dtype_code(x), act, eps, 0, *_pixel_view("x", x, x),
-                         *((0, 0, 0) if dy is None else _pixel_view("dy", dy, x)), *_pixel_view("out", out, x),
-                         _param("weight", weight, (C,), dev), _param("bias", bias, (C,), dev),
-                         _param("mean", mean, (B, groups), dev), _param("rstd", rstd, (B, groups), dev),
-                         _param("dweight", dweight, (C,), dev), _param("dbias", dbias, (C,), dev))
+    return _GN_ARGS.pack(B, P, C, groups, _dtype_code(dtype), act, eps, 0, *_pixel_view("x", x, shape, dtype),
+                         *((0, 0, 0) if dy is None else _pixel_view("dy", dy, shape, dtype)),
+                         *((0, 0, 0) if out is None else _pixel_view("out", out, shape, dtype)),
+                         _param("weight", weight, (C,)), _param("bias", bias, (C,)),
+                         _param("mean", mean, (B, groups)), _param("rstd", rstd, (B, groups)),
+                         _param("dweight", dweight, (C,)), _param("dbias", dbias, (C,)))
 
 
 def dit_group_norm_forward(x, y, groups: int, *, weight=None, bias=None, mean=None, rstd=None, eps=1e-6, act=ACT_NONE,
@@ -372,8 +384,8 @@ def dit_group_norm_forward(x, y, groups: int, *, weight=None, bias=None, mean=No
     dit_group_norm_workspace_bytes, or None to take one from torch's allocator
     (only on torch's current stream)."""
     args = _gn_args(x, None, y, groups, weight, bias, mean, rstd, None, None, eps, act)
-    L = lib()
-    ws, n, s = _launch_on(x.device, workspace, stream, lambda a: L.dit_group_norm_workspace_bytes(a, 0), args)
+    L, s = lib(), _raw_stream(x, stream)
+    ws, n, owner = _workspace(x, workspace, stream, L.dit_group_norm_workspace_bytes(args, 0))
     _check(L.dit_group_norm_forward(args, ws, n, s))
 
 
@@ -383,21 +395,15 @@ def dit_group_norm_backward(x, dy, mean, rstd, dx, groups: int, *, weight=None, 
     dweight / dbias (float32 [channels], overwritten) where given.  mean and
     rstd are what the forward call wrote."""
     args = _gn_args(x, dy, dx, groups, weight, bias, mean, rstd, dweight, dbias, 0.0, act)
-    L = lib()
-    ws, n, s = _launch_on(x.device, workspace, stream, lambda a: L.dit_group_norm_workspace_bytes(a, 1), args)
+    L, s = lib(), _raw_stream(x, stream)
+    ws, n, owner = _workspace(x, workspace, stream, L.dit_group_norm_workspace_bytes(args, 1))
     _check(L.dit_group_norm_backward(args, ws, n, s))
 
 
 def dit_group_norm_workspace_bytes(x, groups: int, backward: bool) -> int:
-    """Workspace of a group-norm call on tensors like x (the same strides and
-    alignment in every argument)."""
-    view = _pixel_view("x", x, x)
-    P = 1
-    for v in x.shape[1:-1]:
-        P *= v
+    """Workspace of a group-norm call on tensors of x's shape and type."""
     n = lib().dit_group_norm_workspace_bytes(
-        _GN_ARGS.pack(x.shape[0], P, x.shape[-1], groups, _dtype_code(x), ACT_NONE, 0.0, 0, *view, *view, *view,
-                      0, 0, 0, 0, 0, 0), 1 if backward else 0)
+        _gn_args(x, None, None, groups, None, None, None, None, None, None, 0.0, ACT_NONE), 1 if backward else 0)
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
     return n
