@@ -7,24 +7,24 @@
 // pixels; dw = sum_batch B, db = sum_batch A; with the group means
 // s1 = mean(w dz), s2 = mean(w dz xhat): dx = rstd (w dz - s1 - xhat s2).
 //
-// Sums.  A thread owns a run of V channels and walks pixels.  It keeps, per
-// channel, sums of x - K and (x - K)^2 about a pivot K (its first value, then
-// its running mean), and folds them every 32 pixels into (count, mean, M2):
-// nothing cancels however large the mean is against the deviation.  Threads,
-// channels of a group and blocks are then joined as (count, mean, M2) in a
-// fixed order, so results are the same bits every time.
+// Sums.  A thread owns a run of V channels and walks pixels, summing x - K and
+// (x - K)^2 per channel about the block's pivot K, the median of three of the
+// channel's pixels in the block: the sums are of deviations, so nothing
+// cancels however large the mean, and a single outlier cannot become the
+// pivot.  Threads are joined by plain sums, then turned into (mean, M2) about
+// the mean, and channels of a group and blocks joined as (count, mean, M2), all
+// in a fixed order: results are the same bits every time.
 //
 // What bounds it: HBM and the second look at x.  Two forms:
 //   - whole groups of a batch element that fit a cluster's shared memory: one
 //     launch.  A block loads its pixels once, into shared memory, the cluster
 //     joins the groups' sums through distributed shared memory, and the block
 //     writes its pixels out of shared memory: one read, one write.
-//   - otherwise three launches chained by programmatic dependence: sums per
-//     (pixel range, group), a join per (batch element, group), and a pass that
-//     walks the pixel ranges backwards, so that what the sums read last is
-//     still in L2.
-#include <stdio.h>
-#include <stdlib.h>
+//   - otherwise sums per (share of the pixels, group), a join per (batch
+//     element, group) where the shares are many, and a pass that walks the
+//     pixels backwards, so that what the sums read last is still in L2;
+//     launches chained by programmatic dependence, the pass's first loads on
+//     their way before the sums are done.
 #include "launch.cuh"
 #include "operators.h"
 #include "vec.cuh"
@@ -34,22 +34,24 @@ namespace dit {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSumUnroll = 4;    // pixels in flight a thread: forward
-constexpr int kPassUnroll = 4;
-constexpr int kGradUnroll = 2;   // gradient: of both tensors
-constexpr int kFold = 32;        // pixels a thread sums before it folds
+// Blocks an SM of the kernels that stream a tensor: two, whose shared-memory
+// rings keep about 110 KB on its way; six where runs are shorter than 16 bytes
+// and loads go to registers.
+constexpr int stream_blocks(int run_bytes) { return run_bytes == 16 ? 2 : 6; }
 
 struct GnParams {
   const void* x;
   const void* dy;
   void* out;
   int64_t xs[2], ds[2], os[2];
-  int64_t batch, pixels;
-  int channels, groups, cpg;
-  int splits;      // pixel ranges a batch element is cut into
+  int64_t batch;
+  int pixels, channels, groups, cpg;
+  int splits;      // blocks that share a batch element's pixels
   int passes;      // the same for the pass that writes
   int slab;        // runs of V channels a block covers
+  int part_lanes;  // threads that sum one channel's rows: a power of two
   int unit;        // channels of one partial: cpg where slabs hold whole groups, else 1
+  int fold;        // the forward's pass joins the partials itself
   int act;
   float eps;
   const float* w;
@@ -126,97 +128,148 @@ DIT_DEV void v_sigmoid(float (&d)[V], const float (&z)[V]) {
   for (int i = 0; i < V; ++i) d[i] = rcp_approx(t[i]);
 }
 
-DIT_DEV int64_t range_begin(int64_t pixels, int splits, int s) { return pixels * s / splits; }
-
 // ---------------------------------------------------------------- blocks
-// Thread (row, run) takes run `run` of the slab and pixels row, row + rows,
-// ... of the block's range [p0, p1).
+// `shares` blocks take a batch element's pixels in turn, `rows` at a time: at
+// any moment all of them are near the same place, so what was read last is the
+// end of the tensor.
+// Thread (row, run) of share s takes run `run` of the slab and pixels
+// p, p + step, ...
 struct Place {
-  int rows, row, run, c, count;
-  int64_t p;
+  int rows, row, run, c, p, step, count;
   bool on;
-  DIT_DEV Place(const GnParams& P, int V, int slab_index, int64_t p0, int64_t p1) {
-    rows = kThreads / P.slab;
-    row = threadIdx.x / P.slab;
+  DIT_DEV Place(const GnParams& P, int V, int slab_index, int s, int shares) {
+    rows = kThreads / (unsigned)P.slab;
+    row = threadIdx.x / (unsigned)P.slab;
     run = threadIdx.x - row * P.slab;
     c = (slab_index * P.slab + run) * V;
     on = row < rows && c < P.channels;
-    p = p0 + row;
-    count = on && p < p1 ? (int)((p1 - p + rows - 1) / rows) : 0;
+    step = shares * rows;
+    p = s * rows + row;
+    count = on && p < P.pixels ? (P.pixels - p + step - 1) / (unsigned)step : 0;
   }
 };
-
-// Calls body(i, raw...) for pixels 0 .. count - 1 of a thread, U loads of each
-// tensor ahead.
-template <typename T, int V, int U, class Body>
-DIT_DEV void walk(const T* x, int64_t step, int count, Body body) {
-  int i = 0;
-  for (; i + U <= count; i += U) {
-    Raw<T, V> r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = load_raw<T, V>(x + u * step);
-    x += U * step;
-#pragma unroll
-    for (int u = 0; u < U; ++u) body(i + u, r[u]);
-  }
-  Raw<T, V> r[U - 1];
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (i + u < count) r[u] = load_raw<T, V>(x + u * step);
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (i + u < count) body(i + u, r[u]);
-}
-template <typename T, int V, int U, class Body>
-DIT_DEV void walk2(const T* x, int64_t xstep, const T* g, int64_t gstep, int count, Body body) {
-  int i = 0;
-  for (; i + U <= count; i += U) {
-    Raw<T, V> r[U], q[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = load_raw<T, V>(x + u * xstep), q[u] = load_raw<T, V>(g + u * gstep);
-    x += U * xstep;
-    g += U * gstep;
-#pragma unroll
-    for (int u = 0; u < U; ++u) body(i + u, r[u], q[u]);
-  }
-  Raw<T, V> r[U - 1], q[U - 1];
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (i + u < count) r[u] = load_raw<T, V>(x + u * xstep), q[u] = load_raw<T, V>(g + u * gstep);
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (i + u < count) body(i + u, r[u], q[u]);
+// Pixels of share s.
+DIT_DEV int share_pixels(const GnParams& P, int rows, int s, int shares) {
+  const int turns = P.pixels / (unsigned)(shares * rows), left = P.pixels - turns * shares * rows - s * rows;
+  return turns * rows + (left < 0 ? 0 : left < rows ? left : rows);
 }
 
-// A thread's mean and M2 per channel.
+// A thread's pixels 0 .. count - 1 of N tensors, read ahead of their use: run(
+// body) calls body(i, raw[N]) for each.  Runs of 16 bytes come through a ring in
+// shared memory by cp.async, STAGES batches of U pixels, each thread filling and
+// reading its own slots only (no barriers, no registers held by what is on its
+// way); a slot is filled again one batch after its values were used.  Shorter
+// runs, which cp.async cannot move, are loaded into registers a batch ahead.
+// LAST: the data is not read again (first out of L2).
+template <typename T, int V, int N, int U, int STAGES, bool LAST>
+struct Feed {
+  enum : int {
+    kRing = V * sizeof(T) == 16,
+    kSlot = kRing ? kThreads * V : 0,  // elements of a slot of all threads
+    kBytes = STAGES * U * N * kSlot * (int)sizeof(T)
+  };
+  const T* src[N];
+  int64_t step[N];
+  T* ring;
+  int count, next, slot;
+  uint64_t policy;
+  Raw<T, V> reg[kRing ? 1 : U * N];
+
+  DIT_DEV void from(int k, const T* p, int64_t s) { src[k] = p, step[k] = s; }
+  DIT_DEV void fetch() {  // the next batch
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool some = next + u < count;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if constexpr (kRing) {
+          if (some) copy16(ring + ((slot * U + u) * N + k) * kSlot, src[k]);
+        } else {
+          if (some) reg[u * N + k] = LAST ? load_raw_stream<T, V>(src[k]) : load_raw<T, V>(src[k]);
+        }
+        src[k] += step[k];
+      }
+    }
+    next += U;
+    if constexpr (kRing) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+  }
+  DIT_DEV void copy16(T* dst, const T* p) const {
+    if constexpr (LAST)
+      asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(p), "l"(policy) : "memory");
+    else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(p) : "memory");
+  }
+  // the first loads on their way; `ring_` is the block's, kBytes of it
+  DIT_DEV void start(void* ring_, int count_) {
+    ring = static_cast<T*>(ring_) + threadIdx.x * V;
+    count = count_;
+    next = slot = 0;
+    if constexpr (LAST) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    if constexpr (kRing) {
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) fetch();
+    } else {
+      fetch();
+    }
+  }
+  template <class Body>
+  DIT_DEV void run(Body body) {
+    int at = 0;
+    for (int i = 0; i < count; i += U) {
+      Raw<T, V> r[U][N];
+      if constexpr (kRing) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < N; ++k) r[u][k] = load_raw<T, V>(ring + ((at * U + u) * N + k) * kSlot);
+        at = at + 1 == STAGES ? 0 : at + 1;
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < N; ++k) r[u][k] = reg[u * N + k];
+      }
+      fetch();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u < count) body(i + u, r[u]);
+    }
+  }
+};
+template <typename T, int V, bool LAST>
+using Feed1 = Feed<T, V, 1, (V * sizeof(T) == 16 ? 2 : 8), 8, LAST>;
+template <typename T, int V, bool LAST>
+using Feed2 = Feed<T, V, 2, (V * sizeof(T) == 16 ? 1 : 8), 8, LAST>;
+
+// A thread's sums of x - K and (x - K)^2 per channel.
 template <int V>
 struct Moments {
-  float K[V], s[V], q[V], M2[V];
-  int n, m;
-  DIT_DEV Moments() : n(0), m(0) { v_set(K, 0.f), v_set(s, 0.f), v_set(q, 0.f), v_set(M2, 0.f); }
-  DIT_DEV void add(const float (&v)[V]) {
-    if (n + m == 0) {
+  float K[V], s[V], q[V];
+  DIT_DEV Moments() { v_set(K, 0.f), v_set(s, 0.f), v_set(q, 0.f); }
+  // median of three of the block's pixels: row 0's first, middle and last
+  template <typename T>
+  DIT_DEV void pivot(const T* first, int64_t step, int count) {
+    const Raw<T, V> r[3] = {load_raw<T, V>(first), load_raw<T, V>(first + count / 2 * step),
+                            load_raw<T, V>(first + (count - 1) * step)};
+    float a[V], b[V], c[V];
+    unpack<T, V>(r[0], a);
+    unpack<T, V>(r[1], b);
+    unpack<T, V>(r[2], c);
 #pragma unroll
-      for (int i = 0; i < V; ++i) K[i] = v[i];
+    for (int i = 0; i < V; ++i) {
+      const float m = fmaxf(fminf(a[i], b[i]), fminf(fmaxf(a[i], b[i]), c[i]));
+      K[i] = fabsf(m) <= 3.402823466e38f ? m : 0.f;
     }
+  }
+  DIT_DEV void add(const float (&v)[V]) {
     float d[V];
     v_sub(d, v, K);
     v_add(s, s, d);
     v_fma(q, d, d, q);
-    if (++m == kFold) fold();
-  }
-  DIT_DEV void fold() {
-    if (!m) return;
-    const float im = 1.f / (float)m, f = (float)m / (float)(n + m), g = (float)n * f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float d = s[i] * im;
-      M2[i] += fmaf(-d, s[i], q[i]) + d * d * g;
-      K[i] = fmaf(d, f, K[i]);
-      s[i] = q[i] = 0.f;
-    }
-    n += m;
-    m = 0;
   }
 };
 
@@ -234,65 +287,33 @@ DIT_DEV void store_raw(T* p, const Raw<T, V>& r) {
   }
 }
 
-// Per-channel pairs of a block's rows in shared memory, [rows][V][slab]: a
-// warp's accesses fall on consecutive words.
-DIT_DEV int pair_at(int V, int slab, int c) { return c % V * slab + c / V; }  // channel c of row 0
-
-// Joins the rows' (count, mean, M2) of every channel into row 0 of sm,
-// halving the rows; cnt[rows] is scratch.
-template <int V>
-DIT_DEV void join_rows(const Place& at, Moments<V>& A, float2* sm, float* cnt, int slab) {
-  auto put = [&](int row) { return sm + row * V * slab + at.run; };
-  float n = (float)at.count;
+// Per-channel pairs of a block's rows in shared memory, [rows][V][slab] and a
+// pair of padding a row: neither the writers (runs next to each other) nor the
+// readers (rows or channels next to each other) meet on a bank.
+// Sums the rows' pairs: out(c, total) once for every channel c of the slab, by
+// `part` neighbouring threads a channel.
+template <int V, class Out>
+DIT_DEV void sum_rows(const Place& at, const float (&A)[V], const float (&B)[V], float2* sm, int slab, int part, Out out) {
+  const int width = slab * V, pitch = width + 1;
   if (at.row < at.rows) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) put(at.row)[i * slab] = make_float2(A.K[i], A.M2[i]);
-    if (at.run == 0) cnt[at.row] = n;
-  }
-  for (int rows = at.rows; rows > 1;) {
-    const int h = (rows + 1) / 2;
-    __syncthreads();
-    if (at.row + h < rows) {
-      const float nb = cnt[at.row + h];
-      if (nb > 0.f) {
-        const float f = nb / (n + nb), g = n * f;
-        n += nb;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 o = put(at.row + h)[i * slab];
-          const float d = o.x - A.K[i];
-          A.K[i] = fmaf(d, f, A.K[i]);
-          A.M2[i] += fmaf(d * d, g, o.y);
-          put(at.row)[i * slab] = make_float2(A.K[i], A.M2[i]);
-        }
-        if (at.run == 0) cnt[at.row] = n;
-      }
-    }
-    rows = h;
+    for (int i = 0; i < V; ++i) sm[at.row * pitch + i * slab + at.run] = make_float2(A[i], B[i]);
   }
   __syncthreads();
-}
-
-// The same for plain sums.
-template <int V>
-DIT_DEV void add_rows(const Place& at, float (&A)[V], float (&B)[V], float2* sm, int slab) {
-  auto put = [&](int row) { return sm + row * V * slab + at.run; };
-  if (at.row < at.rows) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) put(at.row)[i * slab] = make_float2(A[i], B[i]);
-  }
-  for (int rows = at.rows; rows > 1;) {
-    const int h = (rows + 1) / 2;
-    __syncthreads();
-    if (at.row + h < rows) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 o = put(at.row + h)[i * slab];
-        A[i] += o.x, B[i] += o.y;
-        put(at.row)[i * slab] = make_float2(A[i], B[i]);
+  const int t = threadIdx.x & (part - 1), per = kThreads / (unsigned)part;
+  for (int c0 = 0; c0 < width; c0 += per) {
+    const int j = c0 + threadIdx.x / (unsigned)part;  // place in a row: channel run j % slab, element j / slab
+    float2 v = make_float2(0.f, 0.f);
+    if (j < width)
+      for (int r = t; r < at.rows; r += part) {
+        const float2 o = sm[r * pitch + j];
+        v.x += o.x, v.y += o.y;
       }
+    for (int o = part >> 1; o; o >>= 1) {
+      v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+      v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
     }
-    rows = h;
+    if (t == 0 && j < width) out(j % (unsigned)slab * V + j / (unsigned)slab, v);
   }
   __syncthreads();
 }
@@ -304,29 +325,29 @@ DIT_DEV float warp_sum(float v) {
 }
 
 // Joins the channels of every group of the slab, each of `len` pixels, from
-// row 0 of sm; out(g, mean, M2).  A thread a group of few channels, a warp one
-// of many.
-template <int V, class Out>
-DIT_DEV void join_channels(const float2* sm, int slab, int groups, int cpg, float len, Out out) {
+// their (mean, M2) in ch; out(g, mean, M2).  A thread a group of few channels,
+// a warp one of many.
+template <class Out>
+DIT_DEV void join_channels(const float2* ch, int groups, int cpg, float len, Out out) {
   if (cpg <= 8) {
     for (int g = threadIdx.x; g < groups; g += kThreads) {
-      auto e = [&](int c) { return sm[pair_at(V, slab, g * cpg + c)]; };
-      const float K = e(0).x;
+      const float2* e = ch + g * cpg;
+      const float K = e[0].x;
       float mean = 0.f, M = 0.f;
-      for (int c = 1; c < cpg; ++c) mean += e(c).x - K;
+      for (int c = 1; c < cpg; ++c) mean += e[c].x - K;
       mean = K + mean / (float)cpg;
-      for (int c = 0; c < cpg; ++c) M += fmaf(len * (e(c).x - mean), e(c).x - mean, e(c).y);
+      for (int c = 0; c < cpg; ++c) M += fmaf(len * (e[c].x - mean), e[c].x - mean, e[c].y);
       out(g, mean, M);
     }
   } else {
     const int lane = threadIdx.x & 31;
     for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
-      auto e = [&](int c) { return sm[pair_at(V, slab, g * cpg + c)]; };
-      const float K = e(0).x;
+      const float2* e = ch + g * cpg;
+      const float K = e[0].x;
       float mean = 0.f, M = 0.f;
-      for (int c = lane; c < cpg; c += 32) mean += e(c).x - K;
+      for (int c = lane; c < cpg; c += 32) mean += e[c].x - K;
       mean = K + warp_sum(mean) / (float)cpg;
-      for (int c = lane; c < cpg; c += 32) M += fmaf(len * (e(c).x - mean), e(c).x - mean, e(c).y);
+      for (int c = lane; c < cpg; c += 32) M += fmaf(len * (e[c].x - mean), e[c].x - mean, e[c].y);
       M = warp_sum(M);
       if (lane == 0) out(g, mean, M);
     }
@@ -376,32 +397,58 @@ DIT_DEV void activate(float (&v)[V], int act) {
 }
 
 // ---------------------------------------------------------------- forward, three launches
-// part[b, split, unit] = (mean, M2) of the unit's channels over the split.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 3) gn_sums_kernel(const __grid_constant__ GnParams P) {
-  extern __shared__ float2 sm[];  // [rows][slab * V], then cnt[rows]
-  start_next();
-  const int64_t b = blockIdx.x / P.splits;
-  const int split = blockIdx.x - b * P.splits;
-  const int64_t p0 = range_begin(P.pixels, P.splits, split), p1 = range_begin(P.pixels, P.splits, split + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+// Every channel's (mean, M2) over the block's `len` pixels, into ch.  drain(A)
+// runs the thread's pixels through A; ch and piv are [slab * V].
+template <typename T, int V, class Drain>
+DIT_DEV void block_moments(const GnParams& P, const Place& at, const T* x, int len, float2* sm, float2* ch, float* piv,
+                           Drain drain) {
   Moments<V> A;
-  walk<T, V, kSumUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1], at.count,
-                         [&](int, const Raw<T, V>& r) {
-                           float v[V];
-                           unpack<T, V>(r, v);
-                           A.add(v);
-                         });
-  A.fold();
+  if (at.on && len > 0) {
+    const T* row0 = x + (at.p - at.row) * P.xs[1] + at.c;
+    A.pivot(row0, at.step * P.xs[1], (P.pixels - (at.p - at.row) + at.step - 1) / (unsigned)at.step);
+    if (at.row == 0)
+#pragma unroll
+      for (int i = 0; i < V; ++i) piv[at.run * V + i] = A.K[i];
+    drain(A);
+  }
+  const float n = (float)len, in = len > 0 ? 1.f / n : 0.f;
+  sum_rows<V>(at, A.s, A.q, sm, P.slab, P.part_lanes, [&](int c, float2 v) {
+    const float d = v.x * in;
+    ch[c] = make_float2(len > 0 ? piv[c] + d : 0.f, fmaf(-d, v.x, v.y));
+  });
+}
+
+// part[b, split, unit] = (mean, M2) of the unit's channels over the split.
+// Shared memory: the ring, sums [rows][slab * V + 1], ch [slab * V] float2,
+// piv [slab * V].
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_sums_kernel(const __grid_constant__ GnParams P) {
+  extern __shared__ float4 raw_sm[];
+  using F = Feed1<T, V, false>;
+  float2* sm = reinterpret_cast<float2*>(reinterpret_cast<char*>(raw_sm) + F::kBytes);
+  start_next();
+  const uint32_t b = blockIdx.x / (uint32_t)P.splits, split = blockIdx.x - b * P.splits;
+  const Place at(P, V, blockIdx.y, split, P.splits);
+  const T* x = static_cast<const T*>(P.x) + b * P.xs[0];
+  F feed;
+  feed.from(0, x + at.p * P.xs[1] + at.c, at.step * P.xs[1]);
+  feed.start(raw_sm, at.count);
+  const int len = share_pixels(P, at.rows, split, P.splits);
   const int width = P.slab * V, c0 = blockIdx.y * width;
-  join_rows<V>(at, A, sm, reinterpret_cast<float*>(sm + at.rows * width), P.slab);
+  float2* ch = sm + at.rows * (width + 1);
+  block_moments<T, V>(P, at, x, len, sm, ch, reinterpret_cast<float*>(ch + width), [&](Moments<V>& A) {
+    feed.run([&](int, const Raw<T, V>(&r)[1]) {
+      float v[V];
+      unpack<T, V>(r[0], v);
+      A.add(v);
+    });
+  });
   const int here = min(width, P.channels - c0);
-  float2* part = P.part + ((b * P.splits + split) * P.channels + c0) / P.unit;
+  float2* part = P.part + ((int64_t)blockIdx.x * P.channels + c0) / P.unit;
   if (P.unit == 1) {
-    for (int c = threadIdx.x; c < here; c += kThreads) part[c] = sm[pair_at(V, P.slab, c)];
+    for (int c = threadIdx.x; c < here; c += kThreads) part[c] = ch[c];
   } else {
-    join_channels<V>(sm, P.slab, here / P.cpg, P.cpg, (float)(p1 - p0),
-                     [&](int g, float mean, float M) { part[g] = make_float2(mean, M); });
+    join_channels(ch, here / P.cpg, P.cpg, (float)len, [&](int g, float mean, float M) { part[g] = make_float2(mean, M); });
   }
 }
 
@@ -426,18 +473,19 @@ constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads) gn_join_kernel(const __grid_constant__ GnParams P) {
   __shared__ Joint sm[kJoinThreads / 32];
   start_next();
-  const int64_t b = blockIdx.x / P.groups;
+  const uint32_t b = blockIdx.x / (uint32_t)P.groups;
   const int g = blockIdx.x - b * P.groups;
   const int per = P.cpg / P.unit, stride = P.channels / P.unit;
-  const float2* part = P.part + b * P.splits * stride + (int64_t)g * per;
+  const float2* part = P.part + (int64_t)b * P.splits * stride + (int64_t)g * per;
   const int64_t entries = (int64_t)P.splits * per;
+  const int rows = kThreads / (unsigned)P.slab;
   Joint J{0.f, 0.f, 0.f};
   wait_previous();
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < entries; i += kJoinThreads) {
     const int s = per == 1 ? (int)i : (int)(i / per);
     const float2 e = part[(int64_t)s * stride + (i - (int64_t)s * per)];
-    J.take((float)(range_begin(P.pixels, P.splits, s + 1) - range_begin(P.pixels, P.splits, s)) * (float)P.unit, e.x, e.y);
+    J.take((float)share_pixels(P, rows, s, P.splits) * (float)P.unit, e.x, e.y);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -454,30 +502,74 @@ __global__ void __launch_bounds__(kJoinThreads) gn_join_kernel(const __grid_cons
   }
 }
 
+// `lanes` (a power of two) neighbouring threads join one group's partials of a
+// batch element: stat[g] = (mean, rstd) of the slab's groups.
+DIT_DEV void fold_groups(const GnParams& P, uint32_t b, int g0, int groups, float2* stat, int rows, bool write) {
+  int lanes = 1;
+  while (lanes < 32 && 2 * lanes * groups <= kThreads) lanes *= 2;
+  const int t = threadIdx.x & (lanes - 1), per = kThreads / (unsigned)lanes;
+  const float2* part = P.part + (int64_t)b * P.splits * P.groups + g0;
+  for (int base = 0; base < groups; base += per) {
+    const int g = base + threadIdx.x / (unsigned)lanes;
+    Joint J{0.f, 0.f, 0.f};
+    if (g < groups) {
+#pragma unroll 4
+      for (int s = t; s < P.splits; s += lanes) {
+        const float2 e = part[(int64_t)s * P.groups + g];
+        J.take((float)share_pixels(P, rows, s, P.splits) * (float)P.cpg, e.x, e.y);
+      }
+    }
+    for (int o = lanes >> 1; o; o >>= 1) {
+      const float n = __shfl_down_sync(0xFFFFFFFFu, J.n, o), m = __shfl_down_sync(0xFFFFFFFFu, J.mean, o);
+      const float M = __shfl_down_sync(0xFFFFFFFFu, J.M, o);
+      if (t + o < lanes) J.take(n, m, M);
+    }
+    if (t == 0 && g < groups) {
+      const float rstd = rstd_of(J.n > 0.f ? J.M / J.n : 0.f, P.eps);
+      stat[g] = make_float2(J.mean, rstd);
+      if (write) {
+        const int64_t bg = (int64_t)b * P.groups + g0 + g;
+        if (P.mean_out) P.mean_out[bg] = J.mean;
+        if (P.rstd_out) P.rstd_out[bg] = rstd;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Shared memory: the ring, then stat [groups of the slab] float2 (P.fold).
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4) gn_apply_kernel(const __grid_constant__ GnParams P) {
-  // backwards: the ranges that the sums read last first
-  const int64_t at_block = gridDim.x - 1 - blockIdx.x;
-  const int64_t b = at_block / P.passes;
-  const int split = at_block - b * P.passes;
-  const int64_t p0 = range_begin(P.pixels, P.passes, split), p1 = range_begin(P.pixels, P.passes, split + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+__global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_apply_kernel(const __grid_constant__ GnParams P) {
+  extern __shared__ float4 raw_sm[];
+  using F = Feed1<T, V, true>;
+  float2* stat = reinterpret_cast<float2*>(reinterpret_cast<char*>(raw_sm) + F::kBytes);
+  const uint32_t b = blockIdx.x / (uint32_t)P.passes, share = blockIdx.x - b * P.passes;
+  const Place at(P, V, blockIdx.y, share, P.passes);
+  // backwards: what the sums read last first.  x is nobody's output, so its
+  // loads need not wait for the sums.
+  const int64_t last = at.p + (int64_t)(at.count - 1) * at.step, ystep = -at.step * P.os[1];
+  F feed;
+  feed.from(0, static_cast<const T*>(P.x) + b * P.xs[0] + last * P.xs[1] + at.c, -at.step * P.xs[1]);
+  feed.start(raw_sm, at.count);
   Affine<V> f;
   if (at.on) f.weights(P, at.c);
   wait_previous();
-  if (!at.on) return;
-  f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[b * P.groups + g], P.rstd[b * P.groups + g]); });
-  T* y = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
-  const int64_t ystep = at.rows * P.os[1];
-  walk<T, V, kPassUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1], at.count,
-                          [&](int, const Raw<T, V>& r) {
-                            float v[V];
-                            unpack<T, V>(r, v);
-                            f.z(v);
-                            activate(v, P.act);
-                            store_f32<T, V>(y, v);
-                            y += ystep;
-                          });
+  if (P.fold) {
+    const int width = P.slab * V, c0 = blockIdx.y * width, g0 = c0 / P.cpg, groups = min(width, P.channels - c0) / P.cpg;
+    fold_groups(P, b, g0, groups, stat, at.rows, share == 0);
+    if (at.on) f.statistics(at.c, P.cpg, [&](int g) { return stat[g - g0]; });
+  } else if (at.on) {
+    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[(int64_t)b * P.groups + g], P.rstd[(int64_t)b * P.groups + g]); });
+  }
+  T* y = static_cast<T*>(P.out) + b * P.os[0] + last * P.os[1] + at.c;
+  feed.run([&](int, const Raw<T, V>(&r)[1]) {
+    float v[V];
+    unpack<T, V>(r[0], v);
+    f.z(v);
+    activate(v, P.act);
+    store_f32_stream<T, V>(y, v);
+    y += ystep;
+  });
 }
 
 // ---------------------------------------------------------------- forward, one launch
@@ -490,68 +582,68 @@ DIT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.ali
 DIT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 constexpr int kMaxCluster = 8;
 
+// All of a thread's pixels into its own places of shared memory, [i][thread]:
+// in the background where cp.async can (staged() waits), else batch by batch.
+template <typename T, int V>
+DIT_DEV void stage(T* mine, const T* x, int64_t step, int count) {
+  if constexpr (V * sizeof(T) == 16) {
+    for (int i = 0; i < count; ++i, x += step)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + i * (kThreads * V))), "l"(x) : "memory");
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < count; ++i, x += step) store_raw<T, V>(mine + i * (kThreads * V), load_raw<T, V>(x));
+  }
+}
+DIT_DEV void staged() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A cluster of `splits` blocks takes one slab (whole groups) of one batch
 // element; each block keeps its pixels in shared memory, every thread reading
 // back only what it wrote itself.
-// Shared memory: sums [rows][slab * V] float2, cnt[rows] padded to 256 floats,
-// own [groups of the slab] float2 (read by the cluster), stat likewise, data.
+// Shared memory: as gn_sums_kernel, then own [groups of the slab] float2 (read
+// by the cluster), stat likewise, data.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 2) gn_cluster_kernel(const __grid_constant__ GnParams P) {
   extern __shared__ float4 raw_sm[];
-  const int width = P.slab * V, rows = kThreads / P.slab, slab_groups = width / P.cpg;
+  const int width = P.slab * V, rows = kThreads / (unsigned)P.slab, slab_groups = width / P.cpg;
   float2* sm = reinterpret_cast<float2*>(raw_sm);
-  float* cnt = reinterpret_cast<float*>(sm + rows * width);
-  float2* own = reinterpret_cast<float2*>(cnt + kThreads);
+  float2* ch = sm + rows * (width + 1);
+  float2* own = ch + width + (width + 1) / 2;  // piv between
   float2* stat = own + slab_groups;
   T* data = reinterpret_cast<T*>(raw_sm) +
             ((reinterpret_cast<char*>(stat + slab_groups) - reinterpret_cast<char*>(raw_sm) + 15) / 16 * 16) / sizeof(T);
 
-  const int rank = blockIdx.x % P.splits;
-  const int64_t b = blockIdx.x / P.splits;
-  const int64_t p0 = range_begin(P.pixels, P.splits, rank), p1 = range_begin(P.pixels, P.splits, rank + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+  const uint32_t b = blockIdx.x / (uint32_t)P.splits;
+  const int rank = blockIdx.x - b * P.splits;
+  const Place at(P, V, blockIdx.y, rank, P.splits);
+  const int len = share_pixels(P, rows, rank, P.splits);
   T* mine = data + threadIdx.x * V;
-  Moments<V> A;
-  walk<T, V, kSumUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1], at.count,
-                         [&](int i, const Raw<T, V>& r) {
-                           float v[V];
-                           store_raw<T, V>(mine + i * (kThreads * V), r);
-                           unpack<T, V>(r, v);
-                           A.add(v);
-                         });
-  A.fold();
   Affine<V> f;
   if (at.on) f.weights(P, at.c);
-  join_rows<V>(at, A, sm, cnt, P.slab);
+  const T* x = static_cast<const T*>(P.x) + b * P.xs[0];
+  stage<T, V>(mine, x + at.p * P.xs[1] + at.c, at.step * P.xs[1], at.count);
+  block_moments<T, V>(P, at, x, len, sm, ch, reinterpret_cast<float*>(ch + width), [&](Moments<V>& A) {
+    staged();
+#pragma unroll 4
+    for (int i = 0; i < at.count; ++i) {
+      float v[V];
+      unpack<T, V>(load_raw<T, V>(mine + i * (kThreads * V)), v);
+      A.add(v);
+    }
+  });
   const int c0 = blockIdx.y * width, groups = min(width, P.channels - c0) / P.cpg, g0 = c0 / P.cpg;
-  join_channels<V>(sm, P.slab, groups, P.cpg, (float)(p1 - p0),
-                   [&](int g, float mean, float M) { own[g] = make_float2(mean, M); });
+  join_channels(ch, groups, P.cpg, (float)len, [&](int g, float mean, float M) { own[g] = make_float2(mean, M); });
   cluster_arrive();
   cluster_wait();
-  const float total = (float)P.pixels * (float)P.cpg;
   for (int g = threadIdx.x; g < groups; g += kThreads) {
     float2 e[kMaxCluster];
-    float n[kMaxCluster], mean = 0.f, M = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      e[r] = make_float2(0.f, 0.f);
-      n[r] = 0.f;
-      if (r >= P.splits) continue;
-      e[r] = ld_cluster_f2(cluster_map(own + g, r));
-      n[r] = (float)(range_begin(P.pixels, P.splits, r + 1) - range_begin(P.pixels, P.splits, r)) * (float)P.cpg;
-    }
-    // the last block always has pixels
-    float K = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) K = r == P.splits - 1 ? e[r].x : K;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      if (n[r] > 0.f) mean = fmaf(n[r], e[r].x - K, mean);
-    mean = K + mean / total;
+      e[r] = r < P.splits ? ld_cluster_f2(cluster_map(own + g, r)) : make_float2(0.f, 0.f);
+    Joint J{0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      if (n[r] > 0.f) M += fmaf(n[r] * (e[r].x - mean), e[r].x - mean, e[r].y);
-    const float rstd = rstd_of(M / total, P.eps);
+      if (r < P.splits) J.take((float)share_pixels(P, rows, r, P.splits) * (float)P.cpg, e[r].x, e[r].y);
+    const float mean = J.mean, rstd = rstd_of(J.M / J.n, P.eps);
     stat[g] = make_float2(mean, rstd);
     if (rank == 0) {
       if (P.mean_out) P.mean_out[b * P.groups + g0 + g] = mean;
@@ -563,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_cluster_kernel(const __grid_co
   if (at.on) {
     f.statistics(at.c, P.cpg, [&](int g) { return stat[g - g0]; });
     T* y = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
-    const int64_t ystep = at.rows * P.os[1];
+    const int64_t ystep = at.step * P.os[1];
 #pragma unroll 4
     for (int i = 0; i < at.count; ++i) {
       float v[V];
@@ -619,38 +711,42 @@ struct GradSums {
   }
 };
 
-// part[b, split, c] = (sum dz, sum dz xhat) over the split's pixels.
+// part[b, split, c] = (sum dz, sum dz xhat) over the split's pixels.  Shared
+// memory: the ring, then sums [rows][slab * V + 1].
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 3) gn_grad_sums_kernel(const __grid_constant__ GnParams P) {
-  extern __shared__ float2 sm[];  // [rows][slab * V]
+__global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T)) < 4 ? stream_blocks(V * sizeof(T)) : 4) gn_grad_sums_kernel(const __grid_constant__ GnParams P) {
+  extern __shared__ float4 raw_sm[];
+  using F = Feed2<T, V, false>;
+  float2* sm = reinterpret_cast<float2*>(reinterpret_cast<char*>(raw_sm) + F::kBytes);
   start_next();
-  const int64_t b = blockIdx.x / P.splits;
-  const int split = blockIdx.x - b * P.splits;
-  const int64_t p0 = range_begin(P.pixels, P.splits, split), p1 = range_begin(P.pixels, P.splits, split + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+  const uint32_t b = blockIdx.x / (uint32_t)P.splits, split = blockIdx.x - b * P.splits;
+  const Place at(P, V, blockIdx.y, split, P.splits);
+  F feed;
+  feed.from(0, static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.step * P.xs[1]);
+  feed.from(1, static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.step * P.ds[1]);
+  feed.start(raw_sm, at.count);
   const int width = P.slab * V;
   Affine<V> f;
   GradSums<V> S;
   if (at.on) {
     f.weights(P, at.c);
-    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[b * P.groups + g], P.rstd[b * P.groups + g]); });
-    walk2<T, V, kGradUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1],
-                             static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.rows * P.ds[1],
-                             at.count, [&](int, const Raw<T, V>& rx, const Raw<T, V>& rg) {
-                               float v[V], g[V], xm[V], dz[V];
-                               unpack<T, V>(rx, v);
-                               unpack<T, V>(rg, g);
-                               dz_of(f, v, g, P.act, xm, dz);
-                               S.add(dz, xm);
-                             });
+    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[(int64_t)b * P.groups + g], P.rstd[(int64_t)b * P.groups + g]); });
+    feed.run([&](int, const Raw<T, V>(&r)[2]) {
+      float v[V], g[V], xm[V], dz[V];
+      unpack<T, V>(r[0], v);
+      unpack<T, V>(r[1], g);
+      dz_of(f, v, g, P.act, xm, dz);
+      S.add(dz, xm);
+    });
     float r[V];
-    spread(r, at.c, P.cpg, [&](int g) { return P.rstd[b * P.groups + g]; });
+    spread(r, at.c, P.cpg, [&](int g) { return P.rstd[(int64_t)b * P.groups + g]; });
     v_mul(S.B, S.B, r);
   }
-  add_rows<V>(at, S.A, S.B, sm, P.slab);
   const int c0 = blockIdx.y * width, here = min(width, P.channels - c0);
-  float2* part = P.part + (b * P.splits + split) * P.channels + c0;
-  for (int c = threadIdx.x; c < here; c += kThreads) part[c] = sm[pair_at(V, P.slab, c)];
+  float2* part = P.part + (int64_t)blockIdx.x * P.channels + c0;
+  sum_rows<V>(at, S.A, S.B, sm, P.slab, P.part_lanes, [&](int c, float2 v) {
+    if (c < here) part[c] = v;
+  });
 }
 
 DIT_DEV float block_sum(float v, float* sm) {
@@ -670,10 +766,10 @@ __global__ void __launch_bounds__(kThreads) gn_grad_join_kernel(const __grid_con
   __shared__ float2 sm[kThreads];
   __shared__ float sums[kThreads / 32];
   start_next();
-  const int64_t b = blockIdx.x / P.groups;
+  const uint32_t b = blockIdx.x / (uint32_t)P.groups;
   const int g = blockIdx.x - b * P.groups;
   const int rows = kThreads / cols, col = threadIdx.x % cols, row = threadIdx.x / cols;
-  const float2* part = P.part + b * P.splits * P.channels + (int64_t)g * P.cpg;
+  const float2* part = P.part + (int64_t)b * P.splits * P.channels + (int64_t)g * P.cpg;
   float s1 = 0.f, s2 = 0.f;
   wait_previous();
   for (int c0 = 0; c0 < P.cpg; c0 += cols) {
@@ -696,7 +792,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_join_kernel(const __grid_con
     }
     if (row == 0 && c0 + col < P.cpg) {
       const int c = g * P.cpg + c0 + col;
-      P.chan[b * P.channels + c] = make_float2(A, B);
+      P.chan[(int64_t)b * P.channels + c] = make_float2(A, B);
       const float w = P.w ? P.w[c] : 1.f;
       s1 = fmaf(w, A, s1), s2 = fmaf(w, B, s2);
     }
@@ -748,89 +844,91 @@ struct GradApply {
   }
 };
 
-// dx; the blocks behind the last pixel range sum the channels over the batch.
+// dx; the blocks behind the last share sum the channels over the batch.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 3) gn_grad_apply_kernel(const __grid_constant__ GnParams P) {
-  const int64_t work = P.batch * P.passes;
+__global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T)) < 4 ? stream_blocks(V * sizeof(T)) : 4) gn_grad_apply_kernel(const __grid_constant__ GnParams P) {
+  extern __shared__ float4 raw_sm[];
+  using F = Feed2<T, V, true>;
+  const uint32_t work = (uint32_t)P.batch * P.passes;
   if (blockIdx.x >= work) {
     wait_previous();
     if (blockIdx.y == 0) grad_weights(P, (int)(blockIdx.x - work) * kThreads + threadIdx.x);
     return;
   }
-  const int64_t at_block = work - 1 - blockIdx.x;
-  const int64_t b = at_block / P.passes;
-  const int split = at_block - b * P.passes;
-  const int64_t p0 = range_begin(P.pixels, P.passes, split), p1 = range_begin(P.pixels, P.passes, split + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+  const uint32_t b = blockIdx.x / (uint32_t)P.passes, share = blockIdx.x - b * P.passes;
+  const Place at(P, V, blockIdx.y, share, P.passes);
+  // backwards, as gn_apply_kernel
+  const int64_t last = at.p + (int64_t)(at.count - 1) * at.step, ostep = -at.step * P.os[1];
+  F feed;
+  feed.from(0, static_cast<const T*>(P.x) + b * P.xs[0] + last * P.xs[1] + at.c, -at.step * P.xs[1]);
+  feed.from(1, static_cast<const T*>(P.dy) + b * P.ds[0] + last * P.ds[1] + at.c, -at.step * P.ds[1]);
+  feed.start(raw_sm, at.count);
   Affine<V> f;
   GradApply<V> h;
   if (at.on) {
     f.weights(P, at.c);
-    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[b * P.groups + g], P.rstd[b * P.groups + g]); });
+    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[(int64_t)b * P.groups + g], P.rstd[(int64_t)b * P.groups + g]); });
   }
   wait_previous();
   if (!at.on) return;
   h.set(at.c, P.cpg, [&](int g) {
-    const float2 s = P.gsum[b * P.groups + g];
-    return make_float3(P.rstd[b * P.groups + g], s.x, s.y);
+    const float2 s = P.gsum[(int64_t)b * P.groups + g];
+    return make_float3(P.rstd[(int64_t)b * P.groups + g], s.x, s.y);
   });
-  T* out = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
-  const int64_t ostep = at.rows * P.os[1];
-  walk2<T, V, kGradUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1],
-                           static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.rows * P.ds[1],
-                           at.count, [&](int, const Raw<T, V>& rx, const Raw<T, V>& rg) {
-                             float v[V], g[V], xm[V], dz[V];
-                             unpack<T, V>(rx, v);
-                             unpack<T, V>(rg, g);
-                             dz_of(f, v, g, P.act, xm, dz);
-                             h.dx(f, xm, dz);
-                             store_f32<T, V>(out, dz);
-                             out += ostep;
-                           });
+  T* out = static_cast<T*>(P.out) + b * P.os[0] + last * P.os[1] + at.c;
+  feed.run([&](int, const Raw<T, V>(&r)[2]) {
+    float v[V], g[V], xm[V], dz[V];
+    unpack<T, V>(r[0], v);
+    unpack<T, V>(r[1], g);
+    dz_of(f, v, g, P.act, xm, dz);
+    h.dx(f, xm, dz);
+    store_f32_stream<T, V>(out, dz);
+    out += ostep;
+  });
 }
 
 // One launch, as gn_cluster_kernel: x and dy stay in shared memory between
 // the sums and dx.  With one batch element the channel sums are dw and db.
-// Shared memory: sums [rows][slab * V] float2 (row 0 read by the cluster),
-// chan[slab * V] float2, group sums [groups of the slab] float2, x, dy.
+// Shared memory: sums [rows][slab * V + 1] float2, own [slab * V] float2 (read
+// by the cluster), chan likewise, group sums [groups of the slab] float2, x, dy.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __grid_constant__ GnParams P, int data_elems) {
   extern __shared__ float4 raw_sm[];
   start_next();
-  const int width = P.slab * V, rows = kThreads / P.slab, slab_groups = width / P.cpg;
+  const int width = P.slab * V, rows = kThreads / (unsigned)P.slab, slab_groups = width / P.cpg;
   float2* sm = reinterpret_cast<float2*>(raw_sm);
-  float2* chan = sm + rows * width;
+  float2* own = sm + rows * (width + 1);
+  float2* chan = own + width;
   float2* gs = chan + width;
   T* data = reinterpret_cast<T*>(raw_sm) +
             ((reinterpret_cast<char*>(gs + slab_groups) - reinterpret_cast<char*>(raw_sm) + 15) / 16 * 16) / sizeof(T);
 
-  const int rank = blockIdx.x % P.splits;
-  const int64_t b = blockIdx.x / P.splits;
-  const int64_t p0 = range_begin(P.pixels, P.splits, rank), p1 = range_begin(P.pixels, P.splits, rank + 1);
-  const Place at(P, V, blockIdx.y, p0, p1);
+  const uint32_t b = blockIdx.x / (uint32_t)P.splits;
+  const int rank = blockIdx.x - b * P.splits;
+  const Place at(P, V, blockIdx.y, rank, P.splits);
   T* xm_ = data + threadIdx.x * V;
   T* gm_ = xm_ + data_elems;
+  stage<T, V>(xm_, static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.step * P.xs[1], at.count);
+  stage<T, V>(gm_, static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.step * P.ds[1], at.count);
   Affine<V> f;
   GradSums<V> S;
   if (at.on) {
     f.weights(P, at.c);
     f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[b * P.groups + g], P.rstd[b * P.groups + g]); });
-    walk2<T, V, kGradUnroll>(static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.rows * P.xs[1],
-                             static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.rows * P.ds[1],
-                             at.count, [&](int i, const Raw<T, V>& rx, const Raw<T, V>& rg) {
-                               float v[V], g[V], xm[V], dz[V];
-                               store_raw<T, V>(xm_ + i * (kThreads * V), rx);
-                               store_raw<T, V>(gm_ + i * (kThreads * V), rg);
-                               unpack<T, V>(rx, v);
-                               unpack<T, V>(rg, g);
-                               dz_of(f, v, g, P.act, xm, dz);
-                               S.add(dz, xm);
-                             });
+    staged();
+#pragma unroll 2
+    for (int i = 0; i < at.count; ++i) {
+      float v[V], g[V], xm[V], dz[V];
+      unpack<T, V>(load_raw<T, V>(xm_ + i * (kThreads * V)), v);
+      unpack<T, V>(load_raw<T, V>(gm_ + i * (kThreads * V)), g);
+      dz_of(f, v, g, P.act, xm, dz);
+      S.add(dz, xm);
+    }
     float r[V];
     spread(r, at.c, P.cpg, [&](int g) { return P.rstd[b * P.groups + g]; });
     v_mul(S.B, S.B, r);
   }
-  add_rows<V>(at, S.A, S.B, sm, P.slab);
+  sum_rows<V>(at, S.A, S.B, sm, P.slab, P.part_lanes, [&](int c, float2 v) { own[c] = v; });
   cluster_arrive();
   cluster_wait();
   const int c0 = blockIdx.y * width, here = min(width, P.channels - c0), groups = here / P.cpg, g0 = c0 / P.cpg;
@@ -839,11 +937,11 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       if (r >= P.splits) continue;
-      const float2 e = ld_cluster_f2(cluster_map(sm + pair_at(V, P.slab, c), r));
+      const float2 e = ld_cluster_f2(cluster_map(own + c, r));
       A += e.x, B += e.y;
     }
     if (rank == 0) {
-      if (P.chan) P.chan[b * P.channels + c0 + c] = make_float2(A, B);
+      if (P.chan) P.chan[(int64_t)b * P.channels + c0 + c] = make_float2(A, B);
       else {
         if (P.db) P.db[c0 + c] = A;
         if (P.dw) P.dw[c0 + c] = B;
@@ -875,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
     GradApply<V> h;
     h.set(at.c, P.cpg, [&](int g) { return make_float3(P.rstd[b * P.groups + g], gs[g - g0].x, gs[g - g0].y); });
     T* out = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
-    const int64_t ostep = at.rows * P.os[1];
+    const int64_t ostep = at.step * P.os[1];
 #pragma unroll 2
     for (int i = 0; i < at.count; ++i) {
       float v[V], g[V], xm[V], dz[V];
@@ -909,7 +1007,8 @@ int vec_of(const dit_group_norm_args& a) {
 
 struct Plan {
   bool cluster;
-  int vec, slab, nslab, splits, passes, unit;
+  int vec, slab, nslab, unit, splits, passes;
+  bool fold;
   int data_elems;  // cluster form: elements of one staged tensor
   size_t smem;
 };
@@ -920,12 +1019,10 @@ constexpr int64_t kSmemMost = 200 << 10;
 
 size_t scratch_bytes(const Plan& p, int cpg, bool backward) {
   const int rows = kThreads / p.slab, width = p.slab * p.vec;
-  size_t n = (size_t)rows * width * 8;
-  if (p.cluster) {
-    n += backward ? (size_t)width * 8 + (size_t)(width / cpg) * 8 : kThreads * 4 + (size_t)(width / cpg) * 16;
-    return (n + 15) / 16 * 16;
-  }
-  return n + (backward ? 0 : kThreads * 4);
+  size_t n = (size_t)rows * (width + 1) * 8;                          // sums
+  if (!backward) n += (size_t)width * 8 + (size_t)((width + 1) / 2) * 8;  // ch, piv
+  if (p.cluster) n += backward ? (size_t)width * 16 + (size_t)(width / cpg) * 8 : (size_t)(width / cpg) * 16;
+  return (n + 15) / 16 * 16;
 }
 
 // The three-launch form.
@@ -943,18 +1040,21 @@ Plan split_plan(const dit_group_norm_args& a, int vec, bool backward) {
   }
   p.unit = !backward && whole <= kThreads ? cpg : 1;
   const int rows = kThreads / p.slab;
-  // pixel ranges: one wave of three blocks an SM, fewer where a thread would
-  // have less than one batch of loads, more where it would sum over too many
-  // pixels in a row for fp32 (the forward's sums are folded, the gradient's not)
-  const int64_t each = a.batch * p.nslab;
-  int64_t splits = 456 / each, most = a.pixels / ((int64_t)rows * kPassUnroll),
-          least = ceil_div(a.pixels, (int64_t)rows * (backward ? 128 : 1024));
-  if (splits > most) splits = most;
-  if (splits < least) splits = least;
-  p.splits = (int)(splits < 1 ? 1 : splits);
-  int64_t passes = (backward ? 912 : 1216) / each;
-  if (passes > most) passes = most;
-  p.passes = (int)(passes < 1 ? 1 : passes);
+  // shares of a batch element: one wave of blocks, fewer where a thread would
+  // have less than four pixels, more where it would sum over too many in a row
+  // for fp32
+  const int64_t each = a.batch * p.nslab, most = a.pixels / ((int64_t)rows * 4);
+  auto shares = [&](int blocks, int64_t least) {
+    int64_t n = blocks / each;
+    if (n > most) n = most;
+    if (n < least) n = least;
+    return (int)(n < 1 ? 1 : n);
+  };
+  const int wave = 152 * stream_blocks(vec * elem_bytes(a.dtype));
+  p.splits = shares(wave, ceil_div(a.pixels, (int64_t)rows * (backward ? 128 : 256)));
+  p.passes = shares(wave, 1);
+  // few enough partials that every block of the pass joins its groups' itself
+  p.fold = p.unit == cpg && (int64_t)p.splits * (p.slab * vec / cpg) <= 2048;
   p.smem = scratch_bytes(p, cpg, backward);
   return p;
 }
@@ -966,10 +1066,10 @@ Plan cluster_plan(const dit_group_norm_args& a, int vec, int slab, int blocks, b
   p.vec = vec;
   p.slab = slab;
   p.nslab = (int)ceil_div(a.channels / vec, slab);
-  p.splits = blocks;
+  p.splits = blocks;  // a cluster's last blocks may have no pixels
   p.unit = a.channels / a.groups;
   const int rows = kThreads / slab;
-  const int64_t iters = ceil_div(ceil_div(a.pixels, blocks), rows);
+  const int64_t iters = ceil_div(a.pixels, (int64_t)blocks * rows);
   const int64_t data = iters * kThreads * vec * elem_bytes(a.dtype);
   if (data > kSmemMost) return p;
   const size_t smem = scratch_bytes(p, p.unit, backward) + (size_t)data * (backward ? 2 : 1);
@@ -979,15 +1079,29 @@ Plan cluster_plan(const dit_group_norm_args& a, int vec, int slab, int blocks, b
   return p;
 }
 
+// The one-launch form where its blocks have little to do each: slabs of whole
+// groups, at least 32 bytes of a pixel, no more of them than fill the SMs twice;
+// pixels cut over a cluster until a thread has two (one wave) or eight of them
+// (two waves).  Measured (bf16, us, one launch / three): 64 pixels x 320
+// channels 5.1 / 7.7, 2 x 256 x 512 5.7 / 7.7, 4096 x 512 8.6 / 11.1, 8 x 1024 x
+// 320 8.6 / 11.6, 4096 x 1024 10.4 / 13.5; with 16 pixels a thread 16384 x 128
+// 10.1 / 9.3, 16 x 4096 x 128 13.4 / 13.0.  Gradient: 64 x 320 5.8 / 9.0, 4096 x
+// 512 11.1 / 12.3, 4096 x 1024 13.4 / 18.5; with a batch, whose weight sums take
+// a second launch, 32 x 64 x 1280 at six pixels 13.1 / 16.2, 4 x 4096 x 256 at
+// eight 15.6 / 14.6, so six is the limit there.
 Plan plan_of(const dit_group_norm_args& a, int vec, bool backward) {
-  if (getenv("GN_CLUSTER")) {  // EXPERIMENT
-    int slab, blocks;
-    sscanf(getenv("GN_CLUSTER"), "%d,%d", &slab, &blocks);
-    const int cpg = a.channels / a.groups, whole = cpg / gcd(cpg, vec);
-    slab = (slab + whole - 1) / whole * whole;
-    if (slab > a.channels / vec) slab = a.channels / vec;
-    if (slab <= kThreads && a.pixels) {
-      Plan p = cluster_plan(a, vec, slab, blocks, backward);
+  const int cpg = a.channels / a.groups, runs = a.channels / vec, whole = cpg / gcd(cpg, vec);
+  const int run_bytes = vec * elem_bytes(a.dtype);
+  if (a.pixels && whole <= kThreads) {
+    int slab = whole;
+    auto slabs = [&] { return a.batch * ceil_div(runs, slab); };
+    while (2 * slab <= kThreads && slab < runs && (slab * run_bytes < 32 || slabs() > 304)) slab *= 2;
+    int blocks = 1;
+    auto pixels = [&] { return ceil_div(a.pixels, (int64_t)blocks * (kThreads / slab)); };
+    while (blocks < kMaxCluster && ((pixels() > 2 && 2 * blocks * slabs() <= 152) || (pixels() > 8 && 2 * blocks * slabs() <= 304)))
+      blocks *= 2;
+    if (blocks * slabs() <= 304 && pixels() <= (backward && a.batch > 1 ? 6 : 8)) {
+      const Plan p = cluster_plan(a, vec, slab, blocks, backward);
       if (p.smem) return p;
     }
   }
@@ -1022,16 +1136,17 @@ cudaError_t run(const dit_group_norm_args& a, const Plan& pl, const GnParams& P,
     GN_TRY(launch_kernel(gn_grad_cluster_kernel<T, V>, grid, kThreads, pl.smem, s, pl.splits, false, P, pl.data_elems));
     return extra && a.batch > 1 ? launch_kernel(gn_grad_weights_kernel, dim3(extra), kThreads, 0, s, 1, true, P) : cudaSuccess;
   }
+  const size_t ring = Feed1<T, V, false>::kBytes, ring2 = Feed2<T, V, false>::kBytes;
   if (!backward) {
-    GN_TRY(launch_kernel(gn_sums_kernel<T, V>, grid, kThreads, pl.smem, s, 1, false, P));
-    GN_TRY(launch_kernel(gn_join_kernel, bg, kJoinThreads, 0, s, 1, true, P));
-    return a.pixels ? launch_kernel(gn_apply_kernel<T, V>, pass, kThreads, 0, s, 1, true, P) : cudaSuccess;
+    GN_TRY(launch_kernel(gn_sums_kernel<T, V>, grid, kThreads, ring + pl.smem, s, 1, false, P));
+    if (!pl.fold) GN_TRY(launch_kernel(gn_join_kernel, bg, kJoinThreads, 0, s, 1, true, P));
+    return launch_kernel(gn_apply_kernel<T, V>, pass, kThreads, ring + (pl.fold ? (size_t)pl.slab * V / P.cpg * 8 : 0), s, 1, true, P);
   }
   int cols = 1;
   while (cols < P.cpg && cols < 32) cols *= 2;
-  GN_TRY(launch_kernel(gn_grad_sums_kernel<T, V>, grid, kThreads, pl.smem, s, 1, false, P));
+  GN_TRY(launch_kernel(gn_grad_sums_kernel<T, V>, grid, kThreads, ring2 + pl.smem, s, 1, false, P));
   GN_TRY(launch_kernel(gn_grad_join_kernel, bg, kThreads, 0, s, 1, true, P, cols));
-  return launch_kernel(gn_grad_apply_kernel<T, V>, dim3(pass.x + extra, pass.y), kThreads, 0, s, 1, true, P);
+  return launch_kernel(gn_grad_apply_kernel<T, V>, dim3(pass.x + extra, pass.y), kThreads, ring2, s, 1, true, P);
 }
 
 template <typename T>
@@ -1072,14 +1187,16 @@ cudaError_t group_norm_run(const dit_group_norm_args& a, bool backward, float* w
   P.out = a.out;
   for (int i = 0; i < 2; ++i) P.xs[i] = a.x_stride[i], P.ds[i] = a.dy_stride[i], P.os[i] = a.out_stride[i];
   P.batch = a.batch;
-  P.pixels = a.pixels;
+  P.pixels = (int)a.pixels;
   P.channels = a.channels;
   P.groups = a.groups;
   P.cpg = a.channels / a.groups;
   P.splits = pl.splits;
   P.passes = pl.passes;
   P.slab = pl.slab;
+  for (P.part_lanes = 1; P.part_lanes < 32 && 2 * P.part_lanes * pl.slab * pl.vec <= kThreads; P.part_lanes *= 2) {}
   P.unit = pl.unit;
+  P.fold = pl.fold;
   P.act = a.act;
   P.eps = a.eps;
   P.w = a.weight;
@@ -1094,7 +1211,7 @@ cudaError_t group_norm_run(const dit_group_norm_args& a, bool backward, float* w
   if (!backward) {
     P.mean_out = a.mean;
     P.rstd_out = a.rstd;
-    if (!pl.cluster) {
+    if (!pl.cluster && !pl.fold) {
       if (!a.mean) P.mean_out = bg;
       if (!a.rstd) P.rstd_out = bg + a.batch * a.groups;
     }

@@ -284,6 +284,11 @@ GN_CASES = [
     ("f32", (1, 2, 3), 3, "none", True, 0, 0.0),
     ("f16", (1, 70001, 16), 4, "silu", True, 0, 0.0),
     ("bf16", (2, 40000, 48), 16, "silu", True, 0, 0.0),
+    ("bf16", (1, 5000, 2304), 32, "silu", True, 0, 0.0),        # several slabs of whole groups
+    ("bf16", (3, 2500, 96), 32, "silu", True, 5, 0.0),          # rows of any alignment, streamed
+    ("f16", (2, 9001, 66), 6, "none", True, 0, 0.0),            # rows of 4-byte alignment, streamed
+    ("f32", (1, 3001, 1100), 1, "silu", True, 0, 0.0),          # one group wider than a block
+    ("f32", (9, 4000, 32), 32, "silu", True, 0, 0.0),
 ]
 
 
