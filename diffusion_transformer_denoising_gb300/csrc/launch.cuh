@@ -12,6 +12,22 @@ namespace dit {
 DIT_DEV void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 DIT_DEV void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Clusters of up to 8 blocks (the portable limit): the two halves of the
+// cluster barrier, and reads of a peer's shared memory at a cluster_map address.
+constexpr int kMaxCluster = 8;
+DIT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+DIT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+DIT_DEV float ld_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+DIT_DEV float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // Launch on `s`; cluster > 1: blocks of a cluster along x; after: may start
 // before the previous kernel of the stream has ended (it has to wait_previous).
 template <class... Params, class... Args>

@@ -140,7 +140,7 @@ dit_status check_rope_shape(const dit_rope_args* a, bool backward) {
 }
 
 int64_t rope_workspace(const dit_rope_args& a) {
-  if (!a.q.dweight && !a.k.dweight) return 0;
+  if ((!a.q.dweight && !a.k.dweight) || a.batch * a.tokens == 0 || rope_one_cluster(a)) return 0;
   return (int64_t)kRopeGradBlocks * a.head_dim * sizeof(float);
 }
 

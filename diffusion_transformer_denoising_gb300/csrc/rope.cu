@@ -196,6 +196,7 @@ struct RopeSeg {
   int64_t xs[3], ds[3], os[3];
   const float* w;
   float* part;  // ROPE_NORM_GRAD: [blocks][head_dim] partial dweight, or NULL
+  float* dw;    // ROPE_NORM_GRAD on one cluster a tensor: dweight itself, or NULL
   int heads;
 };
 
@@ -204,7 +205,7 @@ struct RopeParams {
   const void* pos;
   int64_t ps[2];
   uint32_t tokens, rows;  // rows = batch * tokens
-  int d, half, n_axes, pos_f32, negate, split, group_log2;
+  int d, half, n_axes, pos_f32, negate, split, group_log2, one_cluster;
   int ends[DIT_ROPE_MAX_AXES];  // last pair + 1 of each axis
   float eps, inv_d;
   uint64_t turn[DIT_ROPE_MAX_HEAD_DIM / 2];
@@ -490,11 +491,12 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   }
 
   if constexpr (GRAD) {
-    // the block's dweight: groups in order, through shared memory
+    // the block's dweight: groups in order, through shared memory; then the
+    // cluster's, where the tensor's blocks are one
     start_next();
-    float* part = P.seg[blockIdx.z].part;
-    if (part) {
-      extern __shared__ float sm[];  // [groups][d]
+    float *part = P.seg[blockIdx.z].part, *dw = P.seg[blockIdx.z].dw;
+    extern __shared__ float sm[];  // [groups][d], then the block's [d]
+    if (part || dw) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[i / 2].y : da[i / 2].x;
@@ -502,11 +504,25 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
       }
       __syncthreads();
       const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+      float* own = sm + groups * P.d;
       for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
         float v = 0.f;
         for (uint32_t j = 0; j < groups; ++j) v += sm[j * P.d + ch];
-        part[block * P.d + ch] = v;
+        if (part) part[block * P.d + ch] = v;
+        else own[ch] = v;
       }
+    }
+    if (P.one_cluster) {
+      cluster_arrive();
+      cluster_wait();
+      if (dw && blockIdx.x == 0)
+        for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
+          float v = 0.f;
+          for (uint32_t r = 0; r < gridDim.x; ++r) v += ld_cluster_f1(cluster_map(sm + groups * P.d + ch, r));
+          dw[ch] = v;
+        }
+      cluster_arrive();
+      cluster_wait();  // a block's memory stays until it has been read
     }
   }
 }
@@ -568,9 +584,8 @@ int log2_ceil(int v) {
 
 template <class L, int MODE, int HU>
 cudaError_t launch(const RopeParams& P, dim3 grid, cudaStream_t s) {
-  const size_t sm = MODE == ROPE_NORM_GRAD ? (size_t)(kRopeThreads >> P.group_log2) * P.d * sizeof(float) : 0;
-  rope_kernel<L, MODE, HU><<<grid, kRopeThreads, sm, s>>>(P);
-  return cudaGetLastError();
+  const size_t sm = MODE == ROPE_NORM_GRAD ? (size_t)((kRopeThreads >> P.group_log2) + 1) * P.d * sizeof(float) : 0;
+  return launch_kernel(rope_kernel<L, MODE, HU>, grid, dim3(kRopeThreads), sm, s, P.one_cluster ? (int)grid.x : 1, false, P);
 }
 
 // HU rows in flight a group: 64 bytes of each lane (element accesses: 2 rows)
@@ -590,6 +605,14 @@ cudaError_t launch_layout(const RopeParams& P, int layout, int mode, dim3 grid, 
 }
 
 }  // namespace
+
+// At most 12 turns of a cluster of eight blocks with eight groups each: there one
+// launch takes as long as two (64 tokens x 3 heads 5.9 / 5.6 us, 256 x 3 8.1 /
+// 5.9; 512 x 3 12.4 / 7.2) and needs no workspace.
+bool rope_one_cluster(const dit_rope_args& a) {
+  const int64_t rows = a.batch * a.tokens, heads = a.q.heads > a.k.heads ? a.q.heads : a.k.heads;
+  return rows > 0 && (rows + 63) / 64 * heads <= 12;
+}
 
 cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cudaStream_t stream) {
   RopeParams P{};
@@ -613,7 +636,8 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
 
   const dit_rope_heads* h[2] = {&a.q, &a.k};
   int mode[2], layout[2], blocks[2] = {0, 0};
-  float* part[2] = {workspace, nullptr};
+  float* part[2] = {workspace, workspace};
+  bool joined[2] = {false, false};
   for (int i = 0; i < 2; ++i) {
     mode[i] = !h[i]->weight ? ROPE_TURN : backward ? ROPE_NORM_GRAD : ROPE_NORM;
     layout[i] = layout_of(a, *h[i], P.half);
@@ -657,8 +681,18 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       // at once, so few partials are left to join (two per SM: 115 us on the
       // 32760-token video gradient, 127 us with 1024 blocks a tensor)
       if (grad && nx * ny > 304 / nz) nx = 304 / nz / ny > 0 ? 304 / nz / ny : 1;
+      // few rows: a cluster of eight blocks a tensor joins the weight sums itself
+      if (grad && rope_one_cluster(a) && (h[first]->dweight || h[last]->dweight)) {
+        Q.one_cluster = 1;
+        ny = 1;
+        nx = kMaxCluster;
+        for (int i = first; i <= last; ++i) {
+          Q.seg[i - first].dw = h[i]->dweight;
+          joined[i] = true;
+        }
+      }
       for (int i = first; i <= last; ++i)
-        if (grad && h[i]->dweight) {
+        if (grad && h[i]->dweight && !joined[i]) {
           blocks[i] = (int)(nx * ny);
           if (i == 1) part[1] = part[0] + (int64_t)blocks[0] * P.d;
           Q.seg[i - first].part = part[i];
@@ -671,7 +705,7 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       if (e != cudaSuccess) return e;
     }
   }
-  float* dw[2] = {backward ? a.q.dweight : nullptr, backward ? a.k.dweight : nullptr};
+  float* dw[2] = {backward && !joined[0] ? a.q.dweight : nullptr, backward && !joined[1] ? a.k.dweight : nullptr};
   if (dw[0] || dw[1])
     return launch_kernel(rope_dweight_kernel, dim3((P.d + 31) / 32, 2), dim3(1024), 0, stream, 1, P.rows != 0, part[0],
                          blocks[0], dw[0], part[1], blocks[1], dw[1], P.d);

@@ -325,10 +325,10 @@ def dit_rope_backward(pos, dq_out, dq, dk_out=None, dk=None, *, axes, theta=1e4,
 
 
 def dit_rope_workspace_bytes(head_dim: int) -> int:
-    """Workspace of dit_rope_backward when weight gradients are wanted."""
+    """Workspace that is enough for any dit_rope_backward with weight gradients."""
     heads = (1, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 16, 32)
     none = (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
-    n = lib().dit_rope_workspace_bytes(_ROPE_ARGS.pack(1, 1, head_dim, DTYPE_F32, 0, 1, 0, 0, 0, 0, 1e4, 0.0, 0, 0, 0,
+    n = lib().dit_rope_workspace_bytes(_ROPE_ARGS.pack(1, 1 << 20, head_dim, DTYPE_F32, 0, 1, 0, 0, 0, 0, 1e4, 0.0, 0, 0, 0,
                                                        POS_I32, 0, *heads, *none))
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())

@@ -298,7 +298,7 @@ typedef struct {
 dit_status dit_rope_forward(const dit_rope_args* a, void* stream);
 /* out = the gradient of x; dweight = the gradient of the weight, summed over
  * batch, tokens and heads in fp32 (overwritten; all zero for no tokens).
- * Needs workspace when a dweight is wanted. */
+ * Needs workspace when a dweight is wanted, unless the rows are few. */
 dit_status dit_rope_backward(const dit_rope_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 /* Bytes dit_rope_backward needs (host-only query; pointers are read as
  * present or NULL only); -1 for arguments the call would refuse. */

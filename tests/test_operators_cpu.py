@@ -62,6 +62,7 @@ def test_rope_forward_refuses(L, kw, status):
 
 def test_rope_backward_refuses(L):
     g = dict(HEADS, dy=2048, ds=(512, 64, 32))
+    many = dict(batch=1, tokens=1 << 20)
     for q, ws, n in ((dict(g, dy=0), 0, 0),                                     # no gradient
                      (dict(g, x=0, weight=64), 0, 0),                           # the norm's gradient needs x
                      (dict(g, weight=0, dweight=64), 0, 0),                     # a gradient of no weight
@@ -69,12 +70,13 @@ def test_rope_backward_refuses(L):
                      (dict(g, weight=64, dweight=128), 1024, 16),               # too little
                      (dict(g, weight=64, dweight=128), 1032, 1 << 30)):         # not aligned
         with pytest.raises(dit.DitError) as e:
-            dit._check(L.dit_rope_backward(rope_args(q=q), ws, n, None))
+            dit._check(L.dit_rope_backward(rope_args(q=q, **many), ws, n, None))
         assert e.value.status == INVALID, e.value
     two = dict(g, weight=64, dweight=128)
     with pytest.raises(dit.DitError):
         dit._check(L.dit_rope_backward(rope_args(q=two, k=dict(two, out=16384)), 1024, 1 << 30, None))
     assert L.dit_rope_workspace_bytes(rope_args(q=dict(two, heads=-3))) == -1
+    assert L.dit_rope_workspace_bytes(rope_args(q=two)) == 0 < L.dit_rope_workspace_bytes(rope_args(q=two, **many))
 
 
 def gn_args(**kw):
