@@ -205,7 +205,9 @@ struct RopeParams {
   const void* pos;
   int64_t ps[2];
   uint32_t tokens, rows;  // rows = batch * tokens
-  int d, half, n_axes, pos_f32, negate, split, group_log2, one_cluster;
+  int d, half, n_axes, pos_f32, negate, split, one_cluster;
+  int slots;     // lanes of a row
+  int per_warp;  // rows a warp takes side by side, where lanes reduce; else 0
   int ends[DIT_ROPE_MAX_AXES];  // last pair + 1 of each axis
   float eps, inv_d;
   uint64_t turn[DIT_ROPE_MAX_HEAD_DIM / 2];
@@ -220,6 +222,33 @@ DIT_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); 
 
 template <int N>
 using Int = std::integral_constant<int, N>;
+
+// Each of N values summed over the group's `slots` lanes, for all of them:
+// lane l takes l + o while there is one, then all take the first lane's.  A power
+// of two needs no last step, lanes taking their partners' both ways.
+template <int N>
+DIT_DEV void group_sums(float (&v)[N], int lane, int slots) {
+  if ((slots & (slots - 1)) == 0) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      if (o >= slots) continue;
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+    }
+  } else {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      if (o >= slots) continue;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float t = __shfl_down_sync(0xFFFFFFFFu, v[j], o);
+        if (lane + o < slots) v[j] += t;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __shfl_sync(0xFFFFFFFFu, v[j], (threadIdx.x & 31) - lane);
+  }
+}
 
 // Two pairs turned; MIX: the first (tx) or second (ty) of them may be a pair
 // of channels that are not turned, which must not meet (0 * inf).
@@ -236,7 +265,7 @@ DIT_DEV void turn_pair(float2 a, float2 b, float2 k0, float2 k1, float2 k2, floa
 }
 
 // blockIdx.y of gridDim.y: a slice of q's heads and of k's; blockIdx.x strides
-// over tokens.  A group of 2^group_log2 lanes takes one token at a time: its
+// over tokens.  A group of `slots` lanes takes one token at a time: its
 // angles once, then the slice's heads in batches of HU rows, the next batch's
 // loads (of the next tensor or token, too) in flight while one is worked on.
 // A row's turn is ya = a k0 + b k1, yb = a k2 + b k3 with (k0, k1, k2, k3) =
@@ -247,10 +276,13 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   using T = typename L::Elem;
   constexpr int NP = L::NP, N2 = NP / 2;
   constexpr bool GRAD = MODE == ROPE_NORM_GRAD;
-  const int lanes = 1 << P.group_log2;
-  const int lane = threadIdx.x & (lanes - 1);
-  const uint32_t groups = kRopeThreads >> P.group_log2;
-  const int group = threadIdx.x >> P.group_log2;
+  // groups lie back to back in the block, or where they reduce in each warp; the
+  // lanes left over have no row
+  const int in = MODE == ROPE_TURN ? threadIdx.x : threadIdx.x & 31;
+  const int side = in / (unsigned)P.slots, lane = in - side * P.slots;
+  const uint32_t groups = MODE == ROPE_TURN ? kRopeThreads / (unsigned)P.slots : kRopeThreads / 32 * P.per_warp;
+  const bool spare = MODE == ROPE_TURN ? side >= (int)groups : side >= P.per_warp;
+  const uint32_t group = MODE == ROPE_TURN ? side : threadIdx.x / 32 * P.per_warp + side;
   const bool partial = 2 * P.half < P.d;
 
   L lay;
@@ -267,7 +299,7 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   // each tensor's weights of the pairs (a, b), as the lanes hold them
   __shared__ float2 weight[MODE == ROPE_TURN ? 1 : 2][MODE == ROPE_TURN ? 1 : DIT_ROPE_MAX_HEAD_DIM / 2];
   if constexpr (MODE != ROPE_TURN) {
-    if (group < 2 && P.seg[group].heads)
+    if (!spare && group < 2 && P.seg[group].heads)
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         if (lay.has(i))
@@ -301,7 +333,7 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   __shared__ int32_t where[NP][kRopeThreads];
   __shared__ float2 spin[NP][kRopeThreads];
   auto token = [&] {
-    ok = base + group < P.rows;
+    ok = !spare && base + group < P.rows;
     b = ok ? (base + group) / P.tokens : 0;
     t = ok ? base + group - b * P.tokens : 0;
     const int32_t* pos = static_cast<const int32_t*>(P.pos) + b * P.ps[0] + t * P.ps[1];
@@ -434,15 +466,8 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
         dot[j] = dt.x + dt.y;
       }
       if constexpr (MODE != ROPE_TURN) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          if (o >= lanes) continue;
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            ss[j] += __shfl_xor_sync(0xFFFFFFFFu, ss[j], o);
-            if constexpr (GRAD) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-          }
-        }
+        group_sums<N>(ss, lane, P.slots);
+        if constexpr (GRAD) group_sums<N>(dot, lane, P.slots);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const float r = rsqrtf(fmaf(ss[j], P.inv_d, P.eps));
@@ -499,6 +524,7 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
     if (part || dw) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
+        if (spare) continue;
         if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[i / 2].y : da[i / 2].x;
         if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = i & 1 ? db[i / 2].y : db[i / 2].x;
       }
@@ -576,15 +602,9 @@ RopeLayout layout_of(const dit_rope_args& a, const dit_rope_heads& h, int half) 
   return LAYOUT_ANY;
 }
 
-int log2_ceil(int v) {
-  int l = 0;
-  while ((1 << l) < v) ++l;
-  return l;
-}
-
 template <class L, int MODE, int HU>
 cudaError_t launch(const RopeParams& P, dim3 grid, cudaStream_t s) {
-  const size_t sm = MODE == ROPE_NORM_GRAD ? (size_t)((kRopeThreads >> P.group_log2) + 1) * P.d * sizeof(float) : 0;
+  const size_t sm = MODE == ROPE_NORM_GRAD ? (size_t)(kRopeThreads / 32 * P.per_warp + 1) * P.d * sizeof(float) : 0;
   return launch_kernel(rope_kernel<L, MODE, HU>, grid, dim3(kRopeThreads), sm, s, P.one_cluster ? (int)grid.x : 1, false, P);
 }
 
@@ -648,9 +668,16 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
     for (int first = 0; first < 2; first += together ? 2 : 1) {
       const int last = together ? 1 : first;
       RopeParams Q = P;
-      Q.group_log2 = 5;
       const int v = layout[first];
-      if (v) Q.group_log2 = log2_ceil(P.split ? P.half / v + (P.d - 2 * P.half + 2 * v - 1) / (2 * v) : P.d / v);
+      Q.slots = !v ? 32 : P.split ? P.half / v + (P.d - 2 * P.half + 2 * v - 1) / (2 * v) : P.d / v;
+      // lanes that reduce: a power of two unless the exact number lets a warp take
+      // more rows (20000 tokens x 24 heads, gradient: 72 channels 58 against 69
+      // us, but 96 channels 83 against 75, 160 channels 158 against 127)
+      int wide = 1;
+      while (wide < Q.slots) wide *= 2;
+      if (mode[first] != ROPE_TURN && 32 / wide == 32 / Q.slots) Q.slots = wide;
+      Q.per_warp = 32 / Q.slots;
+      const int groups = mode[first] == ROPE_TURN ? kRopeThreads / Q.slots : kRopeThreads / 32 * Q.per_warp;
       Q.negate = backward && mode[first] == ROPE_TURN;
       const int hmax = together && h[1]->heads > h[first]->heads ? h[1]->heads : h[first]->heads;
       if (!hmax) continue;
@@ -673,7 +700,7 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       // it takes to give every SM four blocks otherwise
       const bool grad = mode[first] == ROPE_NORM_GRAD;
       const int nz = grad && together ? 2 : 1;
-      int64_t nx = ((int64_t)P.rows + (kRopeThreads >> Q.group_log2) - 1) >> (8 - Q.group_log2);
+      int64_t nx = ((int64_t)P.rows + groups - 1) / groups;
       int64_t ny = (608 + nx * nz - 1) / (nx * nz);
       if (ny > hmax) ny = hmax;
       if (ny > 256) ny = 256;
