@@ -34,10 +34,10 @@ namespace dit {
 namespace {
 
 constexpr int kThreads = 256;
-// Blocks an SM of the kernels that stream a tensor: two, whose shared-memory
-// rings keep about 110 KB on its way; six where runs are shorter than 16 bytes
-// and loads go to registers.
-constexpr int stream_blocks(int run_bytes) { return run_bytes == 16 ? 2 : 6; }
+// Blocks an SM of the kernels that stream a tensor: two or four, whose
+// shared-memory rings keep about 110 KB on its way; six where runs are shorter
+// than 8 bytes and loads go to registers.
+constexpr int stream_blocks(int run_bytes) { return run_bytes == 16 ? 2 : run_bytes == 8 ? 4 : 6; }
 
 struct GnParams {
   const void* x;
@@ -155,17 +155,33 @@ DIT_DEV int share_pixels(const GnParams& P, int rows, int s, int shares) {
   return turns * rows + (left < 0 ? 0 : left < rows ? left : rows);
 }
 
+// B bytes (4, 8 or 16) to shared memory in the background.
+template <int B>
+DIT_DEV void async_copy(void* dst, const void* src) {
+  if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(B) : "memory");
+}
+template <int B>
+DIT_DEV void async_copy(void* dst, const void* src, uint64_t policy) {
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "l"(policy) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(B), "l"(policy) : "memory");
+}
+
 // A thread's pixels 0 .. count - 1 of N tensors, read ahead of their use: run(
-// body) calls body(i, raw[N]) for each.  Runs of 16 bytes come through a ring in
-// shared memory by cp.async, STAGES batches of U pixels, each thread filling and
-// reading its own slots only (no barriers, no registers held by what is on its
-// way); a slot is filled again one batch after its values were used.  Shorter
-// runs, which cp.async cannot move, are loaded into registers a batch ahead.
+// body) calls body(i, raw[N]) for each.  Runs of 16 or 8 bytes come through a ring
+// in shared memory by cp.async, STAGES batches of U pixels, each thread filling
+// and reading its own slots only (no barriers, no registers held by what is on
+// its way); a slot is filled again one batch after its values were used.
+// Shorter runs are loaded into registers a batch ahead: cp.async cannot move 2
+// bytes, and with 4 it measured 6 % slower than registers.
 // LAST: the data is not read again (first out of L2).
 template <typename T, int V, int N, int U, int STAGES, bool LAST>
 struct Feed {
   enum : int {
-    kRing = V * sizeof(T) == 16,
+    kRun = V * (int)sizeof(T),
+    kRing = kRun >= 8,
     kSlot = kRing ? kThreads * V : 0,  // elements of a slot of all threads
     kBytes = STAGES * U * N * kSlot * (int)sizeof(T)
   };
@@ -184,9 +200,9 @@ struct Feed {
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         if constexpr (kRing) {
-          if (some) copy16(ring + ((slot * U + u) * N + k) * kSlot, src[k]);
+          if (some) copy(ring + ((slot * U + u) * N + k) * kSlot, src[k]);
         } else {
-          if (some) reg[u * N + k] = LAST ? load_raw_stream<T, V>(src[k]) : load_raw<T, V>(src[k]);
+          if (some) reg[u * N + k] = load_raw<T, V>(src[k]);
         }
         src[k] += step[k];
       }
@@ -197,11 +213,9 @@ struct Feed {
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
   }
-  DIT_DEV void copy16(T* dst, const T* p) const {
-    if constexpr (LAST)
-      asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(p), "l"(policy) : "memory");
-    else
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(p) : "memory");
+  DIT_DEV void copy(T* dst, const T* p) const {
+    if constexpr (LAST) async_copy<kRun>(dst, p, policy);
+    else async_copy<kRun>(dst, p);
   }
   // the first loads on their way; `ring_` is the block's, kBytes of it
   DIT_DEV void start(void* ring_, int count_) {
@@ -242,9 +256,9 @@ struct Feed {
   }
 };
 template <typename T, int V, bool LAST>
-using Feed1 = Feed<T, V, 1, (V * sizeof(T) == 16 ? 2 : 8), 8, LAST>;
+using Feed1 = Feed<T, V, 1, (V * sizeof(T) >= 8 ? 2 : 8), 8, LAST>;
 template <typename T, int V, bool LAST>
-using Feed2 = Feed<T, V, 2, (V * sizeof(T) == 16 ? 1 : 8), 8, LAST>;
+using Feed2 = Feed<T, V, 2, (V * sizeof(T) >= 8 ? 1 : 8), 8, LAST>;
 
 // A thread's sums of x - K and (x - K)^2 per channel.
 template <int V>
@@ -273,20 +287,6 @@ struct Moments {
     v_fma(q, d, d, q);
   }
 };
-
-template <typename T, int V>
-DIT_DEV void store_raw(T* p, const Raw<T, V>& r) {
-  constexpr int B = Raw<T, V>::kBytes;
-  if constexpr (B >= 16) {
-#pragma unroll
-    for (int i = 0; i < B / 16; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
-  } else if constexpr (B == 4) {
-    *reinterpret_cast<uint32_t*>(p) = r.w[0];
-  } else {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
-  }
-}
 
 // Per-channel pairs of a block's rows in shared memory, [rows][V][slab] and a
 // pair of padding a row: neither the writers (runs next to each other) nor the
@@ -579,12 +579,11 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_app
 // in the background where cp.async can (staged() waits), else batch by batch.
 template <typename T, int V>
 DIT_DEV void stage(T* mine, const T* x, int64_t step, int count) {
-  if constexpr (V * sizeof(T) == 16) {
-    for (int i = 0; i < count; ++i, x += step)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + i * (kThreads * V))), "l"(x) : "memory");
+  if constexpr (V * sizeof(T) >= 4) {
+    for (int i = 0; i < count; ++i, x += step) async_copy<V * sizeof(T)>(mine + i * (kThreads * V), x);
   } else {
 #pragma unroll 4
-    for (int i = 0; i < count; ++i, x += step) store_raw<T, V>(mine + i * (kThreads * V), load_raw<T, V>(x));
+    for (int i = 0; i < count; ++i, x += step) mine[i * (kThreads * V)] = *x;
   }
 }
 DIT_DEV void staged() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -1010,10 +1009,10 @@ bool aligned(const void* p, const int64_t st[2], int elem, int to) {
   return !p || (((uintptr_t)p | (uintptr_t)(st[0] * elem) | (uintptr_t)(st[1] * elem)) & (to - 1)) == 0;
 }
 
-// Channels a thread takes: 16 bytes of them, or 4, or one.
+// Channels a thread takes: 16, 8 or 4 bytes of them, or one.
 int vec_of(const dit_group_norm_args& a) {
   const int e = elem_bytes(a.dtype);
-  for (int to : {16, 4})
+  for (int to : {16, 8, 4})
     if (a.channels % (to / e) == 0 && aligned(a.x, a.x_stride, e, to) && aligned(a.dy, a.dy_stride, e, to) &&
         aligned(a.out, a.out_stride, e, to))
       return to / e;
@@ -1178,6 +1177,7 @@ template <typename T>
 cudaError_t run_vec(const dit_group_norm_args& a, const Plan& pl, const GnParams& P, bool backward, cudaStream_t s) {
   constexpr int most = 16 / sizeof(T);
   if (pl.vec == most) return run<T, most>(a, pl, P, backward, s);
+  if (pl.vec == most / 2) return run<T, most / 2>(a, pl, P, backward, s);
   if constexpr (sizeof(T) == 2)
     if (pl.vec == 2) return run<T, 2>(a, pl, P, backward, s);
   return run<T, 1>(a, pl, P, backward, s);
@@ -1189,7 +1189,7 @@ int64_t group_norm_workspace(const dit_group_norm_args& a, bool backward) {
   if (a.batch == 0) return 0;
   // enough for any alignment of the tensors
   int64_t need = 0;
-  for (int vec : {16 / elem_bytes(a.dtype), 4 / elem_bytes(a.dtype), 1}) {
+  for (int vec : {16 / elem_bytes(a.dtype), 8 / elem_bytes(a.dtype), 4 / elem_bytes(a.dtype), 1}) {
     if (a.channels % vec) continue;
     const Plan p = plan_of(a, vec, backward);
     const int64_t n = part_bytes(a, p) + group_bytes(a, p) + chan_bytes(a, p, backward);

@@ -68,27 +68,6 @@ DIT_DEV Raw<T, N> load_raw(const T* p) {
   }
   return r;
 }
-// The same for data that is not read again (evict-first).
-template <typename T, int N>
-DIT_DEV Raw<T, N> load_raw_stream(const T* p) {
-  constexpr int B = Raw<T, N>::kBytes;
-  if constexpr (B == 2) {
-    return load_raw<T, N>(p);
-  } else {
-    Raw<T, N> r;
-    if constexpr (B >= 16) {
-#pragma unroll
-      for (int i = 0; i < B / 16; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
-      }
-    } else {
-      static_assert(B == 4);
-      r.w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-    }
-    return r;
-  }
-}
 template <typename T, int N>
 DIT_DEV Raw<T, N> zero_raw() {
   Raw<T, N> r;
@@ -129,7 +108,8 @@ DIT_DEV void store_f32(T* p, const float (&f)[N]) {
         else reinterpret_cast<uint4*>(p)[i] = v;
       }
     } else if constexpr (B == 8) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      if constexpr (STREAM) __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+      else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
       *reinterpret_cast<uint32_t*>(p) = w[0];
     }
