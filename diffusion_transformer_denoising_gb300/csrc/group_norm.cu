@@ -35,9 +35,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // Blocks an SM of the kernels that stream a tensor: two or four, whose
-// shared-memory rings keep about 110 KB on its way; six where runs are shorter
-// than 8 bytes and loads go to registers.
-constexpr int stream_blocks(int run_bytes) { return run_bytes == 16 ? 2 : run_bytes == 8 ? 4 : 6; }
+// shared-memory rings keep about 110 KB on its way; five or six where runs are
+// shorter than 8 bytes and loads go to registers.
+constexpr int stream_blocks(int run_bytes) { return run_bytes == 16 ? 2 : run_bytes == 8 ? 4 : run_bytes == 4 ? 5 : 6; }
 
 struct GnParams {
   const void* x;
@@ -182,6 +182,7 @@ struct Feed {
   enum : int {
     kRun = V * (int)sizeof(T),
     kRing = kRun >= 8,
+    kWhole = !kRing && (N == 1 || kRun == 2),  // instructions count there: whole batches go without checks
     kSlot = kRing ? kThreads * V : 0,  // elements of a slot of all threads
     kBytes = STAGES * U * N * kSlot * (int)sizeof(T)
   };
@@ -193,20 +194,25 @@ struct Feed {
   Raw<T, V> reg[kRing ? 1 : U * N];
 
   DIT_DEV void from(int k, const T* p, int64_t s) { src[k] = p, step[k] = s; }
-  DIT_DEV void fetch() {  // the next batch
+  DIT_DEV void fetch_one(int u) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool some = next + u < count;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if constexpr (kRing) {
-          if (some) copy(ring + ((slot * U + u) * N + k) * kSlot, src[k]);
-        } else {
-          if (some) reg[u * N + k] = load_raw<T, V>(src[k]);
-        }
-        src[k] += step[k];
-      }
+    for (int k = 0; k < N; ++k) {
+      const T* p = src[k] + u * step[k];
+      if constexpr (kRing) copy(ring + ((slot * U + u) * N + k) * kSlot, p);
+      else reg[u * N + k] = load_raw<T, V>(p);
     }
+  }
+  DIT_DEV void fetch() {  // the next batch
+    if (kWhole && next + U <= count) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) fetch_one(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < (kWhole ? U - 1 : U); ++u)
+        if (next + u < count) fetch_one(u);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) src[k] += U * step[k];
     next += U;
     if constexpr (kRing) {
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -249,16 +255,21 @@ struct Feed {
           for (int k = 0; k < N; ++k) r[u][k] = reg[u * N + k];
       }
       fetch();
+      if (kWhole && i + U <= count) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u < count) body(i + u, r[u]);
+        for (int u = 0; u < U; ++u) body(i + u, r[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < (kWhole ? U - 1 : U); ++u)
+          if (i + u < count) body(i + u, r[u]);
+      }
     }
   }
 };
 template <typename T, int V, bool LAST>
 using Feed1 = Feed<T, V, 1, (V * sizeof(T) >= 8 ? 2 : 8), 8, LAST>;
 template <typename T, int V, bool LAST>
-using Feed2 = Feed<T, V, 2, (V * sizeof(T) >= 8 ? 1 : 8), 8, LAST>;
+using Feed2 = Feed<T, V, 2, (V * sizeof(T) >= 8 ? 1 : V * sizeof(T) == 4 ? 4 : 8), 8, LAST>;
 
 // A thread's sums of x - K and (x - K)^2 per channel.
 template <int V>
