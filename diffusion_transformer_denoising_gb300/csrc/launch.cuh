@@ -28,7 +28,8 @@ DIT_DEV float2 ld_cluster_f2(uint32_t addr) {
   return v;
 }
 
-// Launch on `s`; cluster > 1: blocks of a cluster along x; after: may start
+// Launch on `s` (dynamic shared memory above 48 KB only for kernels without
+// static shared memory); cluster > 1: blocks of a cluster along x; after: may start
 // before the previous kernel of the stream has ended (it has to wait_previous).
 template <class... Params, class... Args>
 cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
@@ -52,7 +53,9 @@ cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size
     ++c.numAttrs;
   }
   if (smem > (48 << 10)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // one value for every call: another thread's smaller launch of the same
+    // kernel must not take the room away in between
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10);
     if (e != cudaSuccess) return e;
   }
   return cudaLaunchKernelEx(&c, kernel, Params(args)...);

@@ -60,6 +60,13 @@ dit_status check_in_place(const char* what, const void* in, const int64_t* is, c
   return DIT_OK;
 }
 
+// Strides of axes with one element say nothing, whatever a view gives for them.
+template <int N>
+void drop_unused(int64_t (&stride)[N], const int64_t* size) {
+  for (int i = 0; i < N; ++i)
+    if (size[i] <= 1) stride[i] = 0;
+}
+
 // The device that owns the tensors; made current for the call, and the
 // caller's put back afterwards.
 struct OnDevice {
@@ -193,7 +200,14 @@ dit_status rope_call(const dit_rope_args* a, bool backward, void* ws, int64_t ws
   }
   if (need) DIT_TRY(dev.add("workspace", ws));
   DIT_TRY(dev.enter());
-  CU_TRY(rope_run(*a, backward, static_cast<float*>(ws), stream));
+  dit_rope_args c = *a;
+  for (dit_rope_heads* h : {&c.q, &c.k}) {
+    const int64_t size[3] = {c.batch, c.tokens, h->heads};
+    drop_unused(h->x_stride, size);
+    drop_unused(h->dy_stride, size);
+    drop_unused(h->out_stride, size);
+  }
+  CU_TRY(rope_run(c, backward, static_cast<float*>(ws), stream));
   return DIT_OK;
 }
 
@@ -205,6 +219,7 @@ dit_status check_gn_shape(const dit_group_norm_args* a, bool backward) {
   if (a->groups <= 0 || a->channels % a->groups) return fail(DIT_ERR_SHAPE, "groups must divide channels");
   if (a->pixels > INT32_MAX || a->batch > (1 << 20) || a->batch * a->groups > INT32_MAX)
     return fail(DIT_ERR_SHAPE, "pixels must be below 2^31, batch at most 2^20, batch * groups below 2^31");
+  if (a->batch * a->pixels > ((int64_t)1 << 40) / a->channels) return fail(DIT_ERR_SHAPE, "more than 2^40 elements");
   if (a->dtype != DIT_DTYPE_F32 && a->dtype != DIT_DTYPE_BF16 && a->dtype != DIT_DTYPE_F16)
     return fail(DIT_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
   if (a->act != DIT_ACT_NONE && a->act != DIT_ACT_SILU) return fail(DIT_ERR_INVALID_ARG, "unknown act %d", a->act);
@@ -254,7 +269,11 @@ dit_status gn_call(const dit_group_norm_args* a, bool backward, void* ws, int64_
   if (need) DIT_TRY(dev.add("workspace", ws));
   if (dev.owner < 0) return DIT_OK;  // nothing to write
   DIT_TRY(dev.enter());
-  CU_TRY(group_norm_run(*a, backward, static_cast<float*>(ws), stream));
+  dit_group_norm_args c = *a;
+  drop_unused(c.x_stride, size);
+  drop_unused(c.dy_stride, size);
+  drop_unused(c.out_stride, size);
+  CU_TRY(group_norm_run(c, backward, static_cast<float*>(ws), stream));
   return DIT_OK;
 }
 

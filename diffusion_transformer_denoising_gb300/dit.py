@@ -211,9 +211,9 @@ def _param(name, t, shape):
     if t is None:
         return 0
     if t.dtype is not _torch.float32:
-        _refuse(DIT_ERR_INVALID_ARG, f"{name} must be float32")
+        _refuse(DIT_ERR_INVALID_ARG, f"{name}: weights and statistics must be float32")
     if t.shape != shape or not t.is_contiguous():
-        _refuse(DIT_ERR_SHAPE, f"{name} must be contiguous {list(shape)}")
+        _refuse(DIT_ERR_SHAPE, f"{name}: weights and statistics must be contiguous, here {list(shape)}")
     return t.data_ptr()
 
 
@@ -242,16 +242,25 @@ def _workspace(t, workspace, stream, need):
     return ws.data_ptr(), need, ws
 
 
-def _heads_view(name, t, shape, dtype):
-    """(pointer, batch, token and head strides) of a [batch, tokens, heads, head_dim] view."""
+def _bad_view(tag, t, shape, dtype):
     if t.shape != shape:
-        _refuse(DIT_ERR_SHAPE, f"{name} is {list(t.shape)}, not {list(shape)}")
+        _refuse(DIT_ERR_SHAPE, f"{tag} tensor is {list(t.shape)}, not {list(shape)}")
     if t.dtype is not dtype:
-        _refuse(DIT_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
-    sb, st, sh, sd = t.stride()
-    if sd != 1 and t.numel():
-        _refuse(DIT_ERR_SHAPE, f"{name}: the channels of a head must be contiguous")
+        _refuse(DIT_ERR_INVALID_ARG, f"{tag} tensor is {t.dtype}, not {dtype}")
+    _refuse(DIT_ERR_SHAPE, f"{tag}: the channels of a head must be contiguous")
+
+
+def _heads_view(tag, t, shape, dtype):
+    """(pointer, batch, token and head strides) of a [batch, tokens, heads, head_dim] view."""
+    if t is None:
+        return _NO_VIEW
+    sb, st, sh, sd = t.stride() if t.dim() == 4 else _NO_VIEW
+    if t.shape != shape or t.dtype is not dtype or (sd != 1 and t.numel()):
+        _bad_view(tag, t, shape, dtype)
     return t.data_ptr(), sb, st, sh
+
+
+_NO_HEADS = (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
 
 
 def _rope_heads(tag, x, dy, out, weight, dweight, B, N, d, dtype):
@@ -259,16 +268,13 @@ def _rope_heads(tag, x, dy, out, weight, dweight, B, N, d, dtype):
     if out is None:
         if x is not None or dy is not None or weight is not None or dweight is not None:
             _refuse(DIT_ERR_INVALID_ARG, f"{tag} is given without its output")
-        return (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
+        return _NO_HEADS
     shape = out.shape
     if len(shape) != 4 or shape[0] != B or shape[1] != N or shape[3] != d:
         _refuse(DIT_ERR_SHAPE, f"{tag} output is {list(shape)}: [{B}, {N}, heads, {d}] is wanted")
-    return (shape[2], 0,
-            *(_NO_VIEW if x is None else _heads_view(f"{tag} input", x, shape, dtype)),
-            *(_NO_VIEW if dy is None else _heads_view(f"{tag} gradient", dy, shape, dtype)),
-            *_heads_view(f"{tag} output", out, shape, dtype),
-            0 if weight is None else _param(f"{tag}_weight", weight, (d,)),
-            0 if dweight is None else _param(f"d{tag}_weight", dweight, (d,)))
+    return (shape[2], 0, *_heads_view(tag, x, shape, dtype), *_heads_view(tag, dy, shape, dtype),
+            *_heads_view(tag, out, shape, dtype), 0 if weight is None else _param(tag, weight, (d,)),
+            0 if dweight is None else _param(tag, dweight, (d,)))
 
 
 def _rope_args(pos, axes, theta, style, eps, first, q, k):

@@ -436,16 +436,17 @@ def test_rows_around_a_view_are_left_alone():
     assert torch.equal(pix, before)
 
 
-def test_graph_replay_streams_and_repeated_calls_give_the_same_bits():
+@pytest.mark.parametrize("N,side", [(700, 60), (5000, 200), (40, 6)])  # every form of the kernels
+def test_graph_replay_streams_and_repeated_calls_give_the_same_bits(N, side):
     rng = np.random.default_rng(14)
-    pos = positions(rng, "grid", 1, 700, 3)
+    pos = positions(rng, "grid", 1, N, 3)
     kw = dict(axes=(16, 24, 24), style=dit.ROPE_SPLIT)
     s = torch.cuda.Stream()
 
     def state(seed):
         g = np.random.default_rng(seed)
-        x, dy = randn(g, (2, 700, 4, 64), "bf16"), randn(g, (2, 700, 4, 64), "bf16")
-        f, df = randn(g, (2, 60, 50, 96), "bf16"), randn(g, (2, 60, 50, 96), "bf16")
+        x, dy = randn(g, (2, N, 4, 64), "bf16"), randn(g, (2, N, 4, 64), "bf16")
+        f, df = randn(g, (2, side, 50, 96), "bf16"), randn(g, (2, side, 50, 96), "bf16")
         e = torch.empty
         return dict(x=x, dy=dy, w=weights(g, 64), y=torch.empty_like(x), dx=torch.empty_like(x), dw=e(64, device="cuda"),
                     f=f, df=df, fy=torch.empty_like(f), fdx=torch.empty_like(f), fw=weights(g, 96), fb=weights(g, 96),
@@ -487,6 +488,53 @@ def test_graph_replay_streams_and_repeated_calls_give_the_same_bits():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a[k], want_b[k]) for k in outs)
+
+
+def test_host_threads_call_at_once():
+    # the same kernels with different shared memory, from four threads on a stream each
+    import threading
+    rng = np.random.default_rng(16)
+    shapes = [(1, 64, 64, 64), (2, 32, 32, 256), (1, 40, 40, 512), (3, 150, 100, 64)]
+    xs = [randn(rng, s, "bf16") for s in shapes]
+    want = []
+    for x in xs:
+        y = torch.empty_like(x)
+        dit.dit_group_norm_forward(x, y, 8, act=dit.ACT_SILU)
+        want.append(y)
+    ys = [torch.empty_like(x) for x in xs]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            ws = torch.empty(max(1, dit.dit_group_norm_workspace_bytes(xs[i], 8, False)), dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            for _ in range(50):
+                dit.dit_group_norm_forward(xs[i], ys[i], 8, act=dit.ACT_SILU, workspace=ws, stream=s)
+            s.synchronize()
+        except Exception as e:  # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert all(torch.equal(a, b) for a, b in zip(ys, want))
+
+
+def test_single_batch_element_of_an_odd_sized_batch():
+    # the batch stride of one element says nothing about the rows' alignment
+    rng = np.random.default_rng(17)
+    x = randn(rng, (1, 33, 35, 64), "bf16")
+    wide = torch.empty(2, 33 * 35 * 64 + 1, dtype=torch.bfloat16, device="cuda")[:1, :-1].view(1, 33, 35, 64)
+    wide.copy_(x)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    dit.dit_group_norm_forward(x, y, 8)
+    dit.dit_group_norm_forward(wide, z, 8)
+    assert torch.equal(y, z)
 
 
 def test_explicit_stream_needs_a_workspace():

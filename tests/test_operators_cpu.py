@@ -91,7 +91,7 @@ def gn_args(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), SHAPE), (dict(pixels=-1), SHAPE), (dict(pixels=1 << 31), SHAPE), (dict(batch=1 << 21), SHAPE),
-    (dict(channels=0), SHAPE), (dict(channels=1 << 21, groups=1), SHAPE), (dict(groups=0), SHAPE), (dict(groups=5), SHAPE),
+    (dict(batch=1 << 18, pixels=1 << 20), SHAPE), (dict(channels=0), SHAPE), (dict(channels=1 << 21, groups=1), SHAPE), (dict(groups=0), SHAPE), (dict(groups=5), SHAPE),
     (dict(dtype=5), INVALID), (dict(act=2), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(reserved=1), INVALID), (dict(x=0), INVALID), (dict(out=0), INVALID), (dict(x=4098), INVALID),
     (dict(xs=(-1, 12)), SHAPE), (dict(os=(0, 12)), SHAPE), (dict(os=(108, 11)), SHAPE), (dict(os=(12, 12)), SHAPE),
