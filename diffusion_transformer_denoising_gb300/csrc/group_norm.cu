@@ -48,7 +48,7 @@ struct GnParams {
   int pixels, channels, groups, cpg;
   int splits;      // blocks that share a batch element's pixels
   int passes;      // the same for the pass that writes
-  int rounds;      // gradient on clusters that cover the batch: batch elements each of them takes in turn
+  int whole_batch; // gradient on clusters that hold the whole batch
   int slab;        // runs of V channels a block covers
   int part_lanes;  // threads that sum one channel's rows: a power of two
   int unit;        // channels of one partial: cpg where slabs hold whole groups, else 1
@@ -891,12 +891,11 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T)) < 4 ? s
 }
 
 // One launch, as gn_cluster_kernel: x and dy stay in shared memory between
-// the sums and dx.  A cluster holds P.splits blocks of each of one or more batch
-// elements.  Where it covers the whole batch (P.rounds > 0, in so many rounds) it
-// also joins the channel sums into dw and db; else a second launch does.
+// the sums and dx.  P.splits blocks take a batch element.  Where a cluster holds
+// the whole batch's (P.whole_batch) it also joins the channel sums into dw and
+// db; else a second launch does.
 // Shared memory: sums [rows][slab * V + 1] float2, own [slab * V] float2 (read
-// by the cluster), chan likewise, total likewise (read by the cluster), group
-// sums [groups of the slab] float2, x, dy.
+// by the cluster), chan likewise, group sums [groups of the slab] float2, x, dy.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __grid_constant__ GnParams P, int data_elems) {
   extern __shared__ float4 raw_sm[];
@@ -905,112 +904,101 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
   float2* sm = reinterpret_cast<float2*>(raw_sm);
   float2* own = sm + rows * (width + 1);
   float2* chan = own + width;
-  float2* total = chan + width;
-  float2* gs = total + width;
+  float2* gs = chan + width;
   T* data = reinterpret_cast<T*>(raw_sm) +
             ((reinterpret_cast<char*>(gs + slab_groups) - reinterpret_cast<char*>(raw_sm) + 15) / 16 * 16) / sizeof(T);
 
-  const uint32_t first_b = blockIdx.x / (uint32_t)P.splits, elements = gridDim.x / (uint32_t)P.splits;
-  const int share = blockIdx.x - first_b * P.splits;
+  const uint32_t b = blockIdx.x / (uint32_t)P.splits;
+  const int share = blockIdx.x - b * P.splits;
   const uint32_t base = cluster_ctarank() - share;  // rank of the batch element's first block
   const Place at(P, V, blockIdx.y, share, P.splits);
   const int c0 = blockIdx.y * width, here = min(width, P.channels - c0), groups = here / P.cpg, g0 = c0 / P.cpg;
   const float n = (float)P.pixels * (float)P.cpg;
   T* xs = data + threadIdx.x * V;
   T* gy = xs + data_elems;
-  uint32_t b = first_b;
-  for (int round = 0; round < max(P.rounds, 1); ++round, b += elements) {
-    const bool live = b < P.batch;  // the last round's blocks may have no element; they keep the barriers
-    const int count = live ? at.count : 0;
-    stage<T, V>(xs, static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.step * P.xs[1], count);
-    stage<T, V>(gy, static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.step * P.ds[1], count);
-    const int64_t bg = (int64_t)b * P.groups;
-    Affine<V> f;
-    GradSums<V> S;
-    if (at.on && live) {
-      f.weights(P, at.c);
-      f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[bg + g], P.rstd[bg + g]); });
-      staged();
+  stage<T, V>(xs, static_cast<const T*>(P.x) + b * P.xs[0] + at.p * P.xs[1] + at.c, at.step * P.xs[1], at.count);
+  stage<T, V>(gy, static_cast<const T*>(P.dy) + b * P.ds[0] + at.p * P.ds[1] + at.c, at.step * P.ds[1], at.count);
+  const int64_t bg = (int64_t)b * P.groups;
+  Affine<V> f;
+  GradSums<V> S;
+  if (at.on) {
+    f.weights(P, at.c);
+    f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[bg + g], P.rstd[bg + g]); });
+    staged();
 #pragma unroll 2
-      for (int i = 0; i < count; ++i) {
-        float v[V], g[V], xm[V], dz[V];
-        unpack<T, V>(load_raw<T, V>(xs + i * (kThreads * V)), v);
-        unpack<T, V>(load_raw<T, V>(gy + i * (kThreads * V)), g);
-        dz_of(f, v, g, P.act, xm, dz);
-        S.add(dz, xm);
-      }
-      float r[V];
-      spread(r, at.c, P.cpg, [&](int g) { return P.rstd[bg + g]; });
-      v_mul(S.B, S.B, r);
+    for (int i = 0; i < at.count; ++i) {
+      float v[V], g[V], xm[V], dz[V];
+      unpack<T, V>(load_raw<T, V>(xs + i * (kThreads * V)), v);
+      unpack<T, V>(load_raw<T, V>(gy + i * (kThreads * V)), g);
+      dz_of(f, v, g, P.act, xm, dz);
+      S.add(dz, xm);
     }
-    sum_rows<V>(at, S.A, S.B, sm, P.slab, P.part_lanes, [&](int c, float2 v) { own[c] = v; });
-    cluster_arrive();
-    cluster_wait();
+    float r[V];
+    spread(r, at.c, P.cpg, [&](int g) { return P.rstd[bg + g]; });
+    v_mul(S.B, S.B, r);
+  }
+  sum_rows<V>(at, S.A, S.B, sm, P.slab, P.part_lanes, [&](int c, float2 v) { own[c] = v; });
+  cluster_arrive();
+  cluster_wait();
+  for (int c = threadIdx.x; c < here; c += kThreads) {
+    float A = 0.f, B = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= P.splits) continue;
+      const float2 e = ld_cluster_f2(cluster_map(own + c, base + r));
+      A += e.x, B += e.y;
+    }
+    if (share == 0 && P.chan) P.chan[(int64_t)b * P.channels + c0 + c] = make_float2(A, B);
+    const float w = P.w ? P.w[c0 + c] : 1.f;
+    chan[c] = make_float2(w * A, w * B);
+  }
+  __syncthreads();
+  if (P.whole_batch && blockIdx.x == 0) {
+    // the batch's blocks in order
     for (int c = threadIdx.x; c < here; c += kThreads) {
       float A = 0.f, B = 0.f;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        if (r >= P.splits) continue;
-        const float2 e = ld_cluster_f2(cluster_map(own + c, base + r));
-        A += e.x, B += e.y;
+      for (uint32_t r = 0; r < gridDim.x; ++r) {
+        const float2 t = ld_cluster_f2(cluster_map(own + c, r));
+        A += t.x, B += t.y;
       }
-      if (P.rounds) total[c] = round ? make_float2(total[c].x + A, total[c].y + B) : make_float2(A, B);
-      else if (share == 0 && P.chan) P.chan[(int64_t)b * P.channels + c0 + c] = make_float2(A, B);
-      const float w = P.w ? P.w[c0 + c] : 1.f;
-      chan[c] = make_float2(w * A, w * B);
+      if (P.db) P.db[c0 + c] = A;
+      if (P.dw) P.dw[c0 + c] = B;
     }
-    __syncthreads();
-    cluster_arrive();
-    if (P.cpg <= 8) {
-      for (int g = threadIdx.x; g < groups; g += kThreads) {
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = 0; c < P.cpg; ++c) s1 += chan[g * P.cpg + c].x, s2 += chan[g * P.cpg + c].y;
-        gs[g] = make_float2(s1 / n, s2 / n);
-      }
-    } else {
-      const int lane = threadIdx.x & 31;
-      for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = lane; c < P.cpg; c += 32) s1 += chan[g * P.cpg + c].x, s2 += chan[g * P.cpg + c].y;
-        s1 = warp_sum(s1), s2 = warp_sum(s2);
-        if (lane == 0) gs[g] = make_float2(s1 / n, s2 / n);
-      }
+  }
+  cluster_arrive();  // this block has read its peers' memory
+  if (P.cpg <= 8) {
+    for (int g = threadIdx.x; g < groups; g += kThreads) {
+      float s1 = 0.f, s2 = 0.f;
+      for (int c = 0; c < P.cpg; ++c) s1 += chan[g * P.cpg + c].x, s2 += chan[g * P.cpg + c].y;
+      gs[g] = make_float2(s1 / n, s2 / n);
     }
-    __syncthreads();
-    if (at.on && live) {
-      GradApply<V> h;
-      h.set(at.c, P.cpg, [&](int g) { return make_float3(P.rstd[bg + g], gs[g - g0].x, gs[g - g0].y); });
-      T* out = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
-      const int64_t ostep = at.step * P.os[1];
+  } else {
+    const int lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
+      float s1 = 0.f, s2 = 0.f;
+      for (int c = lane; c < P.cpg; c += 32) s1 += chan[g * P.cpg + c].x, s2 += chan[g * P.cpg + c].y;
+      s1 = warp_sum(s1), s2 = warp_sum(s2);
+      if (lane == 0) gs[g] = make_float2(s1 / n, s2 / n);
+    }
+  }
+  __syncthreads();
+  if (at.on) {
+    GradApply<V> h;
+    h.set(at.c, P.cpg, [&](int g) { return make_float3(P.rstd[bg + g], gs[g - g0].x, gs[g - g0].y); });
+    T* out = static_cast<T*>(P.out) + b * P.os[0] + at.p * P.os[1] + at.c;
+    const int64_t ostep = at.step * P.os[1];
 #pragma unroll 2
-      for (int i = 0; i < count; ++i) {
-        float v[V], g[V], xm[V], dz[V];
-        unpack<T, V>(load_raw<T, V>(xs + i * (kThreads * V)), v);
-        unpack<T, V>(load_raw<T, V>(gy + i * (kThreads * V)), g);
-        dz_of(f, v, g, P.act, xm, dz);
-        h.dx(f, xm, dz);
-        store_f32<T, V>(out, dz);
-        out += ostep;
-      }
+    for (int i = 0; i < at.count; ++i) {
+      float v[V], g[V], xm[V], dz[V];
+      unpack<T, V>(load_raw<T, V>(xs + i * (kThreads * V)), v);
+      unpack<T, V>(load_raw<T, V>(gy + i * (kThreads * V)), g);
+      dz_of(f, v, g, P.act, xm, dz);
+      h.dx(f, xm, dz);
+      store_f32<T, V>(out, dz);
+      out += ostep;
     }
-    cluster_wait();  // every peer has read this block's sums
   }
-  if (P.rounds && (P.dw || P.db)) {
-    cluster_arrive();
-    cluster_wait();
-    if (blockIdx.x == 0)
-      for (int c = threadIdx.x; c < here; c += kThreads) {
-        float A = 0.f, B = 0.f;
-        for (uint32_t e = 0; e < elements; ++e) {
-          const float2 t = ld_cluster_f2(cluster_map(total + c, e * P.splits));
-          A += t.x, B += t.y;
-        }
-        if (P.db) P.db[c0 + c] = A;
-        if (P.dw) P.dw[c0 + c] = B;
-      }
-    cluster_arrive();
-    cluster_wait();
-  }
+  cluster_wait();  // a block's memory stays until every peer has read it
 }
 
 // ---------------------------------------------------------------- plan
@@ -1034,7 +1022,7 @@ struct Plan {
   bool cluster;
   int vec, slab, nslab, unit, splits, passes;
   bool fold;
-  int rounds, elements;  // cluster form of the gradient: see GnParams; batch elements side by side
+  bool whole_batch;  // cluster form of the gradient, see GnParams
   int data_elems;  // cluster form: elements of one staged tensor
   size_t smem;
 };
@@ -1047,7 +1035,7 @@ size_t scratch_bytes(const Plan& p, int cpg, bool backward) {
   const int rows = kThreads / p.slab, width = p.slab * p.vec;
   size_t n = (size_t)rows * (width + 1) * 8;                          // sums
   if (!backward) n += (size_t)width * 8 + (size_t)((width + 1) / 2) * 8;  // ch, piv
-  if (p.cluster) n += backward ? (size_t)width * 24 + (size_t)(width / cpg) * 8 : (size_t)(width / cpg) * 16;
+  if (p.cluster) n += backward ? (size_t)width * 16 + (size_t)(width / cpg) * 8 : (size_t)(width / cpg) * 16;
   return (n + 15) / 16 * 16;
 }
 
@@ -1126,15 +1114,10 @@ Plan plan_of(const dit_group_norm_args& a, int vec, bool backward) {
     auto pixels = [&] { return ceil_div(a.pixels, (int64_t)blocks * (kThreads / slab)); };
     while (blocks < kMaxCluster && ((pixels() > 2 && 2 * blocks * slabs() <= 152) || (pixels() > 8 && 2 * blocks * slabs() <= 304)))
       blocks *= 2;
-    // the gradient's clusters cover the batch, and join its weight sums, where
-    // that takes one round, or a few short ones
-    const int elements = backward ? (int)(a.batch < kMaxCluster / blocks ? a.batch : kMaxCluster / blocks) : 1;
-    const int64_t rounds = ceil_div(a.batch, elements);
-    const bool whole_batch = backward && (rounds == 1 || (rounds <= 3 && pixels() <= 2));
+    const bool whole_batch = backward && a.batch * blocks <= kMaxCluster;
     if (blocks * slabs() <= 304 && pixels() <= (backward && !whole_batch ? 6 : 8)) {
       Plan p = cluster_plan(a, vec, slab, blocks, backward);
-      p.rounds = whole_batch ? (int)rounds : 0;
-      p.elements = whole_batch ? elements : (int)a.batch;
+      p.whole_batch = whole_batch;
       if (p.smem) return p;
     }
   }
@@ -1149,7 +1132,7 @@ int64_t part_bytes(const dit_group_norm_args& a, const Plan& p) {
 }
 int64_t group_bytes(const dit_group_norm_args& a, const Plan& p) { return p.cluster ? 0 : round256(a.batch * a.groups * 8); }
 int64_t chan_bytes(const dit_group_norm_args& a, const Plan& p, bool backward) {
-  return !backward || (p.cluster && p.rounds) ? 0 : round256(a.batch * (int64_t)a.channels * 8);
+  return !backward || p.whole_batch ? 0 : round256(a.batch * (int64_t)a.channels * 8);
 }
 
 // ---------------------------------------------------------------- launch
@@ -1166,10 +1149,9 @@ cudaError_t run(const dit_group_norm_args& a, const Plan& pl, const GnParams& P,
   const unsigned extra = P.dw || P.db ? (unsigned)ceil_div(a.channels, kThreads) : 0;
   if (pl.cluster) {
     if (!backward) return launch_kernel(gn_cluster_kernel<T, V>, grid, kThreads, pl.smem, s, pl.splits, false, P);
-    const dim3 side((unsigned)(pl.elements * pl.splits), (unsigned)pl.nslab);
-    GN_TRY(launch_kernel(gn_grad_cluster_kernel<T, V>, side, kThreads, pl.smem, s, pl.rounds ? (int)side.x : pl.splits, false, P,
-                         pl.data_elems));
-    return extra && !pl.rounds ? launch_kernel(gn_grad_weights_kernel, dim3(extra), kThreads, 0, s, 1, true, P) : cudaSuccess;
+    GN_TRY(launch_kernel(gn_grad_cluster_kernel<T, V>, grid, kThreads, pl.smem, s, pl.whole_batch ? (int)grid.x : pl.splits, false,
+                         P, pl.data_elems));
+    return extra && !pl.whole_batch ? launch_kernel(gn_grad_weights_kernel, dim3(extra), kThreads, 0, s, 1, true, P) : cudaSuccess;
   }
   const size_t ring = Feed1<T, V, false>::kBytes, ring2 = Feed2<T, V, false>::kBytes;
   if (!backward) {
@@ -1232,7 +1214,7 @@ cudaError_t group_norm_run(const dit_group_norm_args& a, bool backward, float* w
   P.slab = pl.slab;
   for (P.part_lanes = 1; P.part_lanes < 32 && 2 * P.part_lanes * pl.slab * pl.vec <= kThreads; P.part_lanes *= 2) {}
   P.unit = pl.unit;
-  P.rounds = pl.rounds;
+  P.whole_batch = pl.whole_batch;
   P.fold = pl.fold;
   P.act = a.act;
   P.eps = a.eps;

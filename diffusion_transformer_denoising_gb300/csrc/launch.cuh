@@ -14,9 +14,16 @@ DIT_DEV void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory")
 
 // Clusters of up to 8 blocks (the portable limit): the two halves of the
 // cluster barrier, and reads of a peer's shared memory at a cluster_map address.
+// Every warp of the cluster reaches both halves, its lanes together.
 constexpr int kMaxCluster = 8;
-DIT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-DIT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+DIT_DEV void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+DIT_DEV void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 DIT_DEV float ld_cluster_f1(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");

@@ -289,8 +289,9 @@ GN_CASES = [
     ("f16", (2, 9001, 66), 6, "none", True, 0, 0.0),            # rows of 4-byte alignment, streamed
     ("f32", (1, 3001, 1100), 1, "silu", True, 0, 0.0),          # one group wider than a block
     ("f32", (9, 4000, 32), 32, "silu", True, 0, 0.0),
-    ("bf16", (19, 40, 48), 4, "silu", True, 0, 0.0),            # a batch that one cluster takes in three rounds
+    ("bf16", (19, 40, 48), 4, "silu", True, 0, 0.0),            # small maps, their weight sums in a second launch
     ("f32", (3, 700, 16), 2, "silu", True, 0, 0.0),
+    ("bf16", (8, 30, 64), 8, "silu", True, 0, 0.0),             # a cluster that holds the whole batch
     ("f16", (2, 97, 52), 4, "none", True, 0, 0.0),
 ]
 
