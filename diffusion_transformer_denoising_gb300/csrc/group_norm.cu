@@ -25,6 +25,13 @@
 //     pixels backwards, so that what the sums read last is still in L2;
 //     launches chained by programmatic dependence, the pass's first loads on
 //     their way before the sums are done.
+// Measured on one GB300 (bf16): 1024 x 1024 pixels x 128 channels with SiLU 131 us:
+// the sums 55 us for 328 MB of DRAM traffic (60 of them the previous output on its
+// way out), the pass 78 us for 395 MB, 80 MB of x out of L2 (reading L2 and writing
+// DRAM 5 TB/s of writes, both from DRAM 3.1, so 76 us is what that traffic takes).
+// 21 x 6240 x 384 49.4 us; gradient of 4 x 16384 x 512 52.6 us.  Blocks that each
+// take one range of pixels instead of turns leave only 11 MB of x in L2 (137 us);
+// register loads instead of rings 136 us; normal stores 134 us.
 #include "launch.cuh"
 #include "operators.h"
 #include "vec.cuh"

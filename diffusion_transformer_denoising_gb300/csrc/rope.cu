@@ -6,22 +6,23 @@
 // The frequency is held in turns as a 64-bit fraction f, so the angle modulo
 // one turn is the low 64 bits of the integer product pos * f: the reduction is
 // exact however far the position (the only error is f's own, 2^-53 of it).
-// The top two bits pick the quadrant and the remaining +-1/8 turn goes to
-// sincospif.  With a norm: xhat = x r, r = (mean x^2 + eps)^-1/2, z = xhat w,
+// The top two bits pick the quadrant and the remaining +-1/8 turn goes through
+// two short polynomials.  With a norm: xhat = x r, r = (mean x^2 + eps)^-1/2, z = xhat w,
 // y = R z.  Gradient: g = R^T dy; dw = sum g xhat; with h = g w,
 // dx = r (h - xhat mean(h xhat)); the two row sums (x^2 and h x) are taken
 // together, so a row costs one round of shuffles either way.
 //
-// What bounds it: HBM, once the latency is covered.  Every row is read once
-// and written once.  A group of 2 to 32 lanes holds one row in registers (8
-// channels a lane, 128-bit accesses), forms its pairs' cos and sin once for
-// all the token's heads, and always has the next batch of rows (64 bytes a
-// lane), of the next tensor or token too, and the next token's positions on
-// their way.  Measured on one GB300 (bf16, 128-wide heads, 44/42/42): q and k
-// of 2 x 32760 tokens x 12 heads 122 us = 6.60 TB/s (0.99 of the copy
-// bandwidth); 32760 tokens with the norm, out of a packed projection, 70.5 us
-// = 5.72 TB/s; its gradient 115 us = 5.27 TB/s (without the loads ahead 151 us;
-// with the positions not among them 146 us).
+// What bounds it: HBM, once the latency is covered; with the norm, and more so
+// for its gradient, the instructions of a row (0.65 and 0.59 of the issue slots).
+// Every row is read once and written once.  A group of lanes holds one row in
+// registers (8 channels a lane, 128-bit accesses), forms its pairs' cos and sin
+// once for all the token's heads, and always has the next batch of rows (64 bytes
+// a lane), of the next tensor or token too, and the next token's positions on
+// their way.  Measured on one GB300 (bf16, 128-wide heads, 44/42/42): q and k of
+// 2 x 32760 tokens x 12 heads 122 us = 6.59 TB/s (0.99 of the copy bandwidth);
+// 32760 tokens with the norm, out of a packed projection, 68.7 us = 5.87 TB/s; its
+// gradient 116 us = 5.21 TB/s (without the loads ahead 151 us; with the positions
+// not among them 146 us).
 #include <math.h>
 
 #include <type_traits>
@@ -37,13 +38,23 @@ namespace {
 constexpr int kRopeThreads = 256;
 
 // ---------------------------------------------------------------- angles
-// cos and sin of u / 2^64 turns.
+// cos and sin of u / 2^64 turns.  The remaining angle x half turns, |x| <= 1/4,
+// goes through the Taylor series of sin(pi x) and cos(pi x) about 0 (to x^9 and
+// x^10: what is cut off is below 2^-28), off by at most 1.5 x 2^-24 in all.
 DIT_DEV void turns_sincos(uint64_t u, float& c, float& s) {
   const uint32_t hi = (uint32_t)(u >> 32);
-  const uint32_t k = (hi + 0x20000000u) >> 30;             // nearest quarter turn, 0..3
-  const int32_t rem = (int32_t)(hi - (k << 30));           // in units of 2^-32 turns, |rem| <= 2^29
-  float sr, cr;
-  sincospif((float)rem * 4.656612873077393e-10f, &sr, &cr);  // 2^-31: half turns
+  const uint32_t k = (hi + 0x20000000u) >> 30;                // nearest quarter turn, 0..3
+  const int32_t rem = (int32_t)(hi - (k << 30));              // in units of 2^-32 turns, |rem| <= 2^29
+  const float x = (float)rem * 4.656612873077393e-10f, q = x * x;  // 2^-31: half turns
+  float sr = fmaf(q, 0.08214588661112823f, -0.5992645293207921f);
+  sr = fmaf(sr, q, 2.550164039877345f);
+  sr = fmaf(sr, q, -5.16771278004997f);
+  sr = fmaf(sr, q, 3.141592653589793f) * x;
+  float cr = fmaf(q, -0.02580689139001406f, 0.23533063035889312f);
+  cr = fmaf(cr, q, -1.3352627688545893f);
+  cr = fmaf(cr, q, 4.058712126416768f);
+  cr = fmaf(cr, q, -4.934802200544679f);
+  cr = fmaf(cr, q, 1.f);
   const float a = (k & 1) ? sr : cr, b = (k & 1) ? cr : sr;  // quarter turns swap and negate
   c = (k == 1 || k == 2) ? -a : a;
   s = (k >= 2) ? -b : b;
@@ -255,18 +266,15 @@ DIT_DEV void group_sums(float (&v)[N], int lane, int slots) {
   }
 }
 
-// Two pairs turned; MIX: the first (tx) or second (ty) of them may be a pair
-// of channels that are not turned, which must not meet (0 * inf).
+// Two pairs turned; MIX: the first (tx) or second (ty) of them may be a pair of
+// channels that are not turned (k1 = k2 = 0), which must not meet: 0 * inf.
 template <bool MIX>
 DIT_DEV void turn_pair(float2 a, float2 b, float2 k0, float2 k1, float2 k2, float2 k3, bool tx, bool ty, float2& ya,
                        float2& yb) {
-  ya = fma2(a, k0, mul2(b, k1));
-  yb = fma2(a, k2, mul2(b, k3));
-  if constexpr (MIX) {
-    const float2 pa = mul2(a, k0), pb = mul2(b, k3);
-    ya = make_float2(tx ? ya.x : pa.x, ty ? ya.y : pa.y);
-    yb = make_float2(tx ? yb.x : pb.x, ty ? yb.y : pb.y);
-  }
+  const float2 am = MIX ? make_float2(tx ? a.x : 0.f, ty ? a.y : 0.f) : a;
+  const float2 bm = MIX ? make_float2(tx ? b.x : 0.f, ty ? b.y : 0.f) : b;
+  ya = fma2(a, k0, mul2(bm, k1));
+  yb = fma2(am, k2, mul2(b, k3));
 }
 
 // blockIdx.y of gridDim.y: a slice of q's heads and of k's; blockIdx.x strides
