@@ -415,7 +415,7 @@ DIT_DEV void activate(float (&v)[V], int act) {
   }
 }
 
-// ---------------------------------------------------------------- forward, three launches
+// ---------------------------------------------------------------- forward, two or three launches
 // Every channel's (mean, M2) over the block's `len` pixels, into ch.  drain(A)
 // runs the thread's pixels through A; ch and piv are [slab * V].
 template <typename T, int V, class Drain>
@@ -592,7 +592,6 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_app
 }
 
 // ---------------------------------------------------------------- forward, one launch
-
 // All of a thread's pixels into its own places of shared memory, [i][thread]:
 // in the background where cp.async can (staged() waits), else batch by batch.
 template <typename T, int V>

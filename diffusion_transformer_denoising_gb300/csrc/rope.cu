@@ -527,6 +527,8 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
     else batch(Int<kSide>{}, std::false_type{}, HU);
   }
 
+  cp_async_wait();  // nothing of a token that never came is left on its way
+
   if constexpr (GRAD) {
     // the block's dweight: groups in order, through shared memory; then the
     // cluster's, where the tensor's blocks are one

@@ -238,7 +238,7 @@ def _workspace(t, workspace, stream, need):
     if stream is not None:
         _refuse(DIT_ERR_INVALID_ARG, "a call on an explicit stream needs its workspace passed in")
     # the allocator hands blocks out in the order of the current stream, which is the call's
-    ws = t.new_empty(-(-need // t.element_size()))
+    ws = _torch.empty(need, dtype=_torch.uint8, device=t.device)
     return ws.data_ptr(), need, ws
 
 
