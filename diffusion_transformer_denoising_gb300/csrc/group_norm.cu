@@ -13,7 +13,9 @@
 // cancels however large the mean, and a single outlier cannot become the
 // pivot.  Threads are joined by plain sums, then turned into (mean, M2) about
 // the mean, and channels of a group and blocks joined as (count, mean, M2), all
-// in a fixed order: results are the same bits every time.
+// in a fixed order: results are the same bits every time.  The joined means are
+// unevaluated sums of two floats until the last step, so a group's mean is as good
+// where its channels' means cancel.
 //
 // What bounds it: HBM and the second look at x.  Two forms:
 //   - whole groups of a batch element that fit a cluster's shared memory: one
@@ -25,11 +27,11 @@
 //     pixels backwards, so that what the sums read last is still in L2;
 //     launches chained by programmatic dependence, the pass's first loads on
 //     their way before the sums are done.
-// Measured on one GB300 (bf16): 1024 x 1024 pixels x 128 channels with SiLU 131 us:
+// Measured on one GB300 (bf16): 1024 x 1024 pixels x 128 channels with SiLU 132 us:
 // the sums 55 us for 328 MB of DRAM traffic (60 of them the previous output on its
 // way out), the pass 78 us for 395 MB, 80 MB of x out of L2 (reading L2 and writing
 // DRAM 5 TB/s of writes, both from DRAM 3.1, so 76 us is what that traffic takes).
-// 21 x 6240 x 384 49.4 us; gradient of 4 x 16384 x 512 52.6 us.  Blocks that each
+// 21 x 6240 x 384 50.1 us; gradient of 4 x 16384 x 512 52.7 us.  Blocks that each
 // take one range of pixels instead of turns leave only 11 MB of x in L2 (137 us);
 // register loads instead of rings 136 us; normal stores 134 us.
 #include "launch.cuh"
@@ -68,7 +70,8 @@ struct GnParams {
   const float* rstd;
   float* mean_out;    // [batch, groups], written, or NULL (cluster form)
   float* rstd_out;
-  float2* part;       // forward [batch, splits, channels / unit], gradient [batch, splits, channels]
+  float4* sums;       // forward [batch, splits, channels / unit]: Joint as (n, mean, low, M)
+  float2* part;       // gradient [batch, splits, channels]
   float2* chan;       // [batch, channels]: gradient, (A, B)
   float2* gsum;       // [batch, groups]: gradient, (s1, s2)
   float* dw;
@@ -343,35 +346,83 @@ DIT_DEV float warp_sum(float v) {
   return v;
 }
 
+// a + b = high + low exactly (Knuth).
+DIT_DEV float two_sum(float a, float b, float& low) {
+  const float h = a + b, t = h - a;
+  low = (a - (h - t)) + (b - t);
+  return h;
+}
+// A mean as the unevaluated sum of two floats, and the second moment about it.
+struct Mom {
+  float mean, low, M;
+};
+// mean + low of a sum of n values given as h + l.
+DIT_DEV float2 mean_of(float h, float l, float n) {
+  const float m = h / n;
+  return make_float2(m, isfinite(m) ? (fmaf(-m, n, h) + l) / n : 0.f);
+}
+
 // Joins the channels of every group of the slab, each of `len` pixels, from
-// their (mean, M2) in ch; out(g, mean, M2).  A thread a group of few channels,
-// a warp one of many.
+// their moments in ch; out(g, Mom).  A thread a group of few channels, a warp
+// one of many.
 template <class Out>
-DIT_DEV void join_channels(const float2* ch, int groups, int cpg, float len, Out out) {
-  if (cpg <= 8) {
-    for (int g = threadIdx.x; g < groups; g += kThreads) {
-      const float2* e = ch + g * cpg;
-      const float K = e[0].x;
-      float mean = 0.f, M = 0.f;
-      for (int c = 1; c < cpg; ++c) mean += e[c].x - K;
-      mean = K + mean / (float)cpg;
-      for (int c = 0; c < cpg; ++c) M += fmaf(len * (e[c].x - mean), e[c].x - mean, e[c].y);
-      out(g, mean, M);
+DIT_DEV void join_channels(const Mom* ch, int groups, int cpg, float len, Out out) {
+  const int lanes = cpg <= 8 ? 1 : 32, lane = cpg <= 8 ? 0 : threadIdx.x & 31;
+  for (int g = threadIdx.x / (unsigned)lanes; g < groups; g += kThreads / lanes) {
+    const Mom* e = ch + g * cpg;
+    float h = 0.f, l = 0.f, M = 0.f, t;
+    for (int c = lane; c < cpg; c += lanes) {
+      h = two_sum(h, e[c].mean, t);
+      l += t + e[c].low;
     }
-  } else {
-    const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
-      const float2* e = ch + g * cpg;
-      const float K = e[0].x;
-      float mean = 0.f, M = 0.f;
-      for (int c = lane; c < cpg; c += 32) mean += e[c].x - K;
-      mean = K + warp_sum(mean) / (float)cpg;
-      for (int c = lane; c < cpg; c += 32) M += fmaf(len * (e[c].x - mean), e[c].x - mean, e[c].y);
-      M = warp_sum(M);
-      if (lane == 0) out(g, mean, M);
+    if (lanes > 1) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const float oh = __shfl_xor_sync(0xFFFFFFFFu, h, o), ol = __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        h = two_sum(h, oh, t);
+        l += ol + t;
+      }
     }
+    const float2 m = mean_of(h, l, (float)cpg);
+    for (int c = lane; c < cpg; c += lanes) {
+      const float d = (e[c].mean - m.x) + (e[c].low - m.y);
+      M += fmaf(len * d, d, e[c].M);
+    }
+    if (lanes > 1) M = warp_sum(M);
+    if (lane == 0) out(g, Mom{m.x, m.y, M});
   }
 }
+
+// Moments of two sets joined into the first.
+struct Joint {
+  float n, mean, low, M;
+  DIT_DEV void take(float on, float omean, float olow, float oM) {
+    if (on == 0.f) return;
+    if (n == 0.f) {
+      n = on, mean = omean, low = olow, M = oM;
+      return;
+    }
+    const float f = on / (n + on), d = (omean - mean) + (olow - low);
+    float t;
+    if (!isfinite(d)) {  // a mean that is infinite stays so; no variance about it
+      n += on, mean += omean, low = 0.f, M = d - d;
+      return;
+    }
+    M += fmaf(d * d, n * f, oM);
+    mean = two_sum(mean, d * f, t);
+    low += t;
+    n += on;
+  }
+  DIT_DEV void take(const float4& o) { take(o.x, o.y, o.z, o.w); }
+  // of the lane `o` further on, where there is one
+  DIT_DEV void take_down(int o, bool some) {
+    const float4 v = make_float4(__shfl_down_sync(0xFFFFFFFFu, n, o), __shfl_down_sync(0xFFFFFFFFu, mean, o),
+                                 __shfl_down_sync(0xFFFFFFFFu, low, o), __shfl_down_sync(0xFFFFFFFFu, M, o));
+    if (some) take(v);
+  }
+  DIT_DEV float4 packed() const { return make_float4(n, mean, low, M); }
+  DIT_DEV float rounded_mean() const { return isfinite(mean) ? mean + low : mean; }
+};
 
 DIT_DEV float rstd_of(float var, float eps) {
   return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);  // a NaN stays one
@@ -416,10 +467,10 @@ DIT_DEV void activate(float (&v)[V], int act) {
 }
 
 // ---------------------------------------------------------------- forward, two or three launches
-// Every channel's (mean, M2) over the block's `len` pixels, into ch.  drain(A)
+// Every channel's moments over the block's `len` pixels, into ch.  drain(A)
 // runs the thread's pixels through A; ch and piv are [slab * V].
 template <typename T, int V, class Drain>
-DIT_DEV void block_moments(const GnParams& P, const Place& at, const T* x, int len, float2* sm, float2* ch, float* piv,
+DIT_DEV void block_moments(const GnParams& P, const Place& at, const T* x, int len, float2* sm, Mom* ch, float* piv,
                            Drain drain) {
   Moments<V> A;
   if (at.on && len > 0) {
@@ -433,12 +484,14 @@ DIT_DEV void block_moments(const GnParams& P, const Place& at, const T* x, int l
   const float n = (float)len, in = len > 0 ? 1.f / n : 0.f;
   sum_rows<V>(at, A.s, A.q, sm, P.slab, P.part_lanes, [&](int c, float2 v) {
     const float d = v.x * in;
-    ch[c] = make_float2(len > 0 ? piv[c] + d : 0.f, fmaf(-d, v.x, v.y));
+    Mom m{0.f, 0.f, fmaf(-d, v.x, v.y)};
+    if (len > 0) m.mean = two_sum(piv[c], d, m.low);
+    ch[c] = m;
   });
 }
 
-// part[b, split, unit] = (mean, M2) of the unit's channels over the split.
-// Shared memory: the ring, sums [rows][slab * V + 1], ch [slab * V] float2,
+// sums[b, split, unit] = moments of the unit's channels over the split.
+// Shared memory: the ring, sums [rows][slab * V + 1] float2, ch [slab * V] Mom,
 // piv [slab * V].
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_sums_kernel(const __grid_constant__ GnParams P) {
@@ -454,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_sum
   feed.start(raw_sm, at.count);
   const int len = share_pixels(P, at.rows, split, P.splits);
   const int width = P.slab * V, c0 = blockIdx.y * width;
-  float2* ch = sm + at.rows * (width + 1);
+  Mom* ch = reinterpret_cast<Mom*>(sm + at.rows * (width + 1));
   block_moments<T, V>(P, at, x, len, sm, ch, reinterpret_cast<float*>(ch + width), [&](Moments<V>& A) {
     feed.run([&](int, const Raw<T, V>(&r)[1]) {
       float v[V];
@@ -463,29 +516,14 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_sum
     });
   });
   const int here = min(width, P.channels - c0);
-  float2* part = P.part + ((int64_t)blockIdx.x * P.channels + c0) / P.unit;
+  float4* sums = P.sums + ((int64_t)blockIdx.x * P.channels + c0) / P.unit;
+  const float n = (float)len * (float)P.unit;
   if (P.unit == 1) {
-    for (int c = threadIdx.x; c < here; c += kThreads) part[c] = ch[c];
+    for (int c = threadIdx.x; c < here; c += kThreads) sums[c] = make_float4(n, ch[c].mean, ch[c].low, ch[c].M);
   } else {
-    join_channels(ch, here / P.cpg, P.cpg, (float)len, [&](int g, float mean, float M) { part[g] = make_float2(mean, M); });
+    join_channels(ch, here / P.cpg, P.cpg, (float)len, [&](int g, Mom m) { sums[g] = make_float4(n, m.mean, m.low, m.M); });
   }
 }
-
-// (count, mean, M2) of two sets joined into the first.
-struct Joint {
-  float n, mean, M;
-  DIT_DEV void take(float on, float omean, float oM) {
-    if (on == 0.f) return;
-    if (n == 0.f) {
-      n = on, mean = omean, M = oM;
-      return;
-    }
-    const float f = on / (n + on), d = omean - mean;
-    M += fmaf(d * d, n * f, oM);
-    mean = fmaf(d, f, mean);
-    n += on;
-  }
-};
 
 // Joins the partials of one (batch element, group).
 constexpr int kJoinThreads = 128;
@@ -495,60 +533,48 @@ __global__ void __launch_bounds__(kJoinThreads) gn_join_kernel(const __grid_cons
   const uint32_t b = blockIdx.x / (uint32_t)P.groups;
   const int g = blockIdx.x - b * P.groups;
   const int per = P.cpg / P.unit, stride = P.channels / P.unit;
-  const float2* part = P.part + (int64_t)b * P.splits * stride + (int64_t)g * per;
+  const float4* sums = P.sums + (int64_t)b * P.splits * stride + (int64_t)g * per;
   const int64_t entries = (int64_t)P.splits * per;
-  const int rows = kThreads / (unsigned)P.slab;
-  Joint J{0.f, 0.f, 0.f};
+  Joint J{0.f, 0.f, 0.f, 0.f};
   wait_previous();
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < entries; i += kJoinThreads) {
     const int s = per == 1 ? (int)i : (int)(i / per);
-    const float2 e = part[(int64_t)s * stride + (i - (int64_t)s * per)];
-    J.take((float)share_pixels(P, rows, s, P.splits) * (float)P.unit, e.x, e.y);
+    J.take(sums[(int64_t)s * stride + (i - (int64_t)s * per)]);
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float n = __shfl_down_sync(0xFFFFFFFFu, J.n, o), m = __shfl_down_sync(0xFFFFFFFFu, J.mean, o);
-    J.take(n, m, __shfl_down_sync(0xFFFFFFFFu, J.M, o));
-  }
+  for (int o = 16; o; o >>= 1) J.take_down(o, true);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = J;
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 1; i < kJoinThreads / 32; ++i) J.take(sm[i].n, sm[i].mean, sm[i].M);
-    P.mean_out[blockIdx.x] = J.mean;
+    for (int i = 1; i < kJoinThreads / 32; ++i) J.take(sm[i].packed());
+    P.mean_out[blockIdx.x] = J.rounded_mean();
     P.rstd_out[blockIdx.x] = rstd_of(J.n > 0.f ? J.M / J.n : 0.f, P.eps);
   }
 }
 
 // `lanes` (a power of two) neighbouring threads join one group's partials of a
 // batch element: stat[g] = (mean, rstd) of the slab's groups.
-DIT_DEV void fold_groups(const GnParams& P, uint32_t b, int g0, int groups, float2* stat, int rows, bool write) {
+DIT_DEV void fold_groups(const GnParams& P, uint32_t b, int g0, int groups, float2* stat, bool write) {
   int lanes = 1;
   while (lanes < 32 && 2 * lanes * groups <= kThreads) lanes *= 2;
   const int t = threadIdx.x & (lanes - 1), per = kThreads / (unsigned)lanes;
-  const float2* part = P.part + (int64_t)b * P.splits * P.groups + g0;
+  const float4* sums = P.sums + (int64_t)b * P.splits * P.groups + g0;
   for (int base = 0; base < groups; base += per) {
     const int g = base + threadIdx.x / (unsigned)lanes;
-    Joint J{0.f, 0.f, 0.f};
+    Joint J{0.f, 0.f, 0.f, 0.f};
     if (g < groups) {
 #pragma unroll 4
-      for (int s = t; s < P.splits; s += lanes) {
-        const float2 e = part[(int64_t)s * P.groups + g];
-        J.take((float)share_pixels(P, rows, s, P.splits) * (float)P.cpg, e.x, e.y);
-      }
+      for (int s = t; s < P.splits; s += lanes) J.take(sums[(int64_t)s * P.groups + g]);
     }
-    for (int o = lanes >> 1; o; o >>= 1) {
-      const float n = __shfl_down_sync(0xFFFFFFFFu, J.n, o), m = __shfl_down_sync(0xFFFFFFFFu, J.mean, o);
-      const float M = __shfl_down_sync(0xFFFFFFFFu, J.M, o);
-      if (t + o < lanes) J.take(n, m, M);
-    }
+    for (int o = lanes >> 1; o; o >>= 1) J.take_down(o, t + o < lanes);
     if (t == 0 && g < groups) {
-      const float rstd = rstd_of(J.n > 0.f ? J.M / J.n : 0.f, P.eps);
-      stat[g] = make_float2(J.mean, rstd);
+      const float mean = J.rounded_mean(), rstd = rstd_of(J.n > 0.f ? J.M / J.n : 0.f, P.eps);
+      stat[g] = make_float2(mean, rstd);
       if (write) {
         const int64_t bg = (int64_t)b * P.groups + g0 + g;
-        if (P.mean_out) P.mean_out[bg] = J.mean;
+        if (P.mean_out) P.mean_out[bg] = mean;
         if (P.rstd_out) P.rstd_out[bg] = rstd;
       }
     }
@@ -575,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T))) gn_app
   wait_previous();
   if (P.fold) {
     const int width = P.slab * V, c0 = blockIdx.y * width, g0 = c0 / P.cpg, groups = min(width, P.channels - c0) / P.cpg;
-    fold_groups(P, b, g0, groups, stat, at.rows, share == 0);
+    fold_groups(P, b, g0, groups, stat, share == 0);
     if (at.on) f.statistics(at.c, P.cpg, [&](int g) { return stat[g - g0]; });
   } else if (at.on) {
     f.statistics(at.c, P.cpg, [&](int g) { return make_float2(P.mean[(int64_t)b * P.groups + g], P.rstd[(int64_t)b * P.groups + g]); });
@@ -608,18 +634,19 @@ DIT_DEV void staged() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // A cluster of `splits` blocks takes one slab (whole groups) of one batch
 // element; each block keeps its pixels in shared memory, every thread reading
 // back only what it wrote itself.
-// Shared memory: as gn_sums_kernel, then own [groups of the slab] float2 (read
-// by the cluster), stat likewise, data.
+// Shared memory: own [groups of the slab] float4 (read by the cluster), stat
+// [groups of the slab] float2, sums, ch and piv as gn_sums_kernel, data.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 2) gn_cluster_kernel(const __grid_constant__ GnParams P) {
   extern __shared__ float4 raw_sm[];
   const int width = P.slab * V, rows = kThreads / (unsigned)P.slab, slab_groups = width / P.cpg;
-  float2* sm = reinterpret_cast<float2*>(raw_sm);
-  float2* ch = sm + rows * (width + 1);
-  float2* own = ch + width + (width + 1) / 2;  // piv between
-  float2* stat = own + slab_groups;
+  float4* own = raw_sm;
+  float2* stat = reinterpret_cast<float2*>(own + slab_groups);
+  float2* sm = stat + slab_groups;
+  Mom* ch = reinterpret_cast<Mom*>(sm + rows * (width + 1));
+  float* piv = reinterpret_cast<float*>(ch + width);
   T* data = reinterpret_cast<T*>(raw_sm) +
-            ((reinterpret_cast<char*>(stat + slab_groups) - reinterpret_cast<char*>(raw_sm) + 15) / 16 * 16) / sizeof(T);
+            ((reinterpret_cast<char*>(piv + width) - reinterpret_cast<char*>(raw_sm) + 15) / 16 * 16) / sizeof(T);
 
   const uint32_t b = blockIdx.x / (uint32_t)P.splits;
   const int rank = blockIdx.x - b * P.splits;
@@ -630,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_cluster_kernel(const __grid_co
   if (at.on) f.weights(P, at.c);
   const T* x = static_cast<const T*>(P.x) + b * P.xs[0];
   stage<T, V>(mine, x + at.p * P.xs[1] + at.c, at.step * P.xs[1], at.count);
-  block_moments<T, V>(P, at, x, len, sm, ch, reinterpret_cast<float*>(ch + width), [&](Moments<V>& A) {
+  block_moments<T, V>(P, at, x, len, sm, ch, piv, [&](Moments<V>& A) {
     staged();
 #pragma unroll 4
     for (int i = 0; i < at.count; ++i) {
@@ -640,19 +667,19 @@ __global__ void __launch_bounds__(kThreads, 2) gn_cluster_kernel(const __grid_co
     }
   });
   const int c0 = blockIdx.y * width, groups = min(width, P.channels - c0) / P.cpg, g0 = c0 / P.cpg;
-  join_channels(ch, groups, P.cpg, (float)len, [&](int g, float mean, float M) { own[g] = make_float2(mean, M); });
+  join_channels(ch, groups, P.cpg, (float)len,
+                [&](int g, Mom m) { own[g] = make_float4((float)len * (float)P.cpg, m.mean, m.low, m.M); });
   cluster_arrive();
   cluster_wait();
   for (int g = threadIdx.x; g < groups; g += kThreads) {
-    float2 e[kMaxCluster];
+    float4 e[kMaxCluster];
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      e[r] = r < P.splits ? ld_cluster_f2(cluster_map(own + g, r)) : make_float2(0.f, 0.f);
-    Joint J{0.f, 0.f, 0.f};
+      e[r] = r < P.splits ? ld_cluster_f4(cluster_map(own + g, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    Joint J{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < P.splits) J.take((float)share_pixels(P, rows, r, P.splits) * (float)P.cpg, e[r].x, e[r].y);
-    const float mean = J.mean, rstd = rstd_of(J.M / J.n, P.eps);
+    for (int r = 0; r < kMaxCluster; ++r) J.take(e[r]);
+    const float mean = J.rounded_mean(), rstd = rstd_of(J.M / J.n, P.eps);
     stat[g] = make_float2(mean, rstd);
     if (rank == 0) {
       if (P.mean_out) P.mean_out[b * P.groups + g0 + g] = mean;
@@ -709,14 +736,27 @@ DIT_DEV void spread(float (&d)[V], int c, int cpg, S value) {
     d[i] = t;
   }
 }
-// Sums of a thread.
+// Sums of a thread; of few channels in two levels of 16 pixels, since the sums of
+// few channels are many pixels long and may cancel.
 template <int V>
 struct GradSums {
-  float A[V], B[V];
-  DIT_DEV GradSums() { v_set(A, 0.f), v_set(B, 0.f); }
+  float A[V], B[V], a[V], b[V];
+  int n;
+  DIT_DEV GradSums() : n(0) { v_set(A, 0.f), v_set(B, 0.f), v_set(a, 0.f), v_set(b, 0.f); }
   DIT_DEV void add(const float (&dz)[V], const float (&xm)[V]) {
-    v_add(A, A, dz);
-    v_fma(B, dz, xm, B);
+    if constexpr (V < 4) {
+      v_add(a, a, dz);
+      v_fma(b, dz, xm, b);
+      if ((++n & 15) == 0) fold();
+    } else {
+      v_add(A, A, dz);
+      v_fma(B, dz, xm, B);
+    }
+  }
+  DIT_DEV void fold() {
+    v_add(A, A, a);
+    v_add(B, B, b);
+    v_set(a, 0.f), v_set(b, 0.f);
   }
 };
 
@@ -749,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, stream_blocks(V * sizeof(T)) < 4 ? s
     });
     float r[V];
     spread(r, at.c, P.cpg, [&](int g) { return P.rstd[(int64_t)b * P.groups + g]; });
+    if constexpr (V < 4) S.fold();
     v_mul(S.B, S.B, r);
   }
   const int c0 = blockIdx.y * width, here = min(width, P.channels - c0);
@@ -941,6 +982,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
     }
     float r[V];
     spread(r, at.c, P.cpg, [&](int g) { return P.rstd[bg + g]; });
+    if constexpr (V < 4) S.fold();
     v_mul(S.B, S.B, r);
   }
   sum_rows<V>(at, S.A, S.B, sm, P.slab, P.part_lanes, [&](int c, float2 v) { own[c] = v; });
@@ -1040,8 +1082,8 @@ constexpr int64_t kSmemMost = 200 << 10;
 size_t scratch_bytes(const Plan& p, int cpg, bool backward) {
   const int rows = kThreads / p.slab, width = p.slab * p.vec;
   size_t n = (size_t)rows * (width + 1) * 8;                          // sums
-  if (!backward) n += (size_t)width * 8 + (size_t)((width + 1) / 2) * 8;  // ch, piv
-  if (p.cluster) n += backward ? (size_t)width * 16 + (size_t)(width / cpg) * 8 : (size_t)(width / cpg) * 16;
+  if (!backward) n += (size_t)width * (sizeof(Mom) + sizeof(float));  // ch, piv
+  if (p.cluster) n += backward ? (size_t)width * 16 + (size_t)(width / cpg) * 8 : (size_t)(width / cpg) * 24;
   return (n + 15) / 16 * 16;
 }
 
@@ -1133,8 +1175,8 @@ Plan plan_of(const dit_group_norm_args& a, int vec, bool backward) {
 int64_t round256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 // Workspace of a plan: partials, then [batch, groups] pairs, then channel sums.
-int64_t part_bytes(const dit_group_norm_args& a, const Plan& p) {
-  return p.cluster ? 0 : round256(a.batch * p.splits * (int64_t)(a.channels / p.unit) * 8);
+int64_t part_bytes(const dit_group_norm_args& a, const Plan& p, bool backward) {
+  return p.cluster ? 0 : round256(a.batch * p.splits * (int64_t)(a.channels / p.unit) * (backward ? 8 : 16));
 }
 int64_t group_bytes(const dit_group_norm_args& a, const Plan& p) { return p.cluster ? 0 : round256(a.batch * a.groups * 8); }
 int64_t chan_bytes(const dit_group_norm_args& a, const Plan& p, bool backward) {
@@ -1191,7 +1233,7 @@ int64_t group_norm_workspace(const dit_group_norm_args& a, bool backward) {
   for (int vec : {16 / elem_bytes(a.dtype), 8 / elem_bytes(a.dtype), 4 / elem_bytes(a.dtype), 1}) {
     if (a.channels % vec) continue;
     const Plan p = plan_of(a, vec, backward);
-    const int64_t n = part_bytes(a, p) + group_bytes(a, p) + chan_bytes(a, p, backward);
+    const int64_t n = part_bytes(a, p, backward) + group_bytes(a, p) + chan_bytes(a, p, backward);
     if (n > need) need = n;
   }
   return need;
@@ -1229,8 +1271,9 @@ cudaError_t group_norm_run(const dit_group_norm_args& a, bool backward, float* w
   P.dw = a.dweight;
   P.db = a.dbias;
   char* ws = reinterpret_cast<char*>(workspace);
+  P.sums = reinterpret_cast<float4*>(ws);
   P.part = reinterpret_cast<float2*>(ws);
-  ws += part_bytes(a, pl);
+  ws += part_bytes(a, pl, backward);
   float* bg = reinterpret_cast<float*>(ws);
   ws += group_bytes(a, pl);
   if (!backward) {

@@ -372,13 +372,27 @@ def test_group_norm_large_mean_loses_nothing():
     near(y, ref, 1000.0, 4)
 
 
+def test_group_norm_mean_of_cancelling_channels():
+    # channels near +-1 whose group mean is 1e-4: as good as the terms' own rounding allows, not as their size
+    rng = np.random.default_rng(18)
+    for P in (50, 20000):
+        x = torch.from_numpy(np.where(np.arange(16) % 2, 1.0, -1.0) + 1e-3 * rng.standard_normal((3, P, 16)) + 1e-4).float().cuda()
+        y, mean, rstd = torch.empty_like(x), torch.empty(3, 2, device="cuda"), torch.empty(3, 2, device="cuda")
+        dit.dit_group_norm_forward(x, y, 2, mean=mean, rstd=rstd, eps=0.0)
+        ref, m, r = O.group_norm_forward(n64(x), 2, eps=0.0)
+        # deviations of 1e-3 summed in fp32, the result rounded once
+        near(mean, m, np.abs(m) + 4e-3, 1)
+
+
 def test_group_norm_non_finite_values_stay_in_their_group():
     for bad in (float("nan"), float("inf")):
         for P in (9, 5000):
             x = torch.randn(2, P, 32, device="cuda")
             x[1, P // 2, 9] = bad
-            y = torch.empty_like(x)
-            dit.dit_group_norm_forward(x, y, 4)
+            y, mean, rstd = torch.empty_like(x), torch.empty(2, 4, device="cuda"), torch.empty(2, 4, device="cuda")
+            dit.dit_group_norm_forward(x, y, 4, mean=mean, rstd=rstd)
+            off = torch.isnan(mean) if math.isnan(bad) else mean == bad
+            assert off.nonzero().tolist() == [[1, 1]] and torch.isnan(rstd).nonzero().tolist() == [[1, 1]]
             hit = torch.isnan(y).all(1)
             assert hit[1, 8:16].all() and hit.sum() == 8, (bad, P)
             assert torch.isnan(y).sum() == 8 * P
