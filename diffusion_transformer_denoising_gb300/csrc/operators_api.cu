@@ -176,7 +176,13 @@ dit_status rope_call(const dit_rope_args* a, bool backward, void* ws, int64_t ws
       }
       DIT_TRY(check_view(names[i][2], h.out, 3, size, h.out_stride, a->head_dim, elem, true));
     }
-    if (a->q.heads && a->q.out == a->k.out) return fail(DIT_ERR_INVALID_ARG, "q and k have the same output");
+    // one tensor's output in place of what the other one reads
+    if (a->q.heads && a->k.heads)
+      for (int i = 0; i < 2; ++i) {
+        const dit_rope_heads &h = *hs[i], &o = *hs[1 - i];
+        if (h.out == o.out || ((!backward || o.weight) && h.out == o.x) || (backward && h.out == o.dy))
+          return fail(DIT_ERR_INVALID_ARG, "an output of q or k is the other's input or output");
+      }
   }
   for (int i = 0; i < 2; ++i)
     if (((uintptr_t)hs[i]->weight | (uintptr_t)hs[i]->dweight) % 4)
@@ -206,6 +212,7 @@ dit_status rope_call(const dit_rope_args* a, bool backward, void* ws, int64_t ws
     drop_unused(h->x_stride, size);
     drop_unused(h->dy_stride, size);
     drop_unused(h->out_stride, size);
+    if (backward && !h->weight) h->x = nullptr;  // not read
   }
   CU_TRY(rope_run(c, backward, static_cast<float*>(ws), stream));
   return DIT_OK;

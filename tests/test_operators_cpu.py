@@ -53,6 +53,8 @@ INVALID, SHAPE = dit.DIT_ERR_INVALID_ARG, dit.DIT_ERR_SHAPE
     (dict(q=dict(HEADS, dweight=64)), INVALID), (dict(q=dict(HEADS, weight=66)), INVALID),
     (dict(k=dict(NONE, weight=64)), INVALID), (dict(k=dict(HEADS, reserved=1)), INVALID),
     (dict(k=HEADS), INVALID),                            # q and k with one output
+    (dict(k=dict(HEADS, x=8192, out=12288)), INVALID),   # k read from q's output
+    (dict(q=dict(HEADS, out=4096), k=dict(HEADS, out=12288)), INVALID),   # q in place of the input they share
 ])
 def test_rope_forward_refuses(L, kw, status):
     with pytest.raises(dit.DitError) as e:
@@ -75,6 +77,9 @@ def test_rope_backward_refuses(L):
     two = dict(g, weight=64, dweight=128)
     with pytest.raises(dit.DitError):
         dit._check(L.dit_rope_backward(rope_args(q=two, k=dict(two, out=16384)), 1024, 1 << 30, None))
+    plain = dict(g, x=0)
+    with pytest.raises(dit.DitError):                    # dk written over dq_out
+        dit._check(L.dit_rope_backward(rope_args(q=plain, k=dict(plain, dy=6144, out=2048)), 0, 0, None))
     assert L.dit_rope_workspace_bytes(rope_args(q=dict(two, heads=-3))) == -1
     assert L.dit_rope_workspace_bytes(rope_args(q=two)) == 0 < L.dit_rope_workspace_bytes(rope_args(q=two, **many))
 
