@@ -31,7 +31,7 @@
 // the sums 55 us for 328 MB of DRAM traffic (60 of them the previous output on its
 // way out), the pass 78 us for 395 MB, 80 MB of x out of L2 (reading L2 and writing
 // DRAM 5 TB/s of writes, both from DRAM 3.1, so 76 us is what that traffic takes).
-// 21 x 6240 x 384 50.1 us; gradient of 4 x 16384 x 512 52.7 us.  Blocks that each
+// 21 x 6240 x 384 50.0 us; gradient of 4 x 16384 x 512 53.0 us.  Blocks that each
 // take one range of pixels instead of turns leave only 11 MB of x in L2 (137 us);
 // register loads instead of rings 136 us; normal stores 134 us.
 #include "launch.cuh"
