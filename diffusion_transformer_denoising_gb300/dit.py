@@ -354,15 +354,16 @@ def _pixel_view(name, t, shape, dtype):
         _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous (channels last)")
     step = stride[-2]
     if len(shape) > 3:  # the middle axes as one axis of pixels
-        step, span = 0, 0
+        step = span = None  # 0 is a stride like any other (expanded views)
         for i in range(len(shape) - 2, 0, -1):
             if shape[i] == 1:
                 continue
-            if not step:
+            if step is None:
                 step = stride[i]
             elif stride[i] != span:
                 _refuse(DIT_ERR_SHAPE, f"{name}: the axes between batch and channels must have one common stride")
             span = stride[i] * shape[i]
+        step = step or 0
     return t.data_ptr(), stride[0], step
 
 

@@ -1,6 +1,8 @@
 """Refusals of the rotation and group-norm operators that need no GPU: the
 library's checks come before any launch (pointers here are never read), and
 the binding's before the library."""
+import random
+
 import pytest
 import torch
 
@@ -166,3 +168,41 @@ def test_workspace_sizes():
         assert dit.dit_group_norm_workspace_bytes(x, 32, backward) >= 0
     with pytest.raises(dit.DitError):
         dit.dit_group_norm_workspace_bytes(x, 48, False)
+
+
+def test_pixel_views_are_read_where_they_lie():
+    """Middle axes of any strides, expanded ones (stride 0) among them: either the binding's one pixel stride reaches
+    exactly the view's elements, or the view is refused."""
+    rng = random.Random(1)
+    taken = refused = 0
+    for _ in range(3000):
+        shape = [rng.choice([1, 1, 2, 3]) for _ in range(rng.choice([3, 4, 4, 5]))] + [rng.choice([1, 4])]
+        t = torch.arange(4096.0)
+        stride, span = [0] * len(shape), 1
+        for a in rng.sample(range(len(shape)), len(shape)) if rng.random() < 0.2 else reversed(range(len(shape))):
+            stride[a] = 0 if a < len(shape) - 1 and rng.random() < 0.3 else span
+            span = max(span, stride[a] * shape[a]) + (rng.choice([0, 0, 0, 2]) if a < len(shape) - 1 else 0)
+        if shape[-1] > 1 and stride[-1] != 1:
+            continue
+        v = t.as_strided(shape, stride)
+        try:
+            ptr, sb, step = dit._pixel_view("x", v, v.shape, v.dtype)
+        except dit.DitError as e:
+            assert e.status == SHAPE
+            refused += 1
+            continue
+        assert ptr == v.data_ptr()
+        pixels = v.reshape(shape[0], -1, shape[-1])
+        assert torch.equal(pixels, t.as_strided(pixels.shape, (sb, step, 1))), (shape, stride)
+        taken += 1
+    assert taken > 500 and refused > 100
+    # an image whose rows are one row repeated has two pixel strides, in either order of the axes
+    row, col = torch.zeros(2, 1, 5, 12), torch.zeros(2, 4, 1, 12)
+    dense = torch.zeros(2, 4, 5, 12)
+    for wide in (row.expand(2, 4, 5, 12), col.expand(2, 4, 5, 12)):
+        for x, y in ((wide, dense), (dense, wide)):
+            with pytest.raises(dit.DitError) as e:
+                dit.dit_group_norm_forward(x, y, 3)
+            assert e.value.status == SHAPE, e.value
+    every = torch.zeros(2, 1, 1, 12).expand(2, 4, 5, 12)      # one pixel for all: one stride, 0
+    assert dit._pixel_view("x", every, every.shape, every.dtype)[2] == 0
