@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
       new_tensor = true;
       if (g == g_last) {
         new_token = true;
-        base += step;
+        base = P.rows - base > step ? base + step : P.rows;  // the sum can pass 2^32
         token();
         g = g_first;
       } else {

@@ -631,3 +631,23 @@ def test_attention_block_of_a_latent_decoder():
         # a chain of about a dozen fp32 stages, each a few steps of 2^-24 of its terms; sums over 60 rows and 64
         # channels may lose a factor of ten to cancellation
         assert err < 12 * 16 * 10 * ULP, (i, err)
+
+
+def test_rope_in_place_at_the_most_rows():
+    # 2^31 - 1 rows on 42 groups a block: every row is turned once
+    N, d = 2**31 - 1, 48
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    if free < 2 * N * d + 2**33:
+        pytest.skip(f"{free >> 30} GB free")
+    pos = torch.ones(1, 1, dtype=torch.int32, device="cuda").expand(N, 1)
+    row = torch.linspace(-2, 2, d, device="cuda").to(torch.bfloat16)
+    want = torch.empty(1, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    dit.dit_rope_forward(pos[:1], row.expand(1, 1, 1, d), want, axes=(d,))
+    x = torch.empty(N, d, dtype=torch.bfloat16, device="cuda")
+    x.copy_(row.expand(N, d))
+    dit.dit_rope_forward(pos, x[None, :, None], x[None, :, None], axes=(d,))
+    bad = [i for i in range(0, N, 2**24) if not (x[i:i + 2**24] == want[0, 0]).all()]
+    del x
+    torch.cuda.empty_cache()
+    assert not bad, bad
