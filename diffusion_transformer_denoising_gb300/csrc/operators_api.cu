@@ -60,6 +60,100 @@ dit_status check_in_place(const char* what, const void* in, const int64_t* is, c
   return DIT_OK;
 }
 
+// The bytes that a call reads or writes through one pointer: up to three axes
+// (strides in bytes) of `last` bytes each.
+struct Region {
+  const char* what;
+  intptr_t p;
+  int n;
+  int64_t size[3], stride[3], last, span;  // span: from the first byte to the end of the last
+};
+// Whether two regions have a byte in common.  With x_k the index of a's axis k,
+// or minus that of b's, the bytes meet where sum x_k stride_k + (u - v) is the
+// distance of the pointers: strides are settled from the largest down, each x_k
+// within what the smaller ones can still make up, two values at most where
+// strides nest as views of one buffer do.  Views that nest in no way could take
+// a long search: it gives up after kSearch steps and finds no overlap then.
+struct Overlap {
+  static constexpr int kSearch = 4096;
+  int n = 0, steps = 0;
+  int64_t stride[6], lo[6], hi[6], rest_lo[7], rest_hi[7];
+
+  void axis(int64_t s, int64_t l, int64_t h) {
+    for (int k = 0; k < n; ++k)
+      if (stride[k] == s) {
+        lo[k] += l, hi[k] += h;
+        return;
+      }
+    int k = n++;
+    for (; k > 0 && stride[k - 1] < s; --k) stride[k] = stride[k - 1], lo[k] = lo[k - 1], hi[k] = hi[k - 1];
+    stride[k] = s, lo[k] = l, hi[k] = h;
+  }
+  bool meet(int k, int64_t d) {
+    if (k == n) return true;  // rest_lo[n] <= d <= rest_hi[n]
+    if (++steps > kSearch) return false;
+    const int64_t s = stride[k], from = d - rest_hi[k + 1], to = d - rest_lo[k + 1];
+    int64_t x = from / s, last = to / s;
+    if (x * s < from) ++x;
+    if (last * s > to) --last;
+    if (x < lo[k]) x = lo[k];
+    if (last > hi[k]) last = hi[k];
+    for (; x <= last && steps <= kSearch; ++x)
+      if (meet(k + 1, d - x * s)) return true;
+    return false;
+  }
+  bool operator()(const Region& a, const Region& b) {
+    for (int i = 0; i < a.n; ++i) axis(a.stride[i], 0, a.size[i] - 1);
+    for (int i = 0; i < b.n; ++i) axis(b.stride[i], -(b.size[i] - 1), 0);
+    rest_lo[n] = 1 - b.last, rest_hi[n] = a.last - 1;
+    for (int k = n - 1; k >= 0; --k) rest_lo[k] = rest_lo[k + 1] + lo[k] * stride[k], rest_hi[k] = rest_hi[k + 1] + hi[k] * stride[k];
+    const int64_t d = b.p - a.p;
+    return d >= rest_lo[0] && d <= rest_hi[0] && meet(0, d);
+  }
+};
+
+// The regions of a call.  An output has no byte in common with anything else of
+// the call, but that an activation output may be (and by check_in_place then is)
+// the view of an input that it is computed from.
+struct Regions {
+  Region r[12];
+  int n = 0;
+  uint32_t written = 0, in_place[12] = {};  // masks of regions
+  // a view of n axes (sizes, strides in elements) plus a contiguous last axis; NULL and empty ones are none
+  int add(const char* what, const void* p, int axes, const int64_t* size, const int64_t* stride, int64_t last, int elem,
+          bool output) {
+    if (!p || last == 0) return -1;
+    Region& v = r[n];
+    v.what = what;
+    v.p = reinterpret_cast<intptr_t>(p);
+    v.n = 0;
+    v.last = v.span = last * elem;
+    for (int i = 0; i < axes; ++i) {
+      if (size[i] <= 1 || stride[i] == 0) continue;  // adds no bytes
+      v.size[v.n] = size[i];
+      v.stride[v.n++] = stride[i] * elem;
+      v.span += (size[i] - 1) * stride[i] * elem;
+    }
+    if (output) written |= 1u << n;
+    return n++;
+  }
+  int add(const char* what, const void* p, int64_t bytes, bool output) { return add(what, p, 0, nullptr, nullptr, bytes, 1, output); }
+  void may_share(int out, int in) {
+    if (out >= 0 && in >= 0 && r[out].p == r[in].p) in_place[out] |= 1u << in;
+  }
+  dit_status check() const {
+    for (int i = 0; i < n; ++i) {
+      if (!(written >> i & 1)) continue;
+      const uint32_t skip = (written & ((2u << i) - 1)) | in_place[i];  // itself, and pairs looked at already
+      for (int j = 0; j < n; ++j) {
+        if (skip >> j & 1 || r[i].p >= r[j].p + r[j].span || r[j].p >= r[i].p + r[i].span) continue;
+        if (Overlap()(r[i], r[j])) return fail(DIT_ERR_INVALID_ARG, "%s overlaps %s", r[i].what, r[j].what);
+      }
+    }
+    return DIT_OK;
+  }
+};
+
 // Strides of axes with one element say nothing, whatever a view gives for them.
 template <int N>
 void drop_unused(int64_t (&stride)[N], const int64_t* size) {
@@ -176,13 +270,6 @@ dit_status rope_call(const dit_rope_args* a, bool backward, void* ws, int64_t ws
       }
       DIT_TRY(check_view(names[i][2], h.out, 3, size, h.out_stride, a->head_dim, elem, true));
     }
-    // one tensor's output in place of what the other one reads
-    if (a->q.heads && a->k.heads)
-      for (int i = 0; i < 2; ++i) {
-        const dit_rope_heads &h = *hs[i], &o = *hs[1 - i];
-        if (h.out == o.out || ((!backward || o.weight) && h.out == o.x) || (backward && h.out == o.dy))
-          return fail(DIT_ERR_INVALID_ARG, "an output of q or k is the other's input or output");
-      }
   }
   for (int i = 0; i < 2; ++i)
     if (((uintptr_t)hs[i]->weight | (uintptr_t)hs[i]->dweight) % 4)
@@ -190,6 +277,25 @@ dit_status rope_call(const dit_rope_args* a, bool backward, void* ws, int64_t ws
   if (!rows && !a->q.dweight && !a->k.dweight) return DIT_OK;
   const int64_t need = backward ? rope_workspace(*a) : 0;
   DIT_TRY(check_workspace(ws, ws_bytes, need));
+  Regions all;
+  if (rows) {
+    const int64_t psize[2] = {a->batch, a->tokens};
+    all.add("pos", a->pos, 2, psize, a->pos_stride, a->n_axes, 4, false);
+  }
+  for (int i = 0; i < 2; ++i) {
+    const dit_rope_heads& h = *hs[i];
+    const int64_t size[3] = {a->batch, a->tokens, h.heads};
+    if (rows && h.heads) {
+      const int out = all.add(names[i][2], h.out, 3, size, h.out_stride, a->head_dim, elem, true);
+      if (!backward || h.weight)
+        all.may_share(out, all.add(names[i][0], h.x, 3, size, h.x_stride, a->head_dim, elem, false));
+      if (backward) all.may_share(out, all.add(names[i][1], h.dy, 3, size, h.dy_stride, a->head_dim, elem, false));
+    }
+    all.add(i ? "k.weight" : "q.weight", h.weight, (int64_t)a->head_dim * 4, false);
+    all.add(i ? "k.dweight" : "q.dweight", h.dweight, (int64_t)a->head_dim * 4, true);
+  }
+  if (need) all.add("workspace", ws, need, true);
+  DIT_TRY(all.check());
   if (rows) {
     DIT_TRY(dev.add("pos", a->pos));
     for (int i = 0; i < 2; ++i) {
@@ -261,6 +367,21 @@ dit_status gn_call(const dit_group_norm_args* a, bool backward, void* ws, int64_
     return fail(DIT_ERR_INVALID_ARG, "weights and statistics must be aligned to 4 bytes");
   const int64_t need = group_norm_workspace(*a, backward);
   DIT_TRY(check_workspace(ws, ws_bytes, need));
+  Regions all;
+  if (some) {
+    const int out = all.add("out", a->out, 2, size, a->out_stride, a->channels, elem, true);
+    all.may_share(out, all.add("x", a->x, 2, size, a->x_stride, a->channels, elem, false));
+    if (backward) all.may_share(out, all.add("dy", a->dy, 2, size, a->dy_stride, a->channels, elem, false));
+  }
+  const int64_t per_channel = (int64_t)a->channels * 4, per_group = a->batch * a->groups * 4;
+  all.add("weight", a->weight, per_channel, false);
+  all.add("bias", a->bias, per_channel, false);
+  all.add("mean", a->mean, per_group, !backward);
+  all.add("rstd", a->rstd, per_group, !backward);
+  all.add("dweight", a->dweight, per_channel, true);
+  all.add("dbias", a->dbias, per_channel, true);
+  if (need) all.add("workspace", ws, need, true);
+  DIT_TRY(all.check());
   OnDevice dev;
   if (some) {
     DIT_TRY(dev.add("x", a->x));

@@ -240,8 +240,12 @@ dit_status flow_euler_step(float* x, const float* v, float sigma, float sigma_ne
  * ordered on the GPU, captured graphs among them.  Every pointer is a device
  * pointer of one device; the launch goes to that device whichever is current,
  * and `stream` must belong to it.  Results are the same bits from run to run.
- * An output may be the very view of an input (same pointer, same strides) and
- * otherwise overlaps none.  A size of zero is a valid call.
+ * The output `out` may be the very view (same pointer, same strides) of the x
+ * or dy it is computed from.  Apart from that no output (dweight, dbias, the
+ * forward's mean and rstd and the workspace among them) has a byte in common
+ * with an input or another output: such calls are refused.  (Views of one
+ * buffer whose strides do not nest are compared by a bounded search and may
+ * pass unseen.)  A size of zero is a valid call.
  */
 
 /* Rotary position embedding of q and k over 1 to 4 position axes (time,

@@ -206,3 +206,85 @@ def test_pixel_views_are_read_where_they_lie():
             assert e.value.status == SHAPE, e.value
     every = torch.zeros(2, 1, 1, 12).expand(2, 4, 5, 12)      # one pixel for all: one stride, 0
     assert dit._pixel_view("x", every, every.shape, every.dtype)[2] == 0
+
+
+BACK = dict(HEADS, dy=2**20, ds=(512, 64, 32), weight=2**21, dweight=2**22)
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("rope", dict(q=dict(HEADS, out=4096 + 64))),                                    # part of a row further on
+    ("rope", dict(q=HEADS, k=dict(HEADS, x=4096 + 2048, out=8192 + 2048))),          # half of q's output
+    ("rope", dict(q=dict(HEADS, weight=8192 + 3968))),                               # a weight under the output's last row
+    ("rope", dict(pos=8192 + 64)),
+    ("rope_backward", dict(q=dict(BACK, dweight=BACK["weight"]))),                   # a weight's gradient over the weight
+    ("rope_backward", dict(q=dict(BACK, dweight=BACK["weight"] + 64))),
+    ("rope_backward", dict(q=dict(BACK, dweight=BACK["dy"] + 128))),
+    ("rope_backward", dict(q=BACK, k=dict(BACK, dy=2**23, out=2**24, weight=2**25, dweight=BACK["dweight"] + 124))),
+    ("rope_backward", dict(q=dict(BACK, dweight=0), k=dict(BACK, dy=2**23, out=2**24, weight=2**25, dweight=BACK["weight"]))),
+    ("rope_backward", dict(tokens=1 << 20, batch=1, q=dict(BACK, xs=(0, 0, 32), ds=(0, 0, 32), os=(0, 64, 32), out=2**40,
+                                                         dweight=2**30 + 64))),      # inside the workspace
+    ("gn", dict(out=4096 + 48)), ("gn", dict(mean=4096)), ("gn", dict(weight=2048, rstd=2048)),
+    ("gn", dict(mean=64, rstd=84)), ("gn", dict(bias=16384 + 860, weight=128)),
+    ("gn_backward", dict(weight=2048, dweight=2048)), ("gn_backward", dict(bias=2048, dbias=2092)),
+    ("gn_backward", dict(weight=2048, dweight=512)), ("gn_backward", dict(weight=2048, dweight=536)),   # over mean, over rstd
+    ("gn_backward", dict(out=2**20 + 4)), ("gn_backward", dict(weight=2048, bias=2096, dweight=1024, dbias=1068)),
+])
+def test_outputs_that_meet_anything_else_are_refused(L, call, kw):
+    ws = 2**30, 2**20
+    with pytest.raises(dit.DitError) as e:
+        if call == "rope":
+            dit._check(L.dit_rope_forward(rope_args(**kw), None))
+        elif call == "rope_backward":
+            dit._check(L.dit_rope_backward(rope_args(**kw), *ws, None))
+        elif call == "gn":
+            dit._check(L.dit_group_norm_forward(gn_args(**kw), *ws, None))
+        else:
+            kw = {**dict(dy=2**20, ds=(108, 12), mean=512, rstd=536), **kw}
+            dit._check(L.dit_group_norm_backward(gn_args(**kw), *ws, None))
+    assert e.value.status == INVALID and "overlaps" in str(e.value), e.value
+
+
+def test_views_of_one_buffer_pass_where_they_do_not_meet(L):
+    """The library's answer against the sets of elements, for pairs of views laid into one buffer in every order."""
+    import itertools
+    rng = random.Random(2)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        batch, pixels, channels = rng.choice([1, 2, 3]), rng.choice([1, 3, 4]), rng.choice([3, 6])
+        base = rng.choice([channels, 2 * channels, 3 * channels, channels + 1])
+
+        def strides(free):
+            if free and rng.random() < 0.3:
+                return rng.choice([0, 1, channels, base]), rng.choice([0, 1, channels])
+            inner, outer = base, base * pixels + rng.choice([0, 0, channels, 1])
+            return (outer, inner) if rng.random() < 0.5 else (inner, base * batch + rng.choice([0, 0, channels]))
+
+        xs, os = strides(True), strides(False)
+        x, out = 4096 * 16, 4096 * 16 + 4 * rng.randint(-60, 60)
+        at = lambda p, st: {p // 4 + b * st[0] + i * st[1] + c for b, i, c in
+                            itertools.product(range(batch), range(pixels), range(channels))}
+        used = [s for n, s in zip((batch, pixels), os) if n > 1]
+        status = L.dit_group_norm_forward(gn_args(batch=batch, pixels=pixels, channels=channels, groups=1, x=x, xs=xs,
+                                                  out=out, os=os), 2**30, 2**20, None)
+        message = L.dit_last_error().decode()
+        if status == SHAPE:
+            assert len(at(out, os)) < batch * pixels * channels or used
+            continue
+        same = x == out and all(n == 1 or a == b for n, a, b in zip((batch, pixels), xs, os))
+        if x == out and not same:
+            assert status == INVALID
+            continue
+        meets = not same and bool(at(x, xs) & at(out, os))
+        assert ("overlaps" in message) == meets, (message, batch, pixels, channels, x, xs, out, os)
+        seen[meets] += 1
+    assert min(seen.values()) > 300, seen
+    # q and k of a packed projection written over themselves, and a large buffer's slices in any order
+    for step, heads in ((3, 0), (1, 1)):
+        H, d, N = 4, 32, 1 << 20
+        st = (N * 3 * H * d, 3 * H * d, d) if step == 3 else (3 * N * H * d, d, N * d)
+        off = H * d * 4 if step == 3 else H * N * d * 4
+        h = lambda i: dict(HEADS, heads=H, x=2**40 + i * off, out=2**40 + i * off, xs=st, os=st)
+        status = L.dit_rope_forward(rope_args(tokens=N, q=h(0), k=h(1), pos=2**20), None)
+        assert status != dit.DIT_OK and "overlaps" not in L.dit_last_error().decode()
+        status = L.dit_rope_forward(rope_args(tokens=N, q=h(0), k=dict(h(1), out=h(0)["out"] + 64), pos=2**20), None)
+        assert status == INVALID and "overlaps" in L.dit_last_error().decode()
