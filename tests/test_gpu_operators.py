@@ -651,3 +651,32 @@ def test_rope_in_place_at_the_most_rows():
     del x
     torch.cuda.empty_cache()
     assert not bad, bad
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("pixels", [2, 100, 60000], ids=["cluster", "cluster100", "streamed"])
+def test_group_norm_silu_far_from_zero_on_its_own_scale(pixels, dtype):
+    """xhat = +-1 exactly, so z = b +- w rounded once, and y = z sigma(z) to a count of steps of its own value: fp32
+    16 (the exponential 4, the reciprocal 2, seven roundings, the sum 1 + e with e's own), its derivative s + z s (1 - s)
+    (14 (1 + |z|) + 1) / |1 + z (1 - s)| < 20 for z < -8; 16 bits also 1.25 |z|, the rounding of the exponent."""
+    C = 256
+    z0 = np.linspace(-86, 40, C).astype(np.float32)
+    x = torch.ones(1, pixels, C, dtype=DT[dtype], device="cuda")
+    x[:, ::2] = -1
+    w, b = torch.full((C,), 2.0**-12, device="cuda"), torch.from_numpy(z0).cuda()
+    mean, rstd = torch.empty(1, 1, device="cuda"), torch.empty(1, 1, device="cuda")
+    y = torch.empty_like(x)
+    dit.dit_group_norm_forward(x, y, 1, weight=w, bias=b, mean=mean, rstd=rstd, eps=0.0, act=dit.ACT_SILU)
+    assert mean.item() == 0 and rstd.item() == 1
+    z = np.stack([(z0.astype(np.float64) - 2.0**-12), (z0.astype(np.float64) + 2.0**-12)]).astype(np.float32).astype(np.float64)
+    s = 1 / (1 + np.exp(-z))
+    steps = 16 + (0 if dtype == "f32" else 1.25) * np.abs(z)
+    for p in (0, 1, pixels - 2, pixels - 1):
+        near(y[0, p], (z * s)[p % 2], np.abs(z * s)[p % 2], steps[p % 2], f"y at pixel {p}")
+    if pixels > 2:
+        return
+    dw, db, dx = torch.empty(C, device="cuda"), torch.empty(C, device="cuda"), torch.empty_like(x)
+    dit.dit_group_norm_backward(x, torch.ones_like(x), mean, rstd, dx, 1, weight=w, bias=b, dweight=dw, dbias=db, act=dit.ACT_SILU)
+    low = z0 < -8
+    ref = (s * (1 + z * (1 - s))).sum(0)[low]
+    near(db[torch.from_numpy(low).cuda()], ref, np.abs(ref), 24 + (0 if dtype == "f32" else 1.25 * np.abs(z0[low])), "dbias")
