@@ -40,12 +40,12 @@ constexpr int kRopeThreads = 256;
 // ---------------------------------------------------------------- angles
 // cos and sin of u / 2^64 turns.  The remaining angle x half turns, |x| <= 1/4,
 // goes through the Taylor series of sin(pi x) and cos(pi x) about 0 (to x^9 and
-// x^10: what is cut off is below 2^-28), off by at most 1.5 x 2^-24 in all.
+// x^10: what is cut off is below 2^-28).  All 64 bits are in x, rounded once, so
+// small sines are as good as large ones: 5 x 2^-24 of themselves at most.
 DIT_DEV void turns_sincos(uint64_t u, float& c, float& s) {
-  const uint32_t hi = (uint32_t)(u >> 32);
-  const uint32_t k = (hi + 0x20000000u) >> 30;                // nearest quarter turn, 0..3
-  const int32_t rem = (int32_t)(hi - (k << 30));              // in units of 2^-32 turns, |rem| <= 2^29
-  const float x = (float)rem * 4.656612873077393e-10f, q = x * x;  // 2^-31: half turns
+  const uint32_t k = ((uint32_t)(u >> 32) + 0x20000000u) >> 30;  // nearest quarter turn, 0..3
+  const int64_t rem = (int64_t)(u - ((uint64_t)k << 62));        // in units of 2^-64 turns, |rem| <= 2^61
+  const float x = __ll2float_rn(rem) * 1.0842021724855044e-19f, q = x * x;  // 2^-63: half turns
   float sr = fmaf(q, 0.08214588661112823f, -0.5992645293207921f);
   sr = fmaf(sr, q, 2.550164039877345f);
   sr = fmaf(sr, q, -5.16771278004997f);

@@ -680,3 +680,27 @@ def test_group_norm_silu_far_from_zero_on_its_own_scale(pixels, dtype):
     low = z0 < -8
     ref = (s * (1 + z * (1 - s))).sum(0)[low]
     near(db[torch.from_numpy(low).cuda()], ref, np.abs(ref), 24 + (0 if dtype == "f32" else 1.25 * np.abs(z0[low])), "dbias")
+
+
+@pytest.mark.parametrize("style", ["interleaved", "split"])
+@pytest.mark.parametrize("kind", ["int", "float"])
+@pytest.mark.parametrize("theta", [1e4, 1e6])
+def test_rope_sine_of_small_angles_on_its_own_scale(theta, kind, style):
+    """Pairs (1, 0) turn to (cos, sin): each within 8 steps of 2^-24 of itself where it is not near 0, the sine of small
+    angles too (the angle is rounded once, then pi, a product, the polynomial's last sum)."""
+    vals = [1, 2, -3, 17, 250] if kind == "int" else [0.015625, 0.7, 1.0, -2.3, 31.9]
+    pos = torch.tensor(vals, dtype=torch.int32 if kind == "int" else torch.float32, device="cuda")[:, None]
+    d = 128
+    x = torch.zeros(1, len(vals), 2, d, device="cuda")
+    i, j = O.rope_pairs(d, style)
+    x[..., torch.from_numpy(i).cuda()] = 1
+    y = torch.empty_like(x)
+    dit.dit_rope_forward(pos, x, y, axes=(d,), theta=theta, style=STYLE[style])
+    angle = n64(pos) * float(np.float32(theta)) ** (-2.0 * np.arange(d // 2) / d)
+    ref = np.stack([np.cos(angle), np.sin(angle)], 0)[:, :, None].repeat(2, 2)
+    got = np.stack([n64(y)[0][..., i], n64(y)[0][..., j]], 0)
+    away = np.abs(ref) > np.abs(angle)[None, :, None] * 0.1     # off the zeros, where the angle's own steps count
+    assert away.mean() > 0.8
+    err = np.abs(got - ref) / np.abs(ref)
+    assert err[away].max() < 8 * ULP, err[away].max() / ULP
+    assert np.abs(got - ref).max() < 8 * ULP
