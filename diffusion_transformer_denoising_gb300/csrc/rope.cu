@@ -5,7 +5,8 @@
 // token at position pos[a] turns by the angle pos[a] * theta^(-2j/axes[a]).
 // The frequency is held in turns as a 64-bit fraction f, so the angle modulo
 // one turn is the low 64 bits of the integer product pos * f: the reduction is
-// exact however far the position (the only error is f's own, 2^-53 of it).
+// exact however far the position.  What is left is f's own error, 2^-53 of it (1 /
+// (2 pi) as a double holds it) and 2^-65: an angle a is off by |a| 2^-53 + |pos| 2^-62.
 // The top two bits pick the quadrant and the remaining +-1/8 turn goes through
 // two short polynomials.  With a norm: xhat = x r, r = (mean x^2 + eps)^-1/2, z = xhat w,
 // y = R z.  Gradient: g = R^T dy; dw = sum g xhat; with h = g w,
@@ -638,6 +639,31 @@ cudaError_t launch_layout(const RopeParams& P, int layout, int mode, dim3 grid, 
   return launch_mode<AnyPairs<T, 4>, 2>(P, mode, grid, s);
 }
 
+// A value as the sum of two doubles, good to 2^-100 of it: powers of the ratio of
+// neighbouring frequencies carry no rounding of their own into the 64 bits.
+struct Twofold {
+  double h, l;
+};
+Twofold operator*(Twofold a, Twofold b) {
+  const double p = a.h * b.h, e = fma(a.h, b.h, -p) + (a.h * b.l + a.l * b.h), h = p + e;
+  return {h, e - (h - p)};
+}
+// theta^(-1/m): pow's answer and one Newton step on r^m theta = 1.
+Twofold root(float theta, int m) {
+  const double r = pow((double)theta, -1.0 / m);
+  Twofold p{theta, 0.0}, s{r, 0.0};
+  for (int n = m; n; n >>= 1, s = s * s)
+    if (n & 1) p = p * s;
+  const double d = r * ((1.0 - p.h) - p.l) / m, h = r + d;
+  return {h, d - (h - r)};
+}
+// f < 1 in units of 2^-64, to the nearest.
+uint64_t turn_fraction(Twofold f) {
+  const double h = f.h * 0x1p64;
+  const uint64_t i = (uint64_t)h;
+  return i + (int64_t)floor((h - (double)i) + f.l * 0x1p64 + 0.5);
+}
+
 }  // namespace
 
 // At most 12 turns of a cluster of eight blocks with eight groups each: there one
@@ -662,11 +688,9 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
   P.eps = a.eps;
   P.inv_d = 1.f / (float)a.head_dim;
   for (int i = 0; i < a.n_axes; ++i) {
-    // frequencies by powers of theta^(-2/w): the j-th is off by at most j roundings
-    // of 2^-53, and shrinks faster than they add up
-    double f = 0.15915494309189533577;  // 1 / (2 pi)
-    const double r = a.axes[i] ? pow((double)a.theta, -2.0 / a.axes[i]) : 0.0;
-    for (int j = 0; j < a.axes[i] / 2; ++j, f *= r) P.turn[P.half++] = (uint64_t)ldexp(f, 64);
+    Twofold f{0.15915494309189533577, 0.0};  // 1 / (2 pi)
+    const Twofold r = a.axes[i] ? root(a.theta, a.axes[i] / 2) : f;
+    for (int j = 0; j < a.axes[i] / 2; ++j, f = f * r) P.turn[P.half++] = turn_fraction(f);
     P.ends[i] = P.half;
   }
 

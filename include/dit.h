@@ -258,9 +258,12 @@ dit_status flow_euler_step(float* x, const float* v, float sigma, float sigma_ne
  * position pos[a] turns by pos[a] * theta^(-2 j / axes[a]).  Pair p is
  * channels (2p, 2p + 1) with DIT_ROPE_INTERLEAVED, (p, p + R / 2) with
  * DIT_ROPE_SPLIT; (a, b) -> (a cos - b sin, a sin + b cos).  Channels from R
- * on are not turned.  Angles are reduced exactly (64-bit fixed-point turns),
- * so far positions lose nothing.  With a weight w[head_dim] the head x is
- * first x * w / sqrt(mean(x^2) + eps), the mean over the whole head.
+ * on are not turned.  The angle pos * frequency is reduced exactly (64-bit
+ * fixed-point turns); the frequency is good to 2^-53 of it and 2^-62, so an
+ * angle a is off by at most |a| 2^-53 + |pos| 2^-62 radians: cos and sin have
+ * fp32 accuracy at every int32 position, 1e-4 at 2^40, none from 2^53 on.
+ * With a weight w[head_dim] the head x is first x * w / sqrt(mean(x^2) + eps),
+ * the mean over the whole head.
  * Arithmetic is fp32, rounded once to the activation type.  */
 enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_SPLIT = 1 };
 enum { DIT_ROPE_MAX_AXES = 4, DIT_ROPE_MAX_HEAD_DIM = 256 };
@@ -294,7 +297,7 @@ typedef struct {
   float eps;             /* >= 0                                                        */
   const void* pos;       /* device [batch, tokens, n_axes], last axis contiguous        */
   int64_t pos_stride[2]; /* batch (0: shared by the batch) and token strides, elements  */
-  int32_t pos_dtype;     /* DIT_POS_I32, or DIT_POS_F32 (exact for any finite value)    */
+  int32_t pos_dtype;     /* DIT_POS_I32, or DIT_POS_F32 (finite; else that token is NaN)  */
   int32_t reserved;      /* 0                                                           */
   dit_rope_heads q, k;   /* their head counts are independent                           */
 } dit_rope_args;

@@ -704,3 +704,30 @@ def test_rope_sine_of_small_angles_on_its_own_scale(theta, kind, style):
     err = np.abs(got - ref) / np.abs(ref)
     assert err[away].max() < 8 * ULP, err[away].max() / ULP
     assert np.abs(got - ref).max() < 8 * ULP
+
+
+PI = "3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803"
+
+
+@pytest.mark.parametrize("kind", ["int", "float"])
+@pytest.mark.parametrize("theta,axes", [(5.0, (256,)), (100.0, (256,)), (1e4, (256,)), (1.25, (64, 192)), (1e4, (44, 42, 42))])
+def test_rope_far_positions_against_the_mathematical_angle(theta, axes, kind):
+    """Angles in 80 decimal digits.  8 steps of 2^-24 in cos and sin, and the frequency's 2^-53 of an angle below 2^31
+    (2^-22, 4 steps)."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 80
+    vals = [2**31 - 1, -2**31, 2**30 + 12345, 987654321, -1234567] if kind == "int" else \
+        [2.0**31, -9e8, 1.5e6 + 0.125, 123456.789, -2.0**30]
+    pos = torch.tensor(vals, dtype=torch.int32 if kind == "int" else torch.float32, device="cuda")[:, None].repeat(1, len(axes))
+    d = sum(axes)
+    x = torch.zeros(1, len(vals), 1, d, device="cuda")
+    x[..., ::2] = 1
+    y = torch.empty_like(x)
+    dit.dit_rope_forward(pos, x, y, axes=axes, theta=theta)
+    turn, ref = 2 * Decimal(PI), np.empty((len(vals), d // 2, 2))
+    freq = [Decimal(theta) ** (Decimal(-2 * j) / w) for w in axes for j in range(w // 2)]
+    for i, v in enumerate(pos[:, 0].tolist()):
+        for j, f in enumerate(freq):
+            a = float((Decimal(v) * f) % turn)
+            ref[i, j] = math.cos(a), math.sin(a)
+    near(y[0, :, 0], ref.reshape(len(vals), d), 1.0, 12, "cos and sin")
