@@ -389,12 +389,6 @@ DIT_DEV float warp_sum(float v) {
   return v;
 }
 
-// a + b = high + low exactly (Knuth).
-DIT_DEV float two_sum(float a, float b, float& low) {
-  const float h = a + b, t = h - a;
-  low = (a - (h - t)) + (b - t);
-  return h;
-}
 // A mean as the unevaluated sum of two floats, and the second moment about it.
 struct Mom {
   float mean, low, M;

@@ -322,9 +322,33 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   bool turned[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) turned[i] = lay.has(i) && lay.pair(i) < P.half;
-  float2 da[N2], db[N2];  // the gradient's sums: a block takes one tensor only
+  // the gradient's sums (a block takes one tensor only): of the last rows in
+  // registers, of all before in shared memory, a pair of channels as (high, low)
+  // twice, so that the sum of many rows is as good as that of kFoldRows
+  constexpr int kFoldRows = 32;
+  [[maybe_unused]] __shared__ float4 total[GRAD ? NP : 1][GRAD ? kRopeThreads : 1];
+  [[maybe_unused]] int since = 0;
+  float2 da[N2], db[N2];
 #pragma unroll
   for (int i = 0; i < N2; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
+  if constexpr (GRAD)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) total[i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&] {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float4 t = total[i][threadIdx.x];
+      float low;
+      t.x = two_sum(t.x, i & 1 ? da[i / 2].y : da[i / 2].x, low);
+      t.y += low;
+      t.z = two_sum(t.z, i & 1 ? db[i / 2].y : db[i / 2].x, low);
+      t.w += low;
+      total[i][threadIdx.x] = t;
+    }
+#pragma unroll
+    for (int i = 0; i < N2; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
+    since = 0;
+  };
 
   // the slice's heads of each tensor
   const auto first_head = [&](int g) { return (int)(P.seg[g].heads * blockIdx.y / gridDim.y); };
@@ -384,148 +408,152 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
   // the loop runs while any group of the block has a row: lanes of a warp stay
   // together for the shuffles
   while (base < P.rows) {
-    if (new_token) {
-      cp_async_wait();
+    do {  // the gradient leaves after kFoldRows rows; an if around fold() in here cost 3 us of 120
+      if (new_token) {
+        cp_async_wait();
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        float c = 1.f, s = 0.f;
-        if (turned[i]) {
-          const uint64_t f = turn[lay.pair(i)];
-          const int32_t at = where[i][threadIdx.x];
-          if (P.pos_f32) {
-            turns_sincos(turns_of(__int_as_float(at), f), c, s);
-            if (!finite_bits(__int_as_float(at))) c = s = __int_as_float(0x7FFFFFFF);
-          } else {
-            turns_sincos((uint64_t)(int64_t)at * f, c, s);
+        for (int i = 0; i < NP; ++i) {
+          float c = 1.f, s = 0.f;
+          if (turned[i]) {
+            const uint64_t f = turn[lay.pair(i)];
+            const int32_t at = where[i][threadIdx.x];
+            if (P.pos_f32) {
+              turns_sincos(turns_of(__int_as_float(at), f), c, s);
+              if (!finite_bits(__int_as_float(at))) c = s = __int_as_float(0x7FFFFFFF);
+            } else {
+              turns_sincos((uint64_t)(int64_t)at * f, c, s);
+            }
+            if (P.negate) s = -s;
           }
-          if (P.negate) s = -s;
+          spin[i][threadIdx.x] = make_float2(c, s);
         }
-        spin[i][threadIdx.x] = make_float2(c, s);
       }
-    }
-    if (new_tensor) {
+      if (new_tensor) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 cs = spin[i][threadIdx.x];
-        float va = 1.f, vb = 1.f;
-        if constexpr (MODE != ROPE_TURN) {
-          const float2 w = lay.has(i) ? weight[g][lay.pair(i)] : make_float2(0.f, 0.f);
-          va = w.x, vb = w.y;
+        for (int i = 0; i < NP; ++i) {
+          const float2 cs = spin[i][threadIdx.x];
+          float va = 1.f, vb = 1.f;
+          if constexpr (MODE != ROPE_TURN) {
+            const float2 w = lay.has(i) ? weight[g][lay.pair(i)] : make_float2(0.f, 0.f);
+            va = w.x, vb = w.y;
+          }
+          const float m0 = MODE == ROPE_NORM ? cs.x * va : cs.x, m1 = MODE == ROPE_NORM ? -cs.y * vb : -cs.y;
+          const float m2 = MODE == ROPE_NORM ? cs.y * va : cs.y, m3 = MODE == ROPE_NORM ? cs.x * vb : cs.x;
+          if (i & 1) k0[i / 2].y = m0, k1[i / 2].y = m1, k2[i / 2].y = m2, k3[i / 2].y = m3, wa[i / 2].y = va, wb[i / 2].y = vb;
+          else k0[i / 2].x = m0, k1[i / 2].x = m1, k2[i / 2].x = m2, k3[i / 2].x = m3, wa[i / 2].x = va, wb[i / 2].x = vb;
         }
-        const float m0 = MODE == ROPE_NORM ? cs.x * va : cs.x, m1 = MODE == ROPE_NORM ? -cs.y * vb : -cs.y;
-        const float m2 = MODE == ROPE_NORM ? cs.y * va : cs.y, m3 = MODE == ROPE_NORM ? cs.x * vb : cs.x;
-        if (i & 1) k0[i / 2].y = m0, k1[i / 2].y = m1, k2[i / 2].y = m2, k3[i / 2].y = m3, wa[i / 2].y = va, wb[i / 2].y = vb;
-        else k0[i / 2].x = m0, k1[i / 2].x = m1, k2[i / 2].x = m2, k3[i / 2].x = m3, wa[i / 2].x = va, wb[i / 2].x = vb;
       }
-    }
-    // this batch's rows out of the load registers, and the next batch's loads
-    typename L::RowRaw cx[HU], cg[GRAD ? HU : 1];
+      // this batch's rows out of the load registers, and the next batch's loads
+      typename L::RowRaw cx[HU], cg[GRAD ? HU : 1];
 #pragma unroll
-    for (int u = 0; u < HU; ++u) {
-      cx[u] = rx[u];
-      if constexpr (GRAD) cg[u] = rg[u];
-    }
-    const bool row_ok = ok;
-    T* const to = out;
-    const int64_t to_step = P.seg[g].os[2];
-    const int left = min(h1 - h, HU);
-    h += HU;
-    out += HU * to_step;
-    new_tensor = new_token = false;
-    if (h >= h1) {
-      new_tensor = true;
-      if (g == g_last) {
-        new_token = true;
-        base = P.rows - base > step ? base + step : P.rows;  // the sum can pass 2^32
-        token();
-        g = g_first;
-      } else {
-        g = 1;
+      for (int u = 0; u < HU; ++u) {
+        cx[u] = rx[u];
+        if constexpr (GRAD) cg[u] = rg[u];
       }
-      tensor();
-    }
-    if (base < P.rows) load();
-    // N rows of the batch at once, their chains of latency side by side; MIX:
-    // some of the lane's channels are not turned
-    auto rows = [&](auto first_, auto n_, auto mix_) {
-      constexpr int N = decltype(n_)::value, first = decltype(first_)::value;
-      constexpr bool MIX = decltype(mix_)::value;
-      [[maybe_unused]] float2 a[N][N2], e[N][N2];
-      float2 ya[N][N2], yb[N][N2];
-      float ss[N], dot[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float af[NP], bf[NP];
-        lay.values(cx[first + j], af, bf);
-        float2 q = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < N2; ++i) {
-          const float2 va = make_float2(af[2 * i], af[2 * i + 1]), vb = make_float2(bf[2 * i], bf[2 * i + 1]);
-          if constexpr (MODE != ROPE_TURN) q = fma2(vb, vb, fma2(va, va, q));
-          if constexpr (GRAD) a[j][i] = va, e[j][i] = vb;
-          else turn_pair<MIX>(va, vb, k0[i], k1[i], k2[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
+      const bool row_ok = ok;
+      T* const to = out;
+      const int64_t to_step = P.seg[g].os[2];
+      const int left = min(h1 - h, HU);
+      h += HU;
+      out += HU * to_step;
+      new_tensor = new_token = false;
+      if (h >= h1) {
+        new_tensor = true;
+        if (g == g_last) {
+          new_token = true;
+          base = P.rows - base > step ? base + step : P.rows;  // the sum can pass 2^32
+          token();
+          g = g_first;
+        } else {
+          g = 1;
         }
-        if constexpr (GRAD) {
-          lay.values(cg[first + j], af, bf);
+        tensor();
+      }
+      if (base < P.rows) load();
+      // N rows of the batch at once, their chains of latency side by side; MIX:
+      // some of the lane's channels are not turned
+      auto rows = [&](auto first_, auto n_, auto mix_) {
+        constexpr int N = decltype(n_)::value, first = decltype(first_)::value;
+        constexpr bool MIX = decltype(mix_)::value;
+        [[maybe_unused]] float2 a[N][N2], e[N][N2];
+        float2 ya[N][N2], yb[N][N2];
+        float ss[N], dot[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float af[NP], bf[NP];
+          lay.values(cx[first + j], af, bf);
+          float2 q = make_float2(0.f, 0.f), dt = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
             const float2 va = make_float2(af[2 * i], af[2 * i + 1]), vb = make_float2(bf[2 * i], bf[2 * i + 1]);
-            turn_pair<MIX>(va, vb, k0[i], k2[i], k1[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
-            dt = fma2(mul2(ya[j][i], wa[i]), a[j][i], dt);
-            dt = fma2(mul2(yb[j][i], wb[i]), e[j][i], dt);
+            if constexpr (MODE != ROPE_TURN) q = fma2(vb, vb, fma2(va, va, q));
+            if constexpr (GRAD) a[j][i] = va, e[j][i] = vb;
+            else turn_pair<MIX>(va, vb, k0[i], k1[i], k2[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
           }
-        }
-        ss[j] = q.x + q.y;
-        dot[j] = dt.x + dt.y;
-      }
-      if constexpr (MODE != ROPE_TURN) {
-        group_sums<N>(ss, lane, P.slots);
-        if constexpr (GRAD) group_sums<N>(dot, lane, P.slots);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float r = rsqrtf(fmaf(ss[j], P.inv_d, P.eps));
-          const float2 r2 = make_float2(r, r);
-          if constexpr (!GRAD) {
-#pragma unroll
-            for (int i = 0; i < N2; ++i) ya[j][i] = mul2(ya[j][i], r2), yb[j][i] = mul2(yb[j][i], r2);
-          } else {
-            const float m = -dot[j] * r * r * r * P.inv_d;  // dx = r (g w) - x r^3 mean(g w x)
-            const float2 m2 = make_float2(m, m);
+          if constexpr (GRAD) {
+            lay.values(cg[first + j], af, bf);
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-              const float2 ga = mul2(ya[j][i], r2), gb = mul2(yb[j][i], r2);
-              if (row_ok) da[i] = fma2(ga, a[j][i], da[i]), db[i] = fma2(gb, e[j][i], db[i]);
-              ya[j][i] = fma2(a[j][i], m2, mul2(ga, wa[i]));
-              yb[j][i] = fma2(e[j][i], m2, mul2(gb, wb[i]));
+              const float2 va = make_float2(af[2 * i], af[2 * i + 1]), vb = make_float2(bf[2 * i], bf[2 * i + 1]);
+              turn_pair<MIX>(va, vb, k0[i], k2[i], k1[i], k3[i], turned[2 * i], turned[2 * i + 1], ya[j][i], yb[j][i]);
+              dt = fma2(mul2(ya[j][i], wa[i]), a[j][i], dt);
+              dt = fma2(mul2(yb[j][i], wb[i]), e[j][i], dt);
+            }
+          }
+          ss[j] = q.x + q.y;
+          dot[j] = dt.x + dt.y;
+        }
+        if constexpr (MODE != ROPE_TURN) {
+          group_sums<N>(ss, lane, P.slots);
+          if constexpr (GRAD) group_sums<N>(dot, lane, P.slots);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float r = rsqrtf(fmaf(ss[j], P.inv_d, P.eps));
+            const float2 r2 = make_float2(r, r);
+            if constexpr (!GRAD) {
+#pragma unroll
+              for (int i = 0; i < N2; ++i) ya[j][i] = mul2(ya[j][i], r2), yb[j][i] = mul2(yb[j][i], r2);
+            } else {
+              const float m = -dot[j] * r * r * r * P.inv_d;  // dx = r (g w) - x r^3 mean(g w x)
+              const float2 m2 = make_float2(m, m);
+#pragma unroll
+              for (int i = 0; i < N2; ++i) {
+                const float2 ga = mul2(ya[j][i], r2), gb = mul2(yb[j][i], r2);
+                if (row_ok) da[i] = fma2(ga, a[j][i], da[i]), db[i] = fma2(gb, e[j][i], db[i]);
+                ya[j][i] = fma2(a[j][i], m2, mul2(ga, wa[i]));
+                yb[j][i] = fma2(e[j][i], m2, mul2(gb, wb[i]));
+              }
             }
           }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float af[NP], bf[NP];
+        for (int j = 0; j < N; ++j) {
+          float af[NP], bf[NP];
 #pragma unroll
-        for (int i = 0; i < N2; ++i)
-          af[2 * i] = ya[j][i].x, af[2 * i + 1] = ya[j][i].y, bf[2 * i] = yb[j][i].x, bf[2 * i + 1] = yb[j][i].y;
-        if (row_ok) lay.store(to + (first + j) * to_step, af, bf);
-      }
-    };
-    // side by side only where two blocks an SM leave the registers for it
-    constexpr int kSide = GRAD && HU > 1 ? 2 : 1;
-    auto batch = [&](auto side_, auto mix, int n) {  // the first n rows, side_ at once
-      constexpr int N = decltype(side_)::value;
-      static_assert(HU <= 4 * N);
-      rows(Int<0>{}, Int<N>{}, mix);
-      if constexpr (HU >= 2 * N)
-        if (n > N) rows(Int<N>{}, Int<N>{}, mix);
-      if constexpr (HU >= 3 * N)
-        if (n > 2 * N) rows(Int<2 * N>{}, Int<N>{}, mix);
-      if constexpr (HU >= 4 * N)
-        if (n > 3 * N) rows(Int<3 * N>{}, Int<N>{}, mix);
-    };
-    if (left < HU) batch(Int<1>{}, std::true_type{}, left);
-    else if (partial) batch(Int<kSide>{}, std::true_type{}, HU);
-    else batch(Int<kSide>{}, std::false_type{}, HU);
+          for (int i = 0; i < N2; ++i)
+            af[2 * i] = ya[j][i].x, af[2 * i + 1] = ya[j][i].y, bf[2 * i] = yb[j][i].x, bf[2 * i + 1] = yb[j][i].y;
+          if (row_ok) lay.store(to + (first + j) * to_step, af, bf);
+        }
+      };
+      // side by side only where two blocks an SM leave the registers for it
+      constexpr int kSide = GRAD && HU > 1 ? 2 : 1;
+      auto batch = [&](auto side_, auto mix, int n) {  // the first n rows, side_ at once
+        constexpr int N = decltype(side_)::value;
+        static_assert(HU <= 4 * N);
+        rows(Int<0>{}, Int<N>{}, mix);
+        if constexpr (HU >= 2 * N)
+          if (n > N) rows(Int<N>{}, Int<N>{}, mix);
+        if constexpr (HU >= 3 * N)
+          if (n > 2 * N) rows(Int<2 * N>{}, Int<N>{}, mix);
+        if constexpr (HU >= 4 * N)
+          if (n > 3 * N) rows(Int<3 * N>{}, Int<N>{}, mix);
+      };
+      if (left < HU) batch(Int<1>{}, std::true_type{}, left);
+      else if (partial) batch(Int<kSide>{}, std::true_type{}, HU);
+      else batch(Int<kSide>{}, std::false_type{}, HU);
+      since += left;
+    } while (base < P.rows && (!GRAD || since < kFoldRows));
+    if constexpr (GRAD) fold();
   }
 
   cp_async_wait();  // nothing of a token that never came is left on its way
@@ -540,8 +568,9 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (spare) continue;
-        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = i & 1 ? da[i / 2].y : da[i / 2].x;
-        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = i & 1 ? db[i / 2].y : db[i / 2].x;
+        const float4 t = total[i][threadIdx.x];
+        if (lay.has(i)) sm[group * P.d + lay.chan_a(i)] = finite_bits(t.x) ? t.x + t.y : t.x;
+        if (lay.has_b(i)) sm[group * P.d + lay.chan_b(i)] = finite_bits(t.z) ? t.z + t.w : t.z;
       }
       __syncthreads();
       const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;

@@ -1,6 +1,6 @@
 // Typed 8-element and single-element accesses of the operators on fp32, bf16
 // and fp16 activations: values are fp32 in registers, rounded once (to
-// nearest even) when they are stored.
+// nearest even) when they are stored.  And the exact sum of two floats.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -10,6 +10,13 @@
 #include "common.cuh"
 
 namespace dit {
+
+// a + b = high + low exactly (Knuth).
+DIT_DEV float two_sum(float a, float b, float& low) {
+  const float h = a + b, t = h - a;
+  low = (a - (h - t)) + (b - t);
+  return h;
+}
 
 DIT_DEV float to_f32(float v) { return v; }
 DIT_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

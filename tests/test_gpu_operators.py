@@ -731,3 +731,24 @@ def test_rope_far_positions_against_the_mathematical_angle(theta, axes, kind):
             a = float((Decimal(v) * f) % turn)
             ref[i, j] = math.cos(a), math.sin(a)
     near(y[0, :, 0], ref.reshape(len(vals), d), 1.0, 12, "cos and sin")
+
+
+@pytest.mark.parametrize("layout", ["tokens", "odd"])
+def test_rope_weight_gradient_of_very_many_rows(layout):
+    """One row 2.56 million times: equal terms, whose roundings do not cancel.  The bound is a sum of 33 rows, joined
+    without loss, then 8 groups of a block, 10 partials a warp and 32 warps, and the term's own steps."""
+    N, H, d = 40000, 64, 256
+    rng = np.random.default_rng(21)
+    x, dy = views(rng, layout, 1, 1, 1, d, "bf16"), views(rng, layout, 1, 1, 1, d, "bf16")
+    pos, w = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), weights(rng, d)
+    dx, dw = torch.empty(1, N, H, d, dtype=torch.bfloat16, device="cuda"), torch.empty(d, device="cuda")
+    dit.dit_rope_backward(pos.expand(N, 1), dy.expand(1, N, H, d), dx, axes=(d,), q=x.expand(1, N, H, d), q_weight=w,
+                          dq_weight=dw, eps=1e-6)
+    _, ref = O.rope_backward(n64(dy), n64(pos), (d,), x=n64(x), weight=n64(w), eps=1e-6)
+    near(dw, N * H * ref, N * H * np.abs(ref), 33 + 8 + 10 + 32 + RSTEPS, "weight gradient")
+    # infinite terms stay where they are
+    x = x.clone()
+    dy = dy.clone()
+    dy[..., 5] = float("inf")
+    dit.dit_rope_backward(pos, dy, dx[:, :1, :1], axes=(d,), q=x, q_weight=w, dq_weight=dw, eps=1e-6)
+    assert not torch.isfinite(dw[5]) and torch.isfinite(dw[6:]).all()
