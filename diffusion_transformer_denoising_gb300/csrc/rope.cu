@@ -6,7 +6,7 @@
 // The frequency is held in turns as a 64-bit fraction f, so the angle modulo
 // one turn is the low 64 bits of the integer product pos * f: the reduction is
 // exact however far the position.  What is left is f's own error, 2^-53 of it (1 /
-// (2 pi) as a double holds it) and 2^-65: an angle a is off by |a| 2^-53 + |pos| 2^-62.
+// (2 pi) as a double holds it) and 2^-58: an angle a is off by |a| 2^-53 + |pos| 2^-55.
 // The top two bits pick the quadrant and the remaining +-1/8 turn goes through
 // two short polynomials.  With a norm: xhat = x r, r = (mean x^2 + eps)^-1/2, z = xhat w,
 // y = R z.  Gradient: g = R^T dy; dw = sum g xhat; with h = g w,
@@ -668,8 +668,7 @@ cudaError_t launch_layout(const RopeParams& P, int layout, int mode, dim3 grid, 
   return launch_mode<AnyPairs<T, 4>, 2>(P, mode, grid, s);
 }
 
-// A value as the sum of two doubles, good to 2^-100 of it: powers of the ratio of
-// neighbouring frequencies carry no rounding of their own into the 64 bits.
+// A value as the sum of two doubles, good to 2^-100 of it.
 struct Twofold {
   double h, l;
 };
@@ -686,11 +685,12 @@ Twofold root(float theta, int m) {
   const double d = r * ((1.0 - p.h) - p.l) / m, h = r + d;
   return {h, d - (h - r)};
 }
-// f < 1 in units of 2^-64, to the nearest.
-uint64_t turn_fraction(Twofold f) {
-  const double h = f.h * 0x1p64;
+// r <= 1 in units of 2^-64, to the nearest (1 itself one unit less).
+uint64_t fraction(Twofold r) {
+  if (r.h >= 1.0) return UINT64_MAX;
+  const double h = r.h * 0x1p64;
   const uint64_t i = (uint64_t)h;
-  return i + (int64_t)floor((h - (double)i) + f.l * 0x1p64 + 0.5);
+  return i + (int64_t)floor((h - (double)i) + r.l * 0x1p64 + 0.5);
 }
 
 }  // namespace
@@ -717,9 +717,14 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
   P.eps = a.eps;
   P.inv_d = 1.f / (float)a.head_dim;
   for (int i = 0; i < a.n_axes; ++i) {
-    Twofold f{0.15915494309189533577, 0.0};  // 1 / (2 pi)
-    const Twofold r = a.axes[i] ? root(a.theta, a.axes[i] / 2) : f;
-    for (int j = 0; j < a.axes[i] / 2; ++j, f = f * r) P.turn[P.half++] = turn_fraction(f);
+    // powers of the neighbours' ratio in 64-bit fractions: half a unit of 2^-64 a step,
+    // which shrink with the frequencies (128 pairs: below 64 units whatever theta)
+    uint64_t f = (uint64_t)(0.15915494309189533577 * 0x1p64);  // 1 / (2 pi)
+    const uint64_t r = a.axes[i] > 2 ? fraction(root(a.theta, a.axes[i] / 2)) : 0;
+    for (int j = 0; j < a.axes[i] / 2; ++j) {
+      P.turn[P.half++] = f;
+      f = (uint64_t)(((unsigned __int128)f * r + (1ull << 63)) >> 64);
+    }
     P.ends[i] = P.half;
   }
 

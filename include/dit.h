@@ -259,8 +259,8 @@ dit_status flow_euler_step(float* x, const float* v, float sigma, float sigma_ne
  * channels (2p, 2p + 1) with DIT_ROPE_INTERLEAVED, (p, p + R / 2) with
  * DIT_ROPE_SPLIT; (a, b) -> (a cos - b sin, a sin + b cos).  Channels from R
  * on are not turned.  The angle pos * frequency is reduced exactly (64-bit
- * fixed-point turns); the frequency is good to 2^-53 of it and 2^-62, so an
- * angle a is off by at most |a| 2^-53 + |pos| 2^-62 radians: cos and sin have
+ * fixed-point turns); the frequency is good to 2^-53 of itself + 2^-55, so an
+ * angle a is off by at most |a| 2^-53 + |pos| 2^-55 radians: cos and sin have
  * fp32 accuracy at every int32 position, 1e-4 at 2^40, none from 2^53 on.
  * With a weight w[head_dim] the head x is first x * w / sqrt(mean(x^2) + eps),
  * the mean over the whole head.
