@@ -182,14 +182,16 @@ def flow_euler_step(x, v, sigma: float, sigma_next: float, n: int, stream=None):
 _ROPE_ARGS = struct.Struct("<2q8i2fQ2q2i" + 2 * "2iQ3qQ3qQ3q2Q")
 _GN_ARGS = struct.Struct("<2q4ifiQ2qQ2qQ2q6Q")
 _NO_VIEW = (0, 0, 0, 0)
-_torch = None          # the module, and its dtypes as dit.h names them, on first use
+_torch = None          # the module, its dtypes as dit.h names them and its grad mode, on first use
 _dtype_codes = {}
+_grad_mode = None
 
 
 def _use_torch():
-    global _torch
+    global _torch, _grad_mode
     if _torch is None:
         import torch
+        _grad_mode = torch.is_grad_enabled
         _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
         _torch = torch
     return _torch
@@ -215,6 +217,13 @@ def _param(name, t, shape):
     if t.shape != shape or not t.is_contiguous():
         _refuse(DIT_ERR_SHAPE, f"{name}: weights and statistics must be contiguous, here {list(shape)}")
     return t.data_ptr()
+
+
+def _refuse_autograd():
+    """The calls write into the tensors they are given and record nothing, so inputs that autograd waits for a gradient
+    of are refused."""
+    _refuse(DIT_ERR_INVALID_ARG, "a tensor requires grad: autograd does not see this call (run it under torch.no_grad(), "
+                                 "or inside a torch.autograd.Function with the backward call)")
 
 
 def _raw_stream(t, stream):
@@ -279,6 +288,11 @@ def _rope_heads(tag, x, dy, out, weight, dweight, B, N, d, dtype):
 
 def _rope_args(pos, axes, theta, style, eps, first, q, k):
     torch = _torch or _use_torch()
+    if _grad_mode():
+        for x, dy, _, weight, _ in (q, k):
+            if (x is not None and x.requires_grad or weight is not None and weight.requires_grad or
+                    dy is not None and dy.requires_grad):
+                _refuse_autograd()
     if first.dim() != 4:
         _refuse(DIT_ERR_SHAPE, "q must be [batch, tokens, heads, head_dim]")
     B, N, _, d = first.shape
@@ -306,7 +320,9 @@ def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, styl
     pos: int32 or float32 [tokens, len(axes)], or [batch, tokens, len(axes)];
     axes: rotary channels per axis; q_out / k_out may be q / k themselves.
     Views may have any strides with contiguous heads; k may have its own
-    number of heads (see dit_rope_forward in include/dit.h)."""
+    number of heads (see dit_rope_forward in include/dit.h).  Nothing is
+    recorded for autograd, so with grad mode on an input that requires grad is
+    refused, here and in the calls below."""
     args = _rope_args(pos, axes, theta, style, eps, q, (q, None, q_out, q_weight, None),
                       (k, None, k_out, k_weight, None))
     status = lib().dit_rope_forward(args, _raw_stream(q, stream))
@@ -369,6 +385,9 @@ def _pixel_view(name, t, shape, dtype):
 
 def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, act):
     _torch or _use_torch()
+    if _grad_mode() and (x.requires_grad or weight is not None and weight.requires_grad or
+                         bias is not None and bias.requires_grad or dy is not None and dy.requires_grad):
+        _refuse_autograd()
     shape, dtype = x.shape, x.dtype
     if len(shape) < 3:
         _refuse(DIT_ERR_SHAPE, "x must be [batch, ..., channels]")

@@ -288,3 +288,42 @@ def test_views_of_one_buffer_pass_where_they_do_not_meet(L):
         assert status != dit.DIT_OK and "overlaps" not in L.dit_last_error().decode()
         status = L.dit_rope_forward(rope_args(tokens=N, q=h(0), k=dict(h(1), out=h(0)["out"] + 64), pos=2**20), None)
         assert status == INVALID and "overlaps" in L.dit_last_error().decode()
+
+
+def test_tensors_that_require_grad_are_refused_unless_grad_mode_is_off():
+    z = torch.zeros
+    pos, q, w = z(8, 2, dtype=torch.int32), z(2, 8, 3, 32), z(32)
+    x, st, c = z(2, 5, 12), z(2, 3), z(12)
+    calls = [lambda q, w, x, st, c: dit.dit_rope_forward(pos, q, q, axes=(16, 16), q_weight=w),
+             lambda q, w, x, st, c: dit.dit_rope_backward(pos, q, q, axes=(16, 16), q=q, q_weight=w, dq_weight=z(32)),
+             lambda q, w, x, st, c: dit.dit_group_norm_forward(x, x, 3, weight=c, bias=c),
+             lambda q, w, x, st, c: dit.dit_group_norm_backward(x, x, st, st.clone(), x, 3, weight=c)]
+    for n, call in enumerate(calls):
+        args = (q, w, x, st, c)
+        for i in (0, 1) if n < 2 else (2, 4):
+            with_grad = list(args)
+            with_grad[i] = args[i].clone().requires_grad_()
+            with pytest.raises(dit.DitError) as e:
+                call(*with_grad)
+            assert e.value.status == INVALID and "autograd" in str(e.value)
+            with torch.no_grad(), pytest.raises(dit.DitError) as e:      # refused for its device only
+                call(*with_grad)
+            assert "CUDA" in str(e.value)
+    seen = []
+
+    class Turn(torch.autograd.Function):                                 # how a program gives the operator to autograd
+        @staticmethod
+        def forward(ctx, q):
+            seen.append(torch.is_grad_enabled())
+            with pytest.raises(dit.DitError) as e:
+                calls[0](q, w, x, st, c)
+            assert "CUDA" in str(e.value)
+            return q * 2
+
+        @staticmethod
+        def backward(ctx, dy):
+            seen.append(torch.is_grad_enabled())
+            return dy
+
+    Turn.apply(q.clone().requires_grad_()).sum().backward()
+    assert seen == [False, False]
