@@ -351,8 +351,8 @@ dit_status dit_group_norm_forward(const dit_group_norm_args* a, void* workspace,
 dit_status dit_group_norm_backward(const dit_group_norm_args* a, void* workspace, int64_t workspace_bytes,
                                    void* stream);
 /* Bytes of workspace of the forward (backward == 0) or the backward call
- * (host-only query, from the sizes, type, strides and alignment); -1 for
- * arguments the call would refuse. */
+ * (host-only query, from the sizes and the type alone: enough for any strides
+ * and alignment); -1 for arguments the call would refuse. */
 int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backward);
 
 /* The whole denoiser stage for `batch` requests: the denoiser role of

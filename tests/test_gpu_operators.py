@@ -752,3 +752,61 @@ def test_rope_weight_gradient_of_very_many_rows(layout):
     dy[..., 5] = float("inf")
     dit.dit_rope_backward(pos, dy, dx[:, :1, :1], axes=(d,), q=x, q_weight=w, dq_weight=dw, eps=1e-6)
     assert not torch.isfinite(dw[5]) and torch.isfinite(dw[6:]).all()
+
+
+def streamed_cases():
+    """Every run width of the three-launch form with enough pixels a thread that its loads ahead are refilled, unchecked
+    batches run and remainders of 0, 1 and U - 1 pixels are left: q pixels for each thread of the writing pass, one more
+    for some where `more`."""
+    wide = [("bf16", 52, 13, 0, 4), ("f16", 60, 6, 0, 4), ("f32", 30, 5, 0, 2), ("bf16", 64, 8, 0, 8), ("f32", 32, 8, 0, 4)]
+    short = [("f32", 27, 9, 0, 1), ("f32", 32, 8, 1, 1), ("bf16", 38, 2, 0, 2), ("f16", 48, 6, 2, 2), ("bf16", 31, 31, 0, 1),
+             ("f16", 32, 4, 5, 1)]
+    return [(*c, q, more) for c in wide for q, more in ((18, 1),)] + \
+        [(*c, q, more) for c in short for q, more in ((16, 0), (17, 0), (23, 1))]
+
+
+def form_check(monkeypatch, dtype, B, P, C, G, pad, forms):
+    """Forward and gradient of one streamed case against the oracle, with the bound of the plans' own sums and 48 steps
+    for xhat, z, the sigmoid, its derivative and the products."""
+    from tests import group_norm_plan as plan
+    rng = np.random.default_rng(C * 1000 + P)
+    x, dy = gn_tensors(rng, dtype, (B, P, C), pad, 0.5)
+    w, b = weights(rng, C), weights(rng, C) - 1
+    nan = lambda *s: torch.full(s, float("nan"), device="cuda")
+    mean, rstd, dw, db = nan(B, G), nan(B, G), nan(C), nan(C)
+    y, dx = (torch.full((B, P, C), float("nan"), dtype=DT[dtype], device="cuda") for _ in range(2))
+    view = lambda t: (t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1))
+    e, steps = x.element_size(), 0
+    for backward, out in ((False, y), (True, dx)):
+        p = plan.plan(B, P, C, G, e, plan.vec_of(e, C, view(x), view(out), *([view(dy)] if backward else [])), backward)
+        forms(p)
+        steps = max(steps, plan.sum_steps(p, B, P, C, G, backward))
+    monkeypatch.setitem(globals(), "GSTEPS", steps + 48)
+    dit.dit_group_norm_forward(x, y, G, weight=w, bias=b, mean=mean, rstd=rstd, eps=1e-3, act=dit.ACT_SILU)
+    dit.dit_group_norm_backward(x, dy, mean, rstd, dx, G, weight=w, bias=b, dweight=dw, dbias=db, act=dit.ACT_SILU)
+    gn_check(x, dy, G, "silu", w, b, y, mean, rstd, dx, dw, db, 1e-3)
+
+
+@pytest.mark.parametrize("case", streamed_cases(), ids=lambda c: "-".join(map(str, c)))
+def test_group_norm_streams_of_every_run_width(case, monkeypatch):
+    from tests import group_norm_plan as plan
+    dtype, C, G, pad, vec, q, more = case
+    e = 4 if dtype == "f32" else 2
+    wave = plan.plan(1, 1 << 28, C, G, e, vec, False)
+    step = wave["passes"] * wave["rows"]
+
+    def forms(p):
+        assert not p["cluster"] and p["vec"] == vec and p["passes"] * p["rows"] == step and p["pixels_a_thread"] == q + more
+
+    form_check(monkeypatch, dtype, 1, step * q + more, C, G, pad, forms)
+
+
+@pytest.mark.parametrize("case", [("f32", 170, 203, 1024, 32), ("bf16", 310, 260, 512, 16)], ids=lambda c: "-".join(map(str, c)))
+def test_group_norm_long_sums_of_a_thread(case, monkeypatch):
+    """More than one wave of work: what bounds a block's share is how many pixels a thread may sum in a row."""
+    dtype, B, P, C, G = case
+
+    def forms(p):
+        assert not p["cluster"] and p["pixels_a_thread"] > (60 if dtype == "bf16" else 100)
+
+    form_check(monkeypatch, dtype, B, P, C, G, 0, forms)

@@ -327,3 +327,24 @@ def test_tensors_that_require_grad_are_refused_unless_grad_mode_is_off():
 
     Turn.apply(q.clone().requires_grad_()).sum().backward()
     assert seen == [False, False]
+
+
+def test_workspace_sizes_follow_the_restated_plan():
+    """Also pins down that only sizes and type count: the query's answer is enough for any strides and alignment."""
+    from tests import group_norm_plan as G
+    rng = random.Random(3)
+    forms = set()
+    for _ in range(3000):
+        groups = rng.choice([1, 2, 3, 4, 8, 13, 32])
+        channels = groups * rng.choice([1, 2, 3, 4, 5, 8, 12, 16, 40, 300])
+        batch, pixels = int(2 ** rng.uniform(0, 6)), int(2 ** rng.uniform(0, 20))
+        dtype, backward = rng.choice([dit.DTYPE_F32, dit.DTYPE_BF16]), rng.random() < 0.5
+        elem = 4 if dtype == dit.DTYPE_F32 else 2
+        got = dit.lib().dit_group_norm_workspace_bytes(
+            gn_args(batch=batch, pixels=pixels, channels=channels, groups=groups, dtype=dtype, x=rng.randint(0, 1 << 20),
+                    xs=(rng.randint(0, 99), rng.randint(0, 99))), backward)
+        want = G.workspace(batch, pixels, channels, groups, elem, backward)
+        assert got == want, (batch, pixels, channels, groups, dtype, backward)
+        p = G.plan(batch, pixels, channels, groups, elem, 1, backward)
+        forms.add((p["cluster"], p["whole_batch"], p["unit"] == 1))
+    assert len(forms) >= 4
