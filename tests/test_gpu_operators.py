@@ -810,3 +810,27 @@ def test_group_norm_long_sums_of_a_thread(case, monkeypatch):
         assert not p["cluster"] and p["pixels_a_thread"] > (60 if dtype == "bf16" else 100)
 
     form_check(monkeypatch, dtype, B, P, C, G, 0, forms)
+
+
+@pytest.mark.parametrize("B,P,C,G", [(200000, 1, 64, 4), (300, 700, 256, 2), (1, 1 << 24, 8, 1)], ids=["batch", "both", "pixels"])
+def test_group_norm_weight_gradients_of_very_many_terms(B, P, C, G):
+    """The same pixels in every batch element and equal gradients, so roundings do not cancel: a thread's sum of at most
+    128 pixels and the rows of a block, then 128 splits and 128 batch elements and joins without loss (8 rows of a tree), and
+    48 steps of the term itself."""
+    rng = np.random.default_rng(22)
+    one = rng.standard_normal((1, min(P, 700), C))
+    x = torch.from_numpy(one).float().cuda()
+    x = x.expand(B, *x.shape[1:]) if P <= 700 else x[:, :64].repeat(B, P // 64, 1)
+    dy = torch.from_numpy(rng.uniform(1, 2, C)).float().cuda().expand(B, P, C)
+    w, b = weights(rng, C), weights(rng, C) - 1
+    mean, rstd, dx = torch.empty(B, G, device="cuda"), torch.empty(B, G, device="cuda"), torch.empty(B, P, C, device="cuda")
+    dw, db = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    mean[:] = torch.from_numpy(rng.standard_normal(G)).float().cuda()
+    rstd[:] = torch.from_numpy(rng.uniform(.5, 2, G)).float().cuda()
+    dit.dit_group_norm_backward(x, dy, mean, rstd, dx, G, weight=w, bias=b, dweight=dw, dbias=db)
+    xs = n64(x[:1, :min(P, 64 if P > 700 else 700)])
+    _, gw, gb = O.group_norm_backward(xs, np.broadcast_to(n64(dy[0, 0]), xs.shape), n64(mean[:1]), n64(rstd[:1]), G, n64(w), n64(b))
+    xhat = np.abs((xs - np.repeat(n64(mean[:1]), C // G, 1)[:, None]) * np.repeat(n64(rstd[:1]), C // G, 1)[:, None])
+    times = B * P / xs.shape[1]
+    near(db, times * gb, times * gb, 128 + 2 * 128 + 8 + 48, "dbias")
+    near(dw, times * gw, times * (n64(dy[0, 0]) * xhat).sum((0, 1)), 128 + 2 * 128 + 8 + 48, "dweight")
