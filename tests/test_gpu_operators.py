@@ -834,3 +834,28 @@ def test_group_norm_weight_gradients_of_very_many_terms(B, P, C, G):
     times = B * P / xs.shape[1]
     near(db, times * gb, times * gb, 128 + 2 * 128 + 8 + 48, "dbias")
     near(dw, times * gw, times * (n64(dy[0, 0]) * xhat).sum((0, 1)), 128 + 2 * 128 + 8 + 48, "dweight")
+
+
+def test_rope_gradient_of_q_and_k_in_different_layouts():
+    """q by runs of 8 channels, k element by element (rows that start anywhere): two launches, k's partial weight sums
+    behind q's; and both few enough for clusters."""
+    rng = np.random.default_rng(23)
+    for N, d, axes in ((1500, 128, (44, 42, 42)), (40, 128, (44, 42, 42)), (700, 64, (32, 32))):
+        pos, kw = positions(rng, "grid", 2, N, len(axes)), dict(axes=axes, eps=1e-5)
+        q, dyq = views(rng, "tokens", 2, N, 6, d, "bf16"), views(rng, "tokens", 2, N, 6, d, "bf16")
+        k, dyk = views(rng, "odd", 2, N, 2, d, "bf16"), views(rng, "odd", 2, N, 2, d, "bf16")
+        wq, wk = weights(rng, d), weights(rng, d)
+        new = lambda: (torch.empty_like(q), torch.empty(2, N, 2, d, dtype=torch.bfloat16, device="cuda"),
+                       torch.full((d,), float("nan"), device="cuda"), torch.full((d,), float("nan"), device="cuda"))
+        dq, dk, dwq, dwk = new()
+        dit.dit_rope_backward(pos, dyq, dq, dyk, dk, q=q, k=k, q_weight=wq, k_weight=wk, dq_weight=dwq, dk_weight=dwk, **kw)
+        # each by itself gives the same rows; the sums are of other blocks
+        eq, ek, ewq, ewk = new()
+        dit.dit_rope_backward(pos, dyq, eq, q=q, q_weight=wq, dq_weight=ewq, **kw)
+        dit.dit_rope_backward(pos, dyk, ek, q=k, q_weight=wk, dq_weight=ewk, **kw)
+        assert torch.equal(dq, eq) and torch.equal(dk, ek)
+        for x, dy, w, dw in ((q, dyq, wq, dwq), (k, dyk, wk, dwk)):
+            _, ref = O.rope_backward(n64(dy), n64(pos), axes, x=n64(x), weight=n64(w), eps=1e-5)
+            xh = np.abs(n64(x)) / np.sqrt(np.mean(n64(x) ** 2, -1, keepdims=True) + 1e-5)
+            # 33 rows, 32 groups of a block, 19 partials a warp and 32 warps; the term's own steps
+            near(dw, ref, np.sum(np.abs(n64(dy)).max(-1, keepdims=True) * xh * 1.5, (0, 1, 2)), 33 + 32 + 19 + 32 + RSTEPS)
