@@ -183,6 +183,8 @@ DIT_DEV void v_sigmoid(float (&d)[V], float (&c)[V], const float (&z)[V]) {
 }
 
 // ---------------------------------------------------------------- blocks
+// ceil(n / step): the sum passes 31 bits near 2^31 pixels
+DIT_DEV int steps_from(int n, int step) { return (int)(((unsigned)n + (unsigned)step - 1) / (unsigned)step); }
 // `shares` blocks take a batch element's pixels in turn, `rows` at a time: at
 // any moment all of them are near the same place, so what was read last is the
 // end of the tensor.
@@ -199,7 +201,7 @@ struct Place {
     on = row < rows && c < P.channels;
     step = shares * rows;
     p = s * rows + row;
-    count = on && p < P.pixels ? (P.pixels - p + step - 1) / (unsigned)step : 0;
+    count = on && p < P.pixels ? steps_from(P.pixels - p, step) : 0;
   }
 };
 // Pixels of share s.
@@ -512,7 +514,7 @@ DIT_DEV void block_moments(const GnParams& P, const Place& at, const T* x, int l
   Moments<V> A;
   if (at.on && len > 0) {
     const T* row0 = x + (at.p - at.row) * P.xs[1] + at.c;
-    A.pivot(row0, at.step * P.xs[1], (P.pixels - (at.p - at.row) + at.step - 1) / (unsigned)at.step);
+    A.pivot(row0, at.step * P.xs[1], steps_from(P.pixels - (at.p - at.row), at.step));
     if (at.row == 0)
 #pragma unroll
       for (int i = 0; i < V; ++i) piv[at.run * V + i] = A.K[i];

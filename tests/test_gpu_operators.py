@@ -859,3 +859,35 @@ def test_rope_gradient_of_q_and_k_in_different_layouts():
             xh = np.abs(n64(x)) / np.sqrt(np.mean(n64(x) ** 2, -1, keepdims=True) + 1e-5)
             # 33 rows, 32 groups of a block, 19 partials a warp and 32 warps; the term's own steps
             near(dw, ref, np.sum(np.abs(n64(dy)).max(-1, keepdims=True) * xh * 1.5, (0, 1, 2)), 33 + 32 + 19 + 32 + RSTEPS)
+
+
+def test_group_norm_of_the_most_pixels():
+    """2^31 - 1 pixels of one channel: the counts of a thread and a block come close to 32 bits."""
+    N = 2**31 - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 8 * N + 2**33:
+        pytest.skip("not enough memory free")
+    x = torch.empty(1, N, 1, dtype=torch.bfloat16, device="cuda")
+    x[0, :, 0] = 1.0
+    x[0, ::2] = -1.0                                    # N odd: they cancel but for the last
+    x[0, N - 1] = 3.0
+    mean, rstd = torch.empty(1, 1, device="cuda"), torch.empty(1, 1, device="cuda")
+    y = torch.empty_like(x)
+    w, b = torch.full((1,), 2.0, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    dit.dit_group_norm_forward(x, y, 1, weight=w, bias=b, mean=mean, rstd=rstd, eps=0.0)
+    assert abs(mean.item() - 3 / N) < 2**-12 and abs(rstd.item() - 1) < 2**-12
+    want = torch.tensor([-1.5, 2.5], device="cuda").to(torch.bfloat16)
+    pairs = y[0, :N - 1, 0].view(-1, 2)
+    for i in range(0, len(pairs), 1 << 26):
+        part = pairs[i:i + (1 << 26)]
+        assert ((part.float() - want.float()).abs().amax() <= 2**-8 * 2.5), i
+    assert abs(y[0, N - 1, 0].item() - 6.5) < 2**-8 * 6.5
+    # gradient: dy = 1 everywhere, so dx is 0 but for what the sums leave, and dbias counts the pixels
+    dy = torch.ones(1, 1, 1, dtype=torch.bfloat16, device="cuda").expand(1, N, 1)
+    mean.zero_(), rstd.fill_(1.0)
+    dw, db = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    dit.dit_group_norm_backward(x, dy, mean, rstd, y, 1, weight=w, bias=b, dweight=dw, dbias=db)
+    assert db.item() == 2.0**31 and dw.item() == 3          # sums of +-1 that stay below 2^24 are exact
+    assert y.abs().max() <= 2**-10
+    del x, y, pairs, part
+    torch.cuda.empty_cache()
