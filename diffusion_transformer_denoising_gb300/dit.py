@@ -385,8 +385,9 @@ def _pixel_view(name, t, shape, dtype):
 
 def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, act):
     _torch or _use_torch()
-    if _grad_mode() and (x.requires_grad or weight is not None and weight.requires_grad or
-                         bias is not None and bias.requires_grad or dy is not None and dy.requires_grad):
+    if out is not None and _grad_mode() and (x.requires_grad or weight is not None and weight.requires_grad or
+                                             bias is not None and bias.requires_grad or
+                                             dy is not None and dy.requires_grad):
         _refuse_autograd()
     shape, dtype = x.shape, x.dtype
     if len(shape) < 3:

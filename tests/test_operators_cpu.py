@@ -348,3 +348,8 @@ def test_workspace_sizes_follow_the_restated_plan():
         p = G.plan(batch, pixels, channels, groups, elem, 1, backward)
         forms.add((p["cluster"], p["whole_batch"], p["unit"] == 1))
     assert len(forms) >= 4
+
+
+def test_workspace_query_of_a_tensor_that_requires_grad():
+    x = torch.zeros(2, 8, 8, 64, requires_grad=True)
+    assert dit.dit_group_norm_workspace_bytes(x, 32, True) == dit.dit_group_norm_workspace_bytes(x.detach(), 32, True)
