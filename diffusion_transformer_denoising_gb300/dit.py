@@ -201,6 +201,10 @@ def _refuse(status, msg):
     raise DitError(status, msg)
 
 
+def _refuse_scalar(e):
+    raise DitError(DIT_ERR_INVALID_ARG, f"an argument has the wrong type or does not fit its field: {e}") from None
+
+
 def _dtype_code(dtype):
     code = _dtype_codes.get(dtype)
     return _refuse(DIT_ERR_INVALID_ARG, f"unsupported dtype {dtype}") if code is None else code
@@ -307,9 +311,12 @@ def _rope_args(pos, axes, theta, style, eps, first, q, k):
     st = pos.stride()
     if st[-1] != 1 and n > 1 and pos.numel():
         _refuse(DIT_ERR_SHAPE, "the axes of a position must be contiguous")
-    return _ROPE_ARGS.pack(B, N, d, code, style, n, *axes, *_NO_VIEW[n:], theta, eps, pos.data_ptr(),
-                           st[0] if len(ps) == 3 else 0, st[-2], POS_I32 if pd is torch.int32 else POS_F32, 0,
-                           *_rope_heads("q", *q, B, N, d, dtype), *_rope_heads("k", *k, B, N, d, dtype))
+    try:
+        return _ROPE_ARGS.pack(B, N, d, code, style, n, *axes, *_NO_VIEW[n:], theta, eps, pos.data_ptr(),
+                               st[0] if len(ps) == 3 else 0, st[-2], POS_I32 if pd is torch.int32 else POS_F32, 0,
+                               *_rope_heads("q", *q, B, N, d, dtype), *_rope_heads("k", *k, B, N, d, dtype))
+    except (struct.error, OverflowError) as e:
+        _refuse_scalar(e)
 
 
 def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, style=ROPE_INTERLEAVED, q_weight=None,
@@ -350,8 +357,11 @@ def dit_rope_workspace_bytes(head_dim: int) -> int:
     """Workspace that is enough for any dit_rope_backward with weight gradients."""
     heads = (1, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 16, 32)
     none = (0, 0, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0)
-    n = lib().dit_rope_workspace_bytes(_ROPE_ARGS.pack(1, 1 << 20, head_dim, DTYPE_F32, 0, 1, 0, 0, 0, 0, 1e4, 0.0, 0, 0, 0,
-                                                       POS_I32, 0, *heads, *none))
+    try:
+        args = _ROPE_ARGS.pack(1, 1 << 20, head_dim, DTYPE_F32, 0, 1, 0, 0, 0, 0, 1e4, 0.0, 0, 0, 0, POS_I32, 0, *heads, *none)
+    except (struct.error, OverflowError) as e:
+        _refuse_scalar(e)
+    n = lib().dit_rope_workspace_bytes(args)
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
     return n
@@ -395,12 +405,15 @@ def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, 
     B, C, P = shape[0], shape[-1], 1
     for v in shape[1:-1]:
         P *= v
-    return _GN_ARGS.pack(B, P, C, groups, _dtype_code(dtype), act, eps, 0, *_pixel_view("x", x, shape, dtype),
-                         *((0, 0, 0) if dy is None else _pixel_view("dy", dy, shape, dtype)),
-                         *((0, 0, 0) if out is None else _pixel_view("out", out, shape, dtype)),
-                         _param("weight", weight, (C,)), _param("bias", bias, (C,)),
-                         _param("mean", mean, (B, groups)), _param("rstd", rstd, (B, groups)),
-                         _param("dweight", dweight, (C,)), _param("dbias", dbias, (C,)))
+    try:
+        return _GN_ARGS.pack(B, P, C, groups, _dtype_code(dtype), act, eps, 0, *_pixel_view("x", x, shape, dtype),
+                             *((0, 0, 0) if dy is None else _pixel_view("dy", dy, shape, dtype)),
+                             *((0, 0, 0) if out is None else _pixel_view("out", out, shape, dtype)),
+                             _param("weight", weight, (C,)), _param("bias", bias, (C,)),
+                             _param("mean", mean, (B, groups)), _param("rstd", rstd, (B, groups)),
+                             _param("dweight", dweight, (C,)), _param("dbias", dbias, (C,)))
+    except (struct.error, OverflowError) as e:
+        _refuse_scalar(e)
 
 
 def dit_group_norm_forward(x, y, groups: int, *, weight=None, bias=None, mean=None, rstd=None, eps=1e-6, act=ACT_NONE,

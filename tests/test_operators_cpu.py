@@ -353,3 +353,20 @@ def test_workspace_sizes_follow_the_restated_plan():
 def test_workspace_query_of_a_tensor_that_requires_grad():
     x = torch.zeros(2, 8, 8, 64, requires_grad=True)
     assert dit.dit_group_norm_workspace_bytes(x, 32, True) == dit.dit_group_norm_workspace_bytes(x.detach(), 32, True)
+
+
+def test_scalars_that_the_structures_cannot_hold_are_refused():
+    pos, q, x = torch.zeros(8, 2, dtype=torch.int32), torch.zeros(2, 8, 3, 32), torch.zeros(2, 5, 12)
+    for kw in (dict(axes=(16.0, 16)), dict(axes=(2**40, 16)), dict(axes=(16, 16), theta=1e39), dict(axes=(16, 16), eps="1"),
+               dict(axes=(16, 16), style=2**31), dict(axes=(16, 16), style="split")):
+        with pytest.raises(dit.DitError) as e:
+            dit.dit_rope_forward(pos, q, q, **kw)
+        assert e.value.status == INVALID
+    for groups, kw in ((3.0, {}), (2**33, {}), (3, dict(eps=1e40)), (3, dict(act="silu"))):
+        with pytest.raises(dit.DitError) as e:
+            dit.dit_group_norm_forward(x, x, groups, **kw)
+        assert e.value.status == INVALID
+    for call in (lambda: dit.dit_rope_workspace_bytes(2**40), lambda: dit.dit_group_norm_workspace_bytes(x, 2**33, True)):
+        with pytest.raises(dit.DitError) as e:
+            call()
+        assert e.value.status in (INVALID, SHAPE)
