@@ -851,14 +851,12 @@ DIT_DEV float2 long_sums(int count, At at) {
     return v;
   };
   if (count <= 128) return some(0, count);
-  float2 high = make_float2(0.f, 0.f), low = high;
+  LongSum x, y;
   for (int i = 0; i < count; i += 128) {
     const float2 v = some(i, min(count, i + 128));
-    float t;
-    high.x = two_sum(high.x, v.x, t), low.x += t;
-    high.y = two_sum(high.y, v.y, t), low.y += t;
+    x.add(v.x), y.add(v.y);
   }
-  return make_float2(isfinite(high.x) ? high.x + low.x : high.x, isfinite(high.y) ? high.y + low.y : high.y);
+  return make_float2(x.value(), y.value());
 }
 
 DIT_DEV float block_sum(float v, float* sm) {
@@ -1045,13 +1043,14 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
   cluster_arrive();
   cluster_wait();
   for (int c = threadIdx.x; c < here; c += kThreads) {
-    float A = 0.f, B = 0.f;
+    LongSum x, y;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       if (r >= P.splits) continue;
       const float2 e = ld_cluster_f2(cluster_map(own + c, base + r));
-      A += e.x, B += e.y;
+      x.add(e.x), y.add(e.y);
     }
+    const float A = x.value(), B = y.value();
     if (share == 0 && P.chan) P.chan[(int64_t)b * P.channels + c0 + c] = make_float2(A, B);
     const float w = P.w ? P.w[c0 + c] : 1.f;
     chan[c] = make_float2(w * A, w * B);
@@ -1060,13 +1059,13 @@ __global__ void __launch_bounds__(kThreads, 2) gn_grad_cluster_kernel(const __gr
   if (P.whole_batch && blockIdx.x == 0) {
     // the batch's blocks in order
     for (int c = threadIdx.x; c < here; c += kThreads) {
-      float A = 0.f, B = 0.f;
+      LongSum x, y;
       for (uint32_t r = 0; r < gridDim.x; ++r) {
         const float2 t = ld_cluster_f2(cluster_map(own + c, r));
-        A += t.x, B += t.y;
+        x.add(t.x), y.add(t.y);
       }
-      if (P.db) P.db[c0 + c] = A;
-      if (P.dw) P.dw[c0 + c] = B;
+      if (P.db) P.db[c0 + c] = x.value();
+      if (P.dw) P.dw[c0 + c] = y.value();
     }
   }
   cluster_arrive();  // this block has read its peers' memory

@@ -576,10 +576,10 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
       const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
       float* own = sm + groups * P.d;
       for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
-        float v = 0.f;
-        for (uint32_t j = 0; j < groups; ++j) v += sm[j * P.d + ch];
-        if (part) part[block * P.d + ch] = v;
-        else own[ch] = v;
+        LongSum v;
+        for (uint32_t j = 0; j < groups; ++j) v.add(sm[j * P.d + ch]);
+        if (part) part[block * P.d + ch] = v.value();
+        else own[ch] = v.value();
       }
     }
     if (P.one_cluster) {
@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(kRopeThreads, MODE == ROPE_NORM_GRAD ? 2 : 3) 
       cluster_wait();
       if (dw && blockIdx.x == 0)
         for (int ch = threadIdx.x; ch < P.d; ch += kRopeThreads) {
-          float v = 0.f;
-          for (uint32_t r = 0; r < gridDim.x; ++r) v += ld_cluster_f1(cluster_map(sm + groups * P.d + ch, r));
-          dw[ch] = v;
+          LongSum v;
+          for (uint32_t r = 0; r < gridDim.x; ++r) v.add(ld_cluster_f1(cluster_map(sm + groups * P.d + ch, r)));
+          dw[ch] = v.value();
         }
       cluster_arrive();
       cluster_wait();  // a block's memory stays until it has been read
@@ -616,10 +616,10 @@ __global__ void __launch_bounds__(1024) rope_dweight_kernel(const float* p0, int
   sm[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && ch < d) {
-    v = 0.f;
+    LongSum all;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += sm[i][lane];
-    dw[ch] = v;
+    for (int i = 0; i < 32; ++i) all.add(sm[i][lane]);
+    dw[ch] = all.value();
   }
 }
 

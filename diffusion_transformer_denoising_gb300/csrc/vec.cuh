@@ -17,6 +17,16 @@ DIT_DEV float two_sum(float a, float b, float& low) {
   low = (a - (h - t)) + (b - t);
   return h;
 }
+// A sum taken one term after the other that loses nothing: high and low part.
+struct LongSum {
+  float h = 0.f, l = 0.f;
+  DIT_DEV void add(float v) {
+    float t;
+    h = two_sum(h, v, t);
+    l += t;
+  }
+  DIT_DEV float value() const { return isfinite(h) ? h + l : h; }
+};
 
 DIT_DEV float to_f32(float v) { return v; }
 DIT_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

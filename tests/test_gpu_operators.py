@@ -891,3 +891,18 @@ def test_group_norm_of_the_most_pixels():
     assert y.abs().max() <= 2**-10
     del x, y, pairs, part
     torch.cuda.empty_cache()
+
+
+def test_rope_weight_gradient_joined_without_loss():
+    """One row in 128 groups of 304 blocks, at position 0 and with root 1, so a term is dy exactly: a lane adds two rows, a
+    warp 10 partials, the results are rounded twice; groups and warps are joined without loss."""
+    N, d = 2 * 128 * 304, 16
+    rng = np.random.default_rng(24)
+    dy = torch.from_numpy((1 + rng.integers(0, 2**23, (1, 1, 1, d)) * 2.0**-23)).float().cuda()
+    x, w = torch.ones(1, 1, 1, d, device="cuda"), weights(rng, d)
+    pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    dx, dw = torch.empty(1, N, 1, d, device="cuda"), torch.empty(d, device="cuda")
+    dit.dit_rope_backward(pos.expand(N, 1), dy.expand(1, N, 1, d), dx, axes=(d,), q=x.expand(1, N, 1, d), q_weight=w,
+                          dq_weight=dw, eps=0.0)
+    ref = N * n64(dy)[0, 0, 0]
+    near(dw, ref, ref, 2 + 10 + 2, "weight gradient")
