@@ -14,16 +14,16 @@
 // together, so a row costs one round of shuffles either way.
 //
 // What bounds it: HBM, once the latency is covered; with the norm, and more so
-// for its gradient, the instructions of a row (0.65 and 0.59 of the issue slots).
+// for its gradient, the instructions of a row (0.65 and 0.61 of the issue slots).
 // Every row is read once and written once.  A group of lanes holds one row in
 // registers (8 channels a lane, 128-bit accesses), forms its pairs' cos and sin
 // once for all the token's heads, and always has the next batch of rows (64 bytes
 // a lane), of the next tensor or token too, and the next token's positions on
 // their way.  Measured on one GB300 (bf16, 128-wide heads, 44/42/42): q and k of
-// 2 x 32760 tokens x 12 heads 122 us = 6.59 TB/s (0.99 of the copy bandwidth);
-// 32760 tokens with the norm, out of a packed projection, 68.7 us = 5.87 TB/s; its
-// gradient 116 us = 5.21 TB/s (without the loads ahead 151 us; with the positions
-// not among them 146 us).
+// 2 x 32760 tokens x 12 heads 122 us = 6.59 TB/s (0.985 of the copy bandwidth);
+// 32760 tokens with the norm, out of a packed projection, 68.9 us = 5.85 TB/s; its
+// gradient 118.8 us = 5.09 TB/s (when it was 116: without the loads ahead 151 us,
+// with the positions not among them 146 us).
 #include <math.h>
 
 #include <type_traits>
@@ -787,7 +787,7 @@ cudaError_t rope_run(const dit_rope_args& a, bool backward, float* workspace, cu
       if (ny > 256) ny = 256;
       // the gradient keeps its weight sums in registers: as many blocks as run
       // at once, so few partials are left to join (two per SM: 115 us on the
-      // 32760-token video gradient, 127 us with 1024 blocks a tensor)
+      // 32760-token video gradient at the time, 127 us with 1024 blocks a tensor)
       if (grad && nx * ny > 304 / nz) nx = 304 / nz / ny > 0 ? 304 / nz / ny : 1;
       // few rows: a cluster of eight blocks a tensor joins the weight sums itself
       if (grad && rope_one_cluster(a) && (h[first]->dweight || h[last]->dweight)) {
