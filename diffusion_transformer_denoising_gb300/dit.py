@@ -293,6 +293,8 @@ def _rope_heads(tag, x, dy, out, weight, dweight, B, N, d, dtype):
 def _rope_args(pos, axes, theta, style, eps, first, q, k):
     torch = _torch or _use_torch()
     if _grad_mode():
+        if pos.requires_grad:
+            _refuse_autograd()
         for x, dy, _, weight, _ in (q, k):
             if (x is not None and x.requires_grad or weight is not None and weight.requires_grad or
                     dy is not None and dy.requires_grad):

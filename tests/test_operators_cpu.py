@@ -309,6 +309,10 @@ def test_tensors_that_require_grad_are_refused_unless_grad_mode_is_off():
             with torch.no_grad(), pytest.raises(dit.DitError) as e:      # refused for its device only
                 call(*with_grad)
             assert "CUDA" in str(e.value)
+    at = z(8, 2, requires_grad=True)                                      # learnt positions have no gradient here
+    with pytest.raises(dit.DitError) as e:
+        dit.dit_rope_forward(at, q, q, axes=(16, 16))
+    assert "autograd" in str(e.value)
     seen = []
 
     class Turn(torch.autograd.Function):                                 # how a program gives the operator to autograd
