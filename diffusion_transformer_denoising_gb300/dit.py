@@ -22,11 +22,12 @@ LIB_PATH = os.environ.get("DIT_LIB") or os.path.join(_PKG, "libdit.so")
 DIT_OK, DIT_ERR_INVALID_ARG, DIT_ERR_SHAPE, DIT_ERR_NOT_LOADED, DIT_ERR_OOM, DIT_ERR_CUDA, DIT_ERR_TIMEOUT = range(7)
 PREC_BF16, PREC_F32, PREC_FP8 = 0, 1, 2
 COND_CROSS, COND_JOINT = 0, 1
-DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+DTYPE_F32, DTYPE_BF16, DTYPE_F16, DTYPE_E4M3 = 0, 1, 2, 3
 ROPE_INTERLEAVED, ROPE_SPLIT = 0, 1
 ROPE_MAX_AXES, ROPE_MAX_HEAD_DIM = 4, 256
 POS_I32, POS_F32 = 0, 1
-ACT_NONE, ACT_SILU = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
+RMS_NORM_MAX_CHANNELS = 16384
 LOOP_PARTIAL_SCHEDULE = 1
 LOOP_CUDA_GRAPH = 2
 
@@ -36,7 +37,10 @@ EXPORTS = ["dit_create", "dit_load_weights", "dit_num_params", "dit_param_info",
            "dit_denoise_loop", "dit_synchronize", "dit_device_bytes", "dit_destroy", "dit_status_string",
            "dit_last_error", "dit_debug_fail_alloc_after", "dit_debug_gemm_cta_pairs", "dit_debug_stall", "dit_profile_start", "dit_profile_stop",
            "dit_timestep_modulation_noalloc", "dit_rope_forward", "dit_rope_backward", "dit_rope_workspace_bytes",
-           "dit_group_norm_forward", "dit_group_norm_backward", "dit_group_norm_workspace_bytes"]
+           "dit_group_norm_forward", "dit_group_norm_backward", "dit_group_norm_workspace_bytes",
+           "dit_rms_norm_forward", "dit_rms_norm_backward", "dit_rms_norm_workspace_bytes",
+           "dit_gated_ffn_forward", "dit_gated_ffn_backward", "dit_gated_ffn_workspace_bytes",
+           "dit_gated_ffn_synchronize", "dit_grad_norm", "dit_grad_norm_workspace_bytes"]
 NOALLOC_MAX_BATCH, NOALLOC_MAX_HIDDEN = 64, 262144
 
 KERNEL_KINDS = ["gemm_qkv", "gemm_out", "gemm_cross_q", "gemm_cross_kv", "gemm_ffn1", "gemm_ffn2", "gemm_embed",
@@ -106,6 +110,15 @@ def lib():
         "dit_group_norm_forward": ([vp, vp, i64, vp], C.c_int),
         "dit_group_norm_backward": ([vp, vp, i64, vp], C.c_int),
         "dit_group_norm_workspace_bytes": ([vp, C.c_int], i64),
+        "dit_rms_norm_forward": ([vp, vp], C.c_int),
+        "dit_rms_norm_backward": ([vp, vp, i64, vp], C.c_int),
+        "dit_rms_norm_workspace_bytes": ([vp], i64),
+        "dit_gated_ffn_forward": ([vp, vp, i64, vp], C.c_int),
+        "dit_gated_ffn_backward": ([vp, vp, i64, vp], C.c_int),
+        "dit_gated_ffn_workspace_bytes": ([vp, C.c_int], i64),
+        "dit_gated_ffn_synchronize": ([vp], C.c_int),
+        "dit_grad_norm": ([vp, i64, f32, vp, vp, i64, vp], C.c_int),
+        "dit_grad_norm_workspace_bytes": ([vp, i64], i64),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -181,9 +194,13 @@ def flow_euler_step(x, v, sigma: float, sigma_next: float, n: int, stream=None):
 # dit_rope_args and dit_group_norm_args of include/dit.h, packed in one go
 _ROPE_ARGS = struct.Struct("<2q8i2fQ2q2i" + 2 * "2iQ3qQ3qQ3q2Q")
 _GN_ARGS = struct.Struct("<2q4ifiQ2qQ2qQ2q6Q")
+_NORM_ARGS = struct.Struct("<2q3if" + 5 * "Q2q" + "3Q")
+_FFN_ARGS = struct.Struct("<q6i" + 3 * "Qq" + "5Q" + 6 * "Qq" + "2Q")
+_GRAD_TENSOR = struct.Struct("<2Qq2i")
 _NO_VIEW = (0, 0, 0, 0)
 _torch = None          # the module, its dtypes as dit.h names them and its grad mode, on first use
 _dtype_codes = {}
+_operand_codes = {}    # and e4m3
 _grad_mode = None
 
 
@@ -193,6 +210,8 @@ def _use_torch():
         import torch
         _grad_mode = torch.is_grad_enabled
         _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+        _operand_codes.update(_dtype_codes)
+        _operand_codes[torch.float8_e4m3fn] = DTYPE_E4M3
         _torch = torch
     return _torch
 
@@ -446,6 +465,255 @@ def dit_group_norm_workspace_bytes(x, groups: int, backward: bool) -> int:
     """Workspace of a group-norm call on tensors of x's shape and type."""
     n = lib().dit_group_norm_workspace_bytes(
         _gn_args(x, None, None, groups, None, None, None, None, None, None, 0.0, ACT_NONE), 1 if backward else 0)
+    if n < 0:
+        raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
+    return n
+
+
+def _any_requires_grad(*tensors):
+    return any(t is not None and t.requires_grad for t in tensors)
+
+
+def _token_view(name, t, shape, dtype):
+    """(pointer, batch stride, token stride) of a [..., channels] view: one axis in front of the channels is tokens of one
+    batch element, of several the first is the batch."""
+    if t is None:
+        return 0, 0, 0
+    if len(shape) >= 3:
+        return _pixel_view(name, t, shape, dtype)
+    if t.shape != shape or t.dtype is not dtype or (t.numel() and t.stride(-1) != 1 and shape[-1] > 1):
+        if t.shape == shape and t.dtype is dtype:
+            _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous")
+        _bad_view(name, t, shape, dtype)
+    return (t.data_ptr(), 0, t.stride(0) if len(shape) == 2 else 0) if t.numel() else (0, 0, 0)
+
+
+def _norm_args(x, residual, total, dy, out, out_dtype, scale, weight, dweight, eps):
+    torch = _torch or _use_torch()
+    if out is not None and _grad_mode() and _any_requires_grad(x, residual, dy, weight):
+        _refuse_autograd()
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 1:
+        _refuse(DIT_ERR_SHAPE, "x must be [..., channels]")
+    B, N = (shape[0] if len(shape) > 2 else 1), 1
+    for v in shape[1:-1] if len(shape) > 2 else shape[:-1]:
+        N *= v
+    code = _dtype_code(dtype)
+    if out_dtype is not dtype and out_dtype is not torch.float8_e4m3fn:
+        _refuse(DIT_ERR_INVALID_ARG, f"out is {out_dtype}: {dtype} or float8_e4m3fn is wanted")
+    try:
+        return _NORM_ARGS.pack(B, N, shape[-1], code, code if out_dtype is dtype else DTYPE_E4M3, eps,
+                               *_token_view("x", x, shape, dtype), *_token_view("residual", residual, shape, dtype),
+                               *_token_view("total", total, shape, dtype), *_token_view("dy", dy, shape, dtype),
+                               *_token_view("out", out, shape, out_dtype), _param("scale", scale, shape[:-1]),
+                               _param("weight", weight, shape[-1:]), _param("dweight", dweight, shape[-1:]))
+    except (struct.error, OverflowError) as e:
+        _refuse_scalar(e)
+
+
+def dit_rms_norm_forward(x, out, *, residual=None, total=None, weight=None, scale=None, eps=1e-6, stream=None):
+    """RMS norm over the channels of x [..., channels], of x + residual where a
+    residual is given: total (which may be x or residual) receives that sum.
+    out: of x's type (and possibly x or residual itself), or float8_e4m3fn with
+    scale, float32 x.shape[:-1]: out * scale is the norm."""
+    args = _norm_args(x, residual, total, None, out, out.dtype, scale, weight, None, eps)
+    status = lib().dit_rms_norm_forward(args, _raw_stream(x, stream))
+    if status:
+        _check(status)
+
+
+def dit_rms_norm_backward(total, dout, dx, *, dtotal=None, weight=None, dweight=None, eps=1e-6, workspace=None,
+                          stream=None):
+    """Gradient of dit_rms_norm_forward: total is what the norm was of (the
+    forward's total, or x without a residual), dtotal the gradient that reaches
+    it from elsewhere.  dx is the gradient of x, and of residual too; dweight
+    (float32 [channels], overwritten) is computed where given.  workspace: a
+    contiguous tensor of dit_rms_norm_workspace_bytes, or None to take one from
+    torch's allocator (only on torch's current stream)."""
+    args = _norm_args(total, dtotal, None, dout, dx, dx.dtype, None, weight, dweight, eps)
+    L, s, ws, n, owner = lib(), _raw_stream(total, stream), 0, 0, None
+    if dweight is not None:
+        ws, n, owner = _workspace(total, workspace, stream, L.dit_rms_norm_workspace_bytes(args))
+    _check(L.dit_rms_norm_backward(args, ws, n, s))
+
+
+def dit_rms_norm_workspace_bytes(total) -> int:
+    """Workspace of a dit_rms_norm_backward with dweight on tensors of this shape and type."""
+    torch = _torch or _use_torch()
+    shape = total.shape
+    B, N = (shape[0] if len(shape) > 2 else 1), 1
+    for v in shape[1:-1] if len(shape) > 2 else shape[:-1]:
+        N *= v
+    code = _dtype_code(total.dtype)
+    n = lib().dit_rms_norm_workspace_bytes(_NORM_ARGS.pack(B, N, shape[-1], code, code, 0.0, *(0,) * 15, 0, 16, 32))
+    if n < 0:
+        raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
+    return n
+
+
+def _matrix(name, t, shape, dtype):
+    """(pointer, row stride) of a [..., columns] view whose leading axes have one common stride."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype is not dtype:
+        _bad_view(name, t, shape, dtype)
+    if t.numel() == 0:
+        return 0, 0
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        _refuse(DIT_ERR_SHAPE, f"{name}: the last axis must be contiguous")
+    if len(shape) == 2:
+        return t.data_ptr(), stride[0]
+    step = span = None
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if step is None:
+            step = stride[i]
+        elif stride[i] != span:
+            _refuse(DIT_ERR_SHAPE, f"{name}: the axes in front of the last must have one common stride")
+        span = stride[i] * shape[i]
+    return t.data_ptr(), step or 0
+
+
+def _ffn_args(x, w_gate, w_up, out, gate, up, act, scales=(None,) * 3, biases=(None,) * 2, dx=None, dw_gate=None,
+              dw_up=None, dbias_gate=None, dbias_up=None):
+    _torch or _use_torch()
+    if _grad_mode() and _any_requires_grad(x, w_gate, w_up, *biases, *((gate, up, out) if dx is not None or
+                                           dw_gate is not None or dw_up is not None else ())):
+        _refuse_autograd()
+    xs, ws = x.shape, w_gate.shape
+    if len(xs) < 1 or len(ws) != 2 or ws[1] != xs[-1]:
+        _refuse(DIT_ERR_SHAPE, f"x is {list(xs)} and w_gate {list(ws)}: [..., width] and [hidden, width] are wanted")
+    F, D = ws
+    rows = 1
+    for v in xs[:-1]:
+        rows *= v
+    hs, dtype, operand = xs[:-1] + (F,), out.dtype, x.dtype
+    codes = _operand_codes.get(dtype), _operand_codes.get(operand)
+    if None in codes:
+        _refuse(DIT_ERR_INVALID_ARG, f"unsupported dtype {dtype if codes[0] is None else operand}")
+    try:
+        return _FFN_ARGS.pack(rows, D, F, *codes, act, 0, *_matrix("x", x, xs, operand), *_matrix("w_gate", w_gate, ws, operand),
+                              *_matrix("w_up", w_up, ws, operand), _param("x_scale", scales[0], xs[:-1]),
+                              _param("gate_scale", scales[1], ws[:1]), _param("up_scale", scales[2], ws[:1]),
+                              _param("bias_gate", biases[0], ws[:1]), _param("bias_up", biases[1], ws[:1]),
+                              *_matrix("gate", gate, hs, dtype), *_matrix("up", up, hs, dtype),
+                              *_matrix("out", out, hs, dtype), *_matrix("dx", dx, xs, dtype),
+                              *_matrix("dw_gate", dw_gate, ws, dtype), *_matrix("dw_up", dw_up, ws, dtype),
+                              _param("dbias_gate", dbias_gate, ws[:1]), _param("dbias_up", dbias_up, ws[:1]))
+    except (struct.error, OverflowError) as e:
+        _refuse_scalar(e)
+
+
+def dit_gated_ffn_forward(x, w_gate, w_up, out, *, gate=None, up=None, bias_gate=None, bias_up=None, x_scale=None,
+                          gate_scale=None, up_scale=None, act=ACT_SILU, workspace=None, stream=None):
+    """out [..., hidden] = act(x w_gate^T + bias_gate) * (x w_up^T + bias_up) of x
+    [..., width] and weights [hidden, width], in bfloat16 or float16.  gate / up
+    receive the two projections, for the backward call.  With x and the weights
+    in float8_e4m3fn, x_scale (float32 x.shape[:-1]) and gate_scale / up_scale
+    (float32 [hidden]) make the values they stand for.  act: ACT_SILU or
+    ACT_GELU (tanh form).  workspace: a contiguous tensor of
+    dit_gated_ffn_workspace_bytes, or None to take one from torch's allocator
+    where the call needs it (only on torch's current stream)."""
+    args = _ffn_args(x, w_gate, w_up, out, gate, up, act, (x_scale, gate_scale, up_scale), (bias_gate, bias_up))
+    L, s = lib(), _raw_stream(x, stream)
+    ws, n, owner = _workspace(x, workspace, stream, L.dit_gated_ffn_workspace_bytes(args, 0))
+    _check(L.dit_gated_ffn_forward(args, ws, n, s))
+
+
+def dit_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, *, dx=None, dw_gate=None, dw_up=None, dbias_gate=None,
+                           dbias_up=None, act=ACT_SILU, workspace=None, stream=None):
+    """Gradient of dit_gated_ffn_forward from the gate and up that it kept.  Each
+    of dx, dw_gate, dw_up (of the inputs' type) and dbias_gate, dbias_up (float32
+    [hidden]) is overwritten where given."""
+    args = _ffn_args(x, w_gate, w_up, dout, gate, up, act, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dbias_gate=dbias_gate,
+                     dbias_up=dbias_up)
+    L, s = lib(), _raw_stream(x, stream)
+    ws, n, owner = _workspace(x, workspace, stream, L.dit_gated_ffn_workspace_bytes(args, 1))
+    _check(L.dit_gated_ffn_backward(args, ws, n, s))
+
+
+def dit_gated_ffn_workspace_bytes(x, w_gate, *, backward=False) -> int:
+    """Workspace that is enough for any call on tensors of the shapes and types of x and w_gate, whatever their strides
+    and alignment and whichever gradients are wanted."""
+    torch = _torch or _use_torch()
+    rows, most = x.numel() // max(1, x.shape[-1]), 0
+    operand = _operand_codes.get(x.dtype, -1)
+    code, p = DTYPE_BF16 if operand == DTYPE_E4M3 else operand, 16 + 1  # a pointer that needs a copy
+    scale = 16 if operand == DTYPE_E4M3 else 0
+    F, D = w_gate.shape
+    for wanted in ((16, 16, 16), (0, 16, 0), (0, 16, 16)) if backward else ((0, 0, 0),):
+        n = lib().dit_gated_ffn_workspace_bytes(_FFN_ARGS.pack(
+            rows, D, F, code, operand, ACT_SILU, 0, p, D, p, D, p, D, scale, scale, scale, 0, 0, 16, F, 16, F, 16, F,
+            *(v for w in wanted for v in (w, D)), 16 * backward, 16 * backward), int(backward))
+        if n < 0:
+            raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
+        most = max(most, n)
+    return most
+
+
+def dit_gated_ffn_synchronize(stream=None):
+    """Wait for the stream (of the current device) and raise if a gated feed-forward kernel abandoned a wait on it."""
+    _check(lib().dit_gated_ffn_synchronize(_stream(stream)))
+
+
+def _grad_tensors(grads, clipped):
+    torch = _torch or _use_torch()
+    pack, codes, parts, ref = _GRAD_TENSOR.pack, _dtype_codes, [], None
+    for i, g in enumerate(grads):
+        if g is None:
+            continue
+        o = None if clipped is None else clipped[i]
+        code = codes.get(g.dtype)
+        if code is None:
+            _refuse(DIT_ERR_INVALID_ARG, f"gradient {i} is {g.dtype}")
+        if not g.is_contiguous():
+            _refuse(DIT_ERR_SHAPE, f"gradient {i} must be contiguous")
+        if o is not None and o is not g and (o.shape != g.shape or o.dtype is not g.dtype or not o.is_contiguous()):
+            _refuse(DIT_ERR_SHAPE, f"the output of gradient {i} must be contiguous, of its shape and type")
+        if g.numel():
+            parts.append(pack(g.data_ptr(), 0 if o is None else o.data_ptr(), g.numel(), code, 0))
+    return b"".join(parts), len(parts)
+
+
+def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, stream=None):
+    """norm (a float32 CUDA tensor of one element) = the 2-norm of all tensors of
+    the list `grads` together (None entries are left out).  With max_norm they
+    are multiplied by max_norm / norm where norm is above it, in place or into
+    the list `clipped`; a norm that is not finite leaves the values as they
+    are.  workspace: a contiguous tensor of dit_grad_norm_workspace_bytes, or
+    None to take one from torch's allocator (only on torch's current stream)."""
+    torch = _torch or _use_torch()
+    grads = list(grads)
+    if max_norm is None:
+        if clipped is not None:
+            _refuse(DIT_ERR_INVALID_ARG, "clipped without max_norm")
+    elif clipped is None:
+        clipped = grads
+    else:
+        clipped = list(clipped)
+        if len(clipped) != len(grads) or any((c is None) != (g is None) for c, g in zip(clipped, grads)):
+            _refuse(DIT_ERR_SHAPE, "clipped must hold one tensor for each gradient")
+    if norm.dtype is not torch.float32 or norm.numel() != 1:
+        _refuse(DIT_ERR_INVALID_ARG, "norm must be one float32")
+    if _grad_mode() and _any_requires_grad(*grads):
+        _refuse_autograd()
+    tensors, n = _grad_tensors(grads, clipped)
+    L, s = lib(), _raw_stream(norm, stream)
+    ws, size, owner = _workspace(norm, workspace, stream, L.dit_grad_norm_workspace_bytes(tensors, n))
+    try:
+        limit = C.c_float(float("inf") if max_norm is None else max_norm)
+    except TypeError as e:
+        _refuse_scalar(e)
+    if max_norm is not None and limit.value == float("inf"):
+        _refuse(DIT_ERR_INVALID_ARG, "max_norm must be finite (None: the norm only)")
+    _check(L.dit_grad_norm(tensors, n, limit, norm.data_ptr(), ws, size, s))
+
+
+def dit_grad_norm_workspace_bytes(grads) -> int:
+    """Workspace of a dit_grad_norm call on these tensors."""
+    n = lib().dit_grad_norm_workspace_bytes(*_grad_tensors(list(grads), None))
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
     return n

@@ -35,7 +35,7 @@
  *     Calls of one model on two unordered streams race on the workspace.
  *     Separate models share nothing and may run concurrently.
  *   - Floating-point tensors crossing the ABI are float32, row-major, densely
- *     packed, in the layouts given per call (dit_rope_* and dit_group_norm_*
+ *     packed, in the layouts given per call (the operators beside the model
  *     take strided views of float32, bfloat16 or float16 activations).  B is
  *     the batch of network passes; in the loop B = 2 x requests with CFG
  *     (conditional passes first, then unconditional ones).
@@ -62,9 +62,9 @@ typedef enum {
 
 enum { DIT_PREC_BF16 = 0, DIT_PREC_F32 = 1, DIT_PREC_FP8 = 2 };
 enum { DIT_COND_CROSS = 0, DIT_COND_JOINT = 1 };
-/* DIT_DTYPE_F16 is a type of the rotation and group-norm operators only:
- * dit_load_weights takes the other two. */
-enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1, DIT_DTYPE_F16 = 2 };
+/* DIT_DTYPE_F16 and DIT_DTYPE_E4M3 are types of the operators beside the model
+ * only: dit_load_weights takes the other two. */
+enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1, DIT_DTYPE_F16 = 2, DIT_DTYPE_E4M3 = 3 };
 /* dit_denoise_loop flags */
 enum {
   DIT_LOOP_PARTIAL_SCHEDULE = 1, /* allow sigmas[0] != 1 or sigmas[n] != 0                     */
@@ -320,7 +320,7 @@ int64_t dit_rope_workspace_bytes(const dit_rope_args* a);
  * channels / groups consecutive channels are normalised over all pixels with
  * their mean and population variance, then y = act(xhat * weight + bias) per
  * channel.  Statistics and arithmetic are fp32, rounded once to the type.  */
-enum { DIT_ACT_NONE = 0, DIT_ACT_SILU = 1 };
+enum { DIT_ACT_NONE = 0, DIT_ACT_SILU = 1, DIT_ACT_GELU = 2 };  /* GELU (tanh form): dit_gated_ffn_* only */
 typedef struct {
   int64_t batch;
   int64_t pixels;
@@ -354,6 +354,134 @@ dit_status dit_group_norm_backward(const dit_group_norm_args* a, void* workspace
  * (host-only query, from the sizes and the type alone: enough for any strides
  * and alignment); -1 for arguments the call would refuse. */
 int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backward);
+
+/* RMS norm of channels-last activations with the residual's addition in front
+ * of it: the feed-forward half of a block beside the denoiser's own (norm, then
+ * dit_gated_ffn_forward).  x, residual, total and out are views [batch, tokens,
+ * channels] whose last axis is contiguous; strides in elements, of the batch and
+ * token axes.
+ *   total = x + residual, rounded once to the type (total = x without residual)
+ *   y = total * weight / sqrt(mean(total^2) + eps), the mean over the channels
+ * out holds y in the type of x, or in e4m3 with a scale for each row: scale =
+ * max |y| / 448 (1 for a row of zeros), out = y / scale rounded to nearest even.
+ * Such a row with a NaN or an infinity in it gets the scale NaN and zeros.  The
+ * outputs total and out may be the very view of x or of residual (out only in
+ * the type of x).  Arithmetic is fp32. */
+enum { DIT_RMS_NORM_MAX_CHANNELS = 16384 };
+typedef struct {
+  int64_t batch;
+  int64_t tokens;
+  int32_t channels;      /* 1 .. DIT_RMS_NORM_MAX_CHANNELS                               */
+  int32_t dtype;         /* DIT_DTYPE_F32, _BF16, _F16                                   */
+  int32_t out_dtype;     /* forward: dtype, or DIT_DTYPE_E4M3; backward: dtype           */
+  float eps;             /* >= 0                                                         */
+  const void* x;         /* forward: input; backward: what the norm was of (the forward's total) */
+  int64_t x_stride[2];
+  const void* residual;  /* forward: or NULL; backward: the gradient that reaches total from elsewhere, or NULL */
+  int64_t residual_stride[2];
+  void* total;           /* forward: x + residual, or NULL: not wanted (NULL without residual); backward: NULL */
+  int64_t total_stride[2];
+  const void* dy;        /* backward: gradient of the forward's out                      */
+  int64_t dy_stride[2];
+  void* out;             /* forward: y; backward: the gradient of x, which is that of residual too */
+  int64_t out_stride[2];
+  float* scale;          /* out_dtype e4m3: device float[batch, tokens], dense; else NULL */
+  const float* weight;   /* device float[channels], or NULL: 1                           */
+  float* dweight;        /* backward: device float[channels], or NULL: not wanted        */
+} dit_rms_norm_args;
+
+dit_status dit_rms_norm_forward(const dit_rms_norm_args* a, void* stream);
+/* dweight is the sum over batch and tokens in fp32 (overwritten; zero for no
+ * rows) and needs workspace.  out may be the very view of x, residual or dy. */
+dit_status dit_rms_norm_backward(const dit_rms_norm_args* a, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes dit_rms_norm_backward needs (host-only query; pointers are read as
+ * present or NULL only); -1 for arguments the call would refuse. */
+int64_t dit_rms_norm_workspace_bytes(const dit_rms_norm_args* a);
+
+/* Gated feed-forward: both projections, the activation and the product,
+ *   gate = x w_gate^T + bias_gate,  up = x w_up^T + bias_up,
+ *   out = act(gate) * up
+ * with act SiLU or GELU (tanh form), where the denoiser's own MLP has one
+ * projection and GELU.  x is [rows, width], the weights [hidden, width], out,
+ * gate and up [rows, hidden], all with a contiguous last axis and one stride in
+ * elements.  dtype is that of out, gate and up, and (operand_dtype ==
+ * dtype) of x and the weights.  With operand_dtype DIT_DTYPE_E4M3, x and the
+ * weights are e4m3, x * x_scale[row] and w * scale[channel] the values they
+ * stand for; forward only.  Sums are fp32 on the tensor cores, every output is
+ * rounded once.  Operands whose pointer or stride is no multiple of 16 bytes
+ * are copied into the workspace first. */
+typedef struct {
+  int64_t rows;
+  int32_t width;             /* 1 .. 2^17                                                   */
+  int32_t hidden;            /* 1 .. 2^17                                                   */
+  int32_t dtype;             /* DIT_DTYPE_BF16 or DIT_DTYPE_F16                             */
+  int32_t operand_dtype;     /* dtype, or DIT_DTYPE_E4M3 (forward)                          */
+  int32_t act;               /* DIT_ACT_SILU or DIT_ACT_GELU                                */
+  int32_t reserved;          /* 0                                                           */
+  const void* x;
+  int64_t x_stride;
+  const void* w_gate;
+  int64_t w_gate_stride;
+  const void* w_up;
+  int64_t w_up_stride;
+  const float* x_scale;      /* e4m3: device float[rows]; else NULL                         */
+  const float* gate_scale;   /* e4m3: device float[hidden]; else NULL                       */
+  const float* up_scale;     /* e4m3: device float[hidden]; else NULL                       */
+  const float* bias_gate;    /* forward: device float[hidden], or NULL: 0                   */
+  const float* bias_up;      /* forward: device float[hidden], or NULL: 0                   */
+  void* gate;                /* forward: kept for the backward call, or NULL; backward: read */
+  int64_t gate_stride;
+  void* up;                  /* as gate; both or neither                                    */
+  int64_t up_stride;
+  void* out;                 /* forward: output; backward: the output's gradient, read      */
+  int64_t out_stride;
+  void* dx;                  /* backward: gradient of x, or NULL: not wanted                */
+  int64_t dx_stride;
+  void* dw_gate;             /* backward: gradients of the weights, or NULL: not wanted     */
+  int64_t dw_gate_stride;
+  void* dw_up;
+  int64_t dw_up_stride;
+  float* dbias_gate;         /* backward: device float[hidden], or NULL: not wanted         */
+  float* dbias_up;
+} dit_gated_ffn_args;
+
+dit_status dit_gated_ffn_forward(const dit_gated_ffn_args* a, void* workspace, int64_t workspace_bytes, void* stream);
+/* The gradient from the gate and up that the forward call kept.  The gradients
+ * of gate and up are formed in fp32, summed into dbias_* as they are, and
+ * rounded to dtype as operands of the products; dx, dw_gate and dw_up are fp32
+ * sums rounded to dtype (overwritten; zero for no rows). */
+dit_status dit_gated_ffn_backward(const dit_gated_ffn_args* a, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes of workspace of the forward (backward == 0) or the backward call
+ * (host-only query; pointers are read as present, NULL or aligned only);
+ * -1 for arguments the call would refuse. */
+int64_t dit_gated_ffn_workspace_bytes(const dit_gated_ffn_args* a, int backward);
+/* Synchronise `stream`, a stream of the current device, and report
+ * DIT_ERR_TIMEOUT if a kernel of dit_gated_ffn_* on that device abandoned a
+ * bounded wait since the last check (its outputs are then invalid). */
+dit_status dit_gated_ffn_synchronize(void* stream);
+
+/* The norm of many tensors together (the gradients of a model, after a
+ * backward pass), and their clipping to it:
+ *   norm = sqrt(sum of all squares),
+ *   out = grad * (norm > max_norm ? max_norm / norm : 1), rounded once.
+ * Tensors are dense, of one type each.  A tensor's out may be the very grad
+ * (then nothing is written unless the norm is above max_norm); all are NULL
+ * when max_norm is infinite: the norm only.  A norm that is NaN or infinite
+ * leaves the values as they are: the caller learns of it by the norm.  Squares
+ * are summed in fp32 over a few dozen values and in fp64 from there, and do not
+ * overflow. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype;         /* DIT_DTYPE_F32, _BF16 or _F16 */
+  int32_t reserved;      /* 0 */
+} dit_grad_tensor;
+/* tensors: host array of n entries, read before the call returns; max_norm >= 0;
+ * norm: device float.  workspace of dit_grad_norm_workspace_bytes. */
+dit_status dit_grad_norm(const dit_grad_tensor* tensors, int64_t n, float max_norm, float* norm, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+int64_t dit_grad_norm_workspace_bytes(const dit_grad_tensor* tensors, int64_t n);
 
 /* The whole denoiser stage for `batch` requests: the denoiser role of
  * SGLang-Diffusion "Disaggregated Diffusion Pipeline" (Quick Start, role
