@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libdit.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libdit_debug.so")
 SOURCES = ["dit_api.cu", "elementwise.cu", "simt_f32.cu", "gemm_tc.cu", "attn_tc.cu", "operators_api.cu", "rope.cu",
-           "group_norm.cu", "ffn_api.cu", "rms_norm.cu", "gated_ffn.cu", "grad_norm.cu"]
+           "group_norm.cu", "ffn_api.cu", "rms_norm.cu", "rms_norm_f32.cu", "rms_norm_bf16.cu",
+           "rms_norm_f16.cu", "gated_ffn.cu", "grad_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(PKG, "..", "include")]

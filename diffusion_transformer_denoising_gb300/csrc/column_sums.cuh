@@ -6,10 +6,9 @@
 
 namespace dit {
 
-// out[c] = sum over p of partial[p][c], c < n, in the same order every time: 32
-// columns a block, each in 32 strands of a loss-free sum (the rows may be many),
-// joined as a tree.  Two sums of n columns a launch (blockIdx.y), each with an
-// output that may be NULL.
+// out[c] = sum over p of partial[p][c], c < n, in the same order every time: 8 columns
+// a block, each in 64 strands of a loss-free sum (the rows may be many), joined as a
+// tree.  Two sums of n columns a launch (blockIdx.y), each with an output that may be NULL.
 struct ColumnSums {
   const float* partial;
   int64_t rows, pitch;  // floats between partial rows
@@ -17,36 +16,39 @@ struct ColumnSums {
   int64_t second;       // floats from the first sum's columns to the second's
   float* out[2];
 };
+constexpr int kSumColumns = 8, kSumStrands = 64;
 template <int UNUSED = 0>
-__global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnSums a) {
-  __shared__ float strands[32][33];
+__global__ void __launch_bounds__(kSumColumns * kSumStrands) column_sums_kernel(const ColumnSums a) {
+  __shared__ float strands[kSumColumns][kSumStrands + 1];
   float* out = a.out[blockIdx.y];
+  const int col = threadIdx.x % kSumColumns, strand = threadIdx.x / kSumColumns;
+  const int c = blockIdx.x * kSumColumns + col;
   wait_previous();
   if (!out) return;
-  const float* partial = a.partial + blockIdx.y * a.second;
-  const int c = blockIdx.x * 32 + threadIdx.x;
   LongSum s;
   if (c < a.n) {
-    int64_t p = threadIdx.y;
-    for (; p + 96 < a.rows; p += 128) {
-      float v[4];
+    const float* p = a.partial + blockIdx.y * a.second + c;
+    constexpr int U = 8;  // loads under way
+    for (int64_t r = strand; r < a.rows; r += U * kSumStrands) {
+      float v[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = partial[(p + 32 * i) * a.pitch + c];
+      for (int i = 0; i < U; ++i) v[i] = r + i * kSumStrands < a.rows ? p[(r + i * kSumStrands) * a.pitch] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.add(v[i]);
+      for (int i = 0; i < U; ++i) s.add(v[i]);
     }
-    for (; p < a.rows; p += 32) s.add(partial[p * a.pitch + c]);
   }
-  strands[threadIdx.y][threadIdx.x] = s.value();
+  strands[col][strand] = s.value();
   __syncthreads();
-  float v = strands[threadIdx.x][threadIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp >= kSumColumns) return;
+  float v = strands[warp][lane] + strands[warp][lane + 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < a.n) out[col] = v;
+  if (lane == 0 && blockIdx.x * kSumColumns + warp < a.n) out[blockIdx.x * kSumColumns + warp] = v;
 }
 inline cudaError_t column_sums(const ColumnSums& a, cudaStream_t s) {
-  return launch_kernel(column_sums_kernel<0>, dim3((a.n + 31) / 32, a.out[1] ? 2 : 1), dim3(32, 32), 0, s, 1, true, a);
+  return launch_kernel(column_sums_kernel<0>, dim3((a.n + kSumColumns - 1) / kSumColumns, a.out[1] ? 2 : 1),
+                       dim3(kSumColumns * kSumStrands), 0, s, 1, true, a);
 }
 
 }  // namespace dit

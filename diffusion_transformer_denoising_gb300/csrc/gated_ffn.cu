@@ -75,59 +75,76 @@ struct Product {
 };
 
 // ---------------------------------------------------------------- activation
-// sigmoid(z) and 1 - sigmoid(z), each with a relative error of a few 2^-22
-// (ex2.approx and rcp.approx; the results are rounded to 16 bits).
-DIT_DEV float2 sigmoids(float z) {
-  float e;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-fabsf(z) * 1.4426950408889634f));
-  const float r = __fdividef(1.f, 1.f + e);
-  const float er = e * r;
-  return z >= 0.f ? make_float2(r, er) : make_float2(er, r);
-}
+// z = g (SiLU) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (GELU, tanh form): act(g) = g sigmoid(z).
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by ex2.approx and rcp.approx, a few 2^-22 of
+// itself (the results are rounded to 16 bits), 0 below z = -87.
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-DIT_DEV float activation(int act, float g) {
-  const float z = act == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, g * g, kGelu2);
-  return g * sigmoids(z).x;
+DIT_DEV float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// act(g) and act'(g)
-DIT_DEV float2 activation_slope(int act, float g) {
+// act(g) u of two columns
+template <int ACT>
+DIT_DEV float2 gated2(float2 g, float2 u) {
+  float2 m;  // -z log2 e
+  if constexpr (ACT == DIT_ACT_SILU) {
+    m = fmul2(g, make_float2(-kLog2e, -kLog2e));
+  } else {
+    constexpr float k0 = -kGelu2 * kLog2e, k1 = k0 * 0.044715f;
+    m = fmul2(g, ffma2(fmul2(g, g), make_float2(k1, k1), make_float2(k0, k0)));
+  }
+  const float2 d = fadd2(make_float2(ex2_approx(m.x), ex2_approx(m.y)), make_float2(1.f, 1.f));
+  return fmul2(fmul2(g, make_float2(rcp_approx(d.x), rcp_approx(d.y))), u);
+}
+// act(g) and act'(g) = s + g s (1 - s) z'
+template <int ACT>
+DIT_DEV float2 activation_slope(float g) {
   const float q = g * g;
-  const float z = act == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, q, kGelu2);
-  const float zp = act == DIT_ACT_SILU ? 1.f : fmaf(3.f * 0.044715f * kGelu2, q, kGelu2);
-  const float2 s = sigmoids(z);
-  // far out 1 - s is 0 and z' may be infinite: the limit of their product is 0
-  return make_float2(g * s.x, s.x == 0.f || s.y == 0.f ? s.x : fmaf(g * s.x * s.y, zp, s.x));
+  const float z = ACT == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, q, kGelu2);
+  const float e = ex2_approx(fminf(-z * kLog2e, 126.f));
+  const float s = rcp_approx(1.f + e), gs = g * s, rest = e * s;  // rest = 1 - s
+  if constexpr (ACT == DIT_ACT_SILU) return make_float2(gs, fmaf(gs, rest, s));
+  // far out rest is 0 and z' may be infinite: the limit of their product is 0
+  const float zp = fmaf(3.f * 0.044715f * kGelu2, q, kGelu2);
+  return make_float2(gs, rest == 0.f ? s : fmaf(gs * rest, zp, s));
 }
 
 DIT_DEV uint32_t pack16(int f16, float lo, float hi) { return f16 ? pack2<__half>(lo, hi) : pack_bf16x2(lo, hi); }
 
-// Four values of a per-column array from column c on, 0 from n on.
-DIT_DEV float4 columns4(const float* p, int c, int n, bool aligned) {
-  if (aligned && c + 4 <= n) return __ldg(reinterpret_cast<const float4*>(p + c));
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < n) v.x = __ldg(p + c);
-  if (c + 1 < n) v.y = __ldg(p + c + 1);
-  if (c + 2 < n) v.z = __ldg(p + c + 2);
-  if (c + 3 < n) v.w = __ldg(p + c + 3);
-  return v;
-}
-
-// acc * (row_scale * scale) + bias over 32 columns
-DIT_DEV void finish32(float (&v)[32], const Product& P, int side, float row_scale, int c0) {
-  const float* sc = P.scale[side];
-  const float* bi = P.bias[side];
-  if (!sc && !bi) return;
-  const bool sa = (reinterpret_cast<uintptr_t>(sc) & 15) == 0, ba = (reinterpret_cast<uintptr_t>(bi) & 15) == 0;
+// 32 values of a per-column array from column c on, `none` from n on or without an
+// array.  One branch for all of them: with a branch for every four columns, which keeps
+// the loads of a tile apart, the e4m3 video case took 728 us instead of 543.
+DIT_DEV void columns32(float (&v)[32], const float* p, int c, int n, float none) {
+  if (p && c + 32 <= n && ((reinterpret_cast<uintptr_t>(p + c) & 15) == 0)) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    const float4 b = bi ? columns4(bi, c0 + j, P.N, ba) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (sc) {
-      const float4 w = columns4(sc, c0 + j, P.N, sa);
-      v[j] = fmaf(v[j], row_scale * w.x, b.x), v[j + 1] = fmaf(v[j + 1], row_scale * w.y, b.y);
-      v[j + 2] = fmaf(v[j + 2], row_scale * w.z, b.z), v[j + 3] = fmaf(v[j + 3], row_scale * w.w, b.w);
-    } else {
-      v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+    for (int j = 0; j < 32; j += 4) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(p + c + j));
+      v[j] = t.x, v[j + 1] = t.y, v[j + 2] = t.z, v[j + 3] = t.w;
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = p && c + j < n ? __ldg(p + c + j) : none;
+  }
+}
+// acc * (row_scale * scale) + bias over 32 columns
+template <bool SCALED>
+DIT_DEV void finish32(float (&v)[32], const Product& P, int side, float row_scale, int c0) {
+  float w[32];
+  if constexpr (SCALED) {
+    columns32(w, P.scale[side], c0, P.N, 0.f);
+    const float2 rs = make_float2(row_scale, row_scale);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 x = fmul2(make_float2(v[j], v[j + 1]), fmul2(rs, make_float2(w[j], w[j + 1])));
+      v[j] = x.x, v[j + 1] = x.y;
+    }
+  }
+  if (P.bias[side]) {
+    columns32(w, P.bias[side], c0, P.N, 0.f);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += w[j];
   }
 }
 
@@ -209,7 +226,7 @@ DIT_DEV void store_partial(const Product& P, float* plane, int64_t row, int c0, 
 
 // One accumulator out of tensor memory: rows row0 .. row0 + 31 of this warp,
 // units of 64 output columns half, half + 2, ...; release() after the last read.
-template <int MODE, int BN, class Release>
+template <int MODE, bool F8, int ACT, int BN, class Release>
 DIT_DEV void drain(const Product& P, const Tile& t, uint32_t tacc, int64_t row0, int half, uint8_t* stg, Release release) {
   constexpr int COLS = MODE == FWD ? BN / 2 : BN;  // output columns of the tile
   const int lane = threadIdx.x & 31;
@@ -258,14 +275,17 @@ DIT_DEV void drain(const Product& P, const Tile& t, uint32_t tacc, int64_t row0,
             wait32(g);
             wait32(v);
             if (last && hh == 1) done();
-            finish32(g, P, 0, row_scale, col0 + hh * 32);
-            finish32(v, P, 1, row_scale, col0 + hh * 32);
+            finish32<F8>(g, P, 0, row_scale, col0 + hh * 32);
+            finish32<F8>(v, P, 1, row_scale, col0 + hh * 32);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= activation(P.act, g[j]);
+            for (int j = 0; j < 32; j += 2) {
+              const float2 h = gated2<ACT>(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
+              v[j] = h.x, v[j + 1] = h.y;
+            }
           } else {
             load32(at + (o - 1) * (BN / 2), v);
             wait32(v);
-            finish32(v, P, o - 1, row_scale, col0 + hh * 32);
+            finish32<F8>(v, P, o - 1, row_scale, col0 + hh * 32);
           }
           stage32(stg, hh, P.f16, v);
         }
@@ -286,7 +306,7 @@ DIT_DEV void drain(const Product& P, const Tile& t, uint32_t tacc, int64_t row0,
   }
 }
 
-template <int MODE, bool F8, bool PAIR>
+template <int MODE, bool F8, bool PAIR, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P) {
   using C = Cfg<F8, PAIR>;
   constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;  // operands that lie across K
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if constexpr (PAIR) mbar_arrive_cluster(tempty_leader + acc * (uint32_t)sizeof(uint64_t));
         else mbar_arrive(&tempty[acc]);
       };
-      drain<MODE, C::BN>(P, t, tmem_base + acc * C::BN + ((uint32_t)(q * 32) << 16), row0, half, stg, release);
+      drain<MODE, F8, ACT, C::BN>(P, t, tmem_base + acc * C::BN + ((uint32_t)(q * 32) << 16), row0, half, stg, release);
     }
     if (!ok && lane == 0) abort_pair();
     if (lane == 0) bulk_wait0();  // this warp's tensor stores have landed
@@ -488,6 +508,133 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Forward of at most 32 rows: both weights are all there is to read.  A block takes
+// 16 hidden channels, its warps a part of K each, and every lane fetches 16-byte
+// pieces of the weights' rows straight into registers, four steps at a time.  The
+// products run on mma.m16n8k16 with the channels as rows and 8 tokens as columns: a
+// lane's eight neighbours in K serve as the fragment's scattered ones, of x alike.
+// e4m3 is widened to fp16, which holds it exactly.
+struct Few {
+  const uint8_t *x, *w[2];
+  int64_t ldx, ldw[2];  // bytes
+  const float *x_scale, *scale[2], *bias[2];
+  uint16_t* out[3];
+  int64_t ldo[3];       // elements
+  int M, D, F;
+};
+constexpr int kFewWarps = 4, kFewRows = 32;
+
+// 16 bytes of a row from element k on (k a multiple of 16 bytes), zeros from D on.
+// WHOLE: D and the row's address are multiples of 16 bytes.
+template <bool F8, bool WHOLE>
+DIT_DEV uint4 piece(const uint8_t* row, int k, int D) {
+  constexpr int E = F8 ? 16 : 8;
+  if (WHOLE) {
+    if (k < D) return __ldg(reinterpret_cast<const uint4*>(row + k * (16 / E)));
+    return make_uint4(0, 0, 0, 0);
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    if (k + j >= D) continue;
+    if constexpr (F8) w[j / 4] |= (uint32_t)__ldg(row + k + j) << (8 * (j & 3));
+    else w[j / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + k + j) << (16 * (j & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+DIT_DEV uint32_t widen(uint32_t two_e4m3) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two_e4m3));
+  return h;
+}
+template <bool F16>
+DIT_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c += the 16 channels' pieces (rows g and g + 8) x 8 tokens' pieces
+template <bool F8, bool F16>
+DIT_DEV void products(float (&c)[4], const uint4& lo, const uint4& hi, const uint4& x) {
+  const uint32_t *a = &lo.x, *b = &hi.x, *t = &x.x;
+  if constexpr (F8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      mma16816<true>(c, widen(a[j]), widen(b[j]), widen(a[j] >> 16), widen(b[j] >> 16), widen(t[j]), widen(t[j] >> 16));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) mma16816<F16>(c, a[j], b[j], a[j + 1], b[j + 1], t[j], t[j + 1]);
+  }
+}
+
+// NT: groups of 8 tokens.  F16: the output's type, and of 16-bit operands theirs.
+template <bool F8, bool F16, int NT, bool WHOLE, int ACT>
+__global__ void __launch_bounds__(32 * kFewWarps, 4) few_rows_kernel(const Few a) {
+  constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 ? 2 : 4;
+  __shared__ float sums[2][kFewWarps][NT][16][9];
+  wait_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int f0 = blockIdx.x * 16;
+  const int steps = (a.D + STEP - 1) / STEP;
+  const int s0 = steps * warp / kFewWarps, s1 = steps * (warp + 1) / kFewWarps;
+  const uint8_t* rows[2][2];  // of channels that are not there: the last one's (never stored)
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    rows[m][0] = a.w[m] + min(f0 + g, a.F - 1) * a.ldw[m];
+    rows[m][1] = a.w[m] + min(f0 + g + 8, a.F - 1) * a.ldw[m];
+  }
+  float acc[2][NT][4] = {};
+  for (int s = s0; s < s1; s += U) {
+    uint4 w[U][2][2], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = s + u < s1 ? (s + u) * STEP + t * E : a.D;  // from D on: zeros
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        w[u][m][0] = piece<F8, WHOLE>(rows[m][0], k, a.D);
+        w[u][m][1] = piece<F8, WHOLE>(rows[m][1], k, a.D);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[u][n] = piece<F8, WHOLE>(a.x + (n * 8 + g) * a.ldx, n * 8 + g < a.M ? k : a.D, a.D);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) products<F8, F16>(acc[m][n], w[u][m][0], w[u][m][1], x[u][n]);
+  }
+  // accumulator element (row g or g + 8, token 2 t or 2 t + 1)
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sums[m][warp][n][g + (j >> 1) * 8][2 * t + (j & 1)] = acc[m][n][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 128 * NT; i += 32 * kFewWarps) {
+    const int c = i & 15, tok = (i >> 4) & 7, n = i >> 7;
+    const int row = n * 8 + tok, f = f0 + c;
+    if (row >= a.M || f >= a.F) continue;
+    float v[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      v[m] = sums[m][0][n][c][tok];
+#pragma unroll
+      for (int w = 1; w < kFewWarps; ++w) v[m] += sums[m][w][n][c][tok];
+      if constexpr (F8) v[m] *= __ldg(a.x_scale + row) * __ldg(a.scale[m] + f);
+      if (a.bias[m]) v[m] += __ldg(a.bias[m] + f);
+      if (a.out[1]) a.out[1 + m][row * a.ldo[1 + m] + f] = (uint16_t)pack16(F16, v[m], 0.f);
+    }
+    const float2 h = gated2<ACT>(make_float2(v[0], v[0]), make_float2(v[1], v[1]));
+    a.out[0][row * a.ldo[0] + f] = (uint16_t)pack16(F16, h.x, 0.f);
   }
 }
 
@@ -554,7 +701,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Join J) {
         store4(J.out[2], row * J.ldo[2] + c, n, J.f16, v);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= activation(J.act, g[j]);
+      for (int j = 0; j < 4; j += 2) {
+        const float2 a = make_float2(g[j], g[j + 1]), b = make_float2(v[j], v[j + 1]);
+        const float2 h = J.act == DIT_ACT_SILU ? gated2<DIT_ACT_SILU>(a, b) : gated2<DIT_ACT_GELU>(a, b);
+        v[j] = h.x, v[j + 1] = h.y;
+      }
       store4(J.out[0], row * J.ldo[0] + c, n, J.f16, v);
     } else {
       sum_planes(p + (int64_t)blockIdx.z * J.splits * J.plane, J.plane, J.splits, v);
@@ -593,28 +744,24 @@ struct Slopes {
   int64_t pitch;
   float* partial;         // [row block][2][pitch] sums of the block's rows, or NULL
   int64_t M;
-  int F, rows_per_block, f16, act;
+  int F, rows_per_block;
 };
 
-DIT_DEV void load8(const uint16_t* p, int n, int f16, float (&v)[8]) {
+template <bool ALIGNED>
+DIT_DEV uint4 load8(const uint16_t* p, int n) {
+  if constexpr (ALIGNED) return __ldcs(reinterpret_cast<const uint4*>(p));
   uint32_t w[4];
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    const uint4 t = __ldcs(reinterpret_cast<const uint4*>(p));
-    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
-  } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 t = f16 ? unpack2<__half>(w[j]) : unpack2<__nv_bfloat16>(w[j]);
-    v[2 * j] = t.x, v[2 * j + 1] = t.y;
-  }
+  for (int j = 0; j < 4; ++j)
+    w[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 256 columns (8 a lane) x rows_per_block rows a block, 8 rows at a time.
+// 256 columns (8 a lane) x rows_per_block rows a block, 8 x ROWS rows at a time.
+// ALIGNED: rows of whole 16-byte vectors.
+template <typename T, int ACT, bool ALIGNED>
 __global__ void __launch_bounds__(256) slopes_kernel(const Slopes a) {
+  constexpr int ROWS = 2;
   __shared__ float sums[8][2][32][9];
   wait_previous();
   const int lane = threadIdx.x, ty = threadIdx.y;
@@ -624,28 +771,38 @@ __global__ void __launch_bounds__(256) slopes_kernel(const Slopes a) {
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_block;
   const int64_t r1 = min(a.M, r0 + a.rows_per_block);
   if (n > 0) {
-    for (int64_t r = r0 + ty; r < r1; r += 8) {
-      float g[8], u[8], d[8];
-      load8(a.gate + r * a.ld_gate + c, n, a.f16, g);
-      load8(a.up + r * a.ld_up + c, n, a.f16, u);
-      load8(a.dout + r * a.ld_dout + c, n, a.f16, d);
-      uint32_t wg[4], wu[4];
+    for (int64_t r = r0 + ty; r < r1; r += 8 * ROWS) {
+      uint4 raw[ROWS][3];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 s = activation_slope(a.act, g[j]);
-        g[j] = d[j] * u[j] * s.y;
-        u[j] = d[j] * s.x;
-        if (j >= n) g[j] = u[j] = 0.f;
-        sg[j] += g[j], su[j] += u[j];
+      for (int k = 0; k < ROWS; ++k) {
+        const int64_t at = r + 8 * k;
+        if (at >= r1) continue;
+        raw[k][0] = load8<ALIGNED>(a.gate + at * a.ld_gate + c, n);
+        raw[k][1] = load8<ALIGNED>(a.up + at * a.ld_up + c, n);
+        raw[k][2] = load8<ALIGNED>(a.dout + at * a.ld_dout + c, n);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        wg[j] = pack16(a.f16, g[2 * j], g[2 * j + 1]);
-        wu[j] = pack16(a.f16, u[2 * j], u[2 * j + 1]);
+      for (int k = 0; k < ROWS; ++k) {
+        const int64_t at = r + 8 * k;
+        if (at >= r1) continue;
+        const uint32_t *pg = &raw[k][0].x, *pu = &raw[k][1].x, *pd = &raw[k][2].x;
+        uint32_t wg[4], wu[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 g = unpack2<T>(pg[j]), u = unpack2<T>(pu[j]), d = unpack2<T>(pd[j]);
+          const float2 s0 = activation_slope<ACT>(g.x), s1 = activation_slope<ACT>(g.y);
+          float2 dg = fmul2(fmul2(d, u), make_float2(s0.y, s1.y)), du = fmul2(d, make_float2(s0.x, s1.x));
+          if (!ALIGNED && 2 * j >= n) dg.x = du.x = 0.f;
+          if (!ALIGNED && 2 * j + 1 >= n) dg.y = du.y = 0.f;
+          sg[2 * j] += dg.x, sg[2 * j + 1] += dg.y;
+          su[2 * j] += du.x, su[2 * j + 1] += du.y;
+          wg[j] = pack2<T>(dg.x, dg.y);
+          wu[j] = pack2<T>(du.x, du.y);
+        }
+        // c + 8 <= pitch: the pitch is a multiple of 8
+        *reinterpret_cast<uint4*>(a.dgate + at * a.pitch + c) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+        *reinterpret_cast<uint4*>(a.dup + at * a.pitch + c) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
       }
-      // c + 8 <= pitch: the pitch is a multiple of 8
-      *reinterpret_cast<uint4*>(a.dgate + r * a.pitch + c) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-      *reinterpret_cast<uint4*>(a.dup + r * a.pitch + c) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
     }
   }
   if (!a.partial) return;
@@ -701,6 +858,7 @@ struct Operand {
 struct Plan {
   Operand x, wg, wu;
   Split fwd, dx, dw;
+  bool few = false;
   int64_t slopes = -1, slope_pitch = 0;   // [rows][2][pitch] 16-bit
   int64_t sums = -1, sum_blocks = 0, rows_per_block = 0;
   int64_t partial = -1;
@@ -717,11 +875,12 @@ int64_t planes(const Split& s, int64_t M, int64_t N, int sides) {
 Plan make_plan(const dit_gated_ffn_args& a, bool backward) {
   Plan p;
   const int esz = a.operand_dtype == DIT_DTYPE_E4M3 ? 1 : 2;
+  p.few = !backward && a.rows <= kFewRows;
   auto operand = [&](Operand& o, const void* ptr, int64_t stride, int64_t rows, bool used) {
     o.p = ptr, o.stride = stride;
     if (rows <= 1) o.stride = round_up(a.width, 16 / esz);  // the stride of a single row says nothing
     // as a tensor map wants them: 16-byte rows, strides below 2^40 bytes; rows that overlap are no matrix
-    o.packed = used && ((((uintptr_t)ptr | (uintptr_t)(o.stride * esz)) & 15) != 0 || o.stride < a.width ||
+    o.packed = used && !p.few && ((((uintptr_t)ptr | (uintptr_t)(o.stride * esz)) & 15) != 0 || o.stride < a.width ||
                         o.stride * esz >= kMaxStride);
     o.pitch = round_up(a.width, 16 / esz);
     o.offset = o.packed ? p.take(rows * o.pitch * esz) : 0;
@@ -730,6 +889,7 @@ Plan make_plan(const dit_gated_ffn_args& a, bool backward) {
   operand(p.wg, a.w_gate, a.w_gate_stride, a.hidden, !backward || a.dx);
   operand(p.wu, a.w_up, a.w_up_stride, a.hidden, !backward || a.dx);
   const int bk = 128 / esz;
+  if (p.few) return p;
   if (!backward) {
     p.fwd = choose(a.rows, a.hidden, 2, (a.width + bk - 1) / bk, 1);
     if (p.fwd.splits > 1) p.partial = p.take(planes(p.fwd, a.rows, a.hidden, 2));
@@ -759,7 +919,7 @@ Plan make_plan(const dit_gated_ffn_args& a, bool backward) {
 // ---------------------------------------------------------------- launches
 // CTAs, or pairs of them, that run at once on the current device: a persistent
 // launch asks for no more (one that had to wait would run its whole share last).
-template <int MODE, bool F8, bool PAIR>
+template <int MODE, bool F8, bool PAIR, int ACT>
 cudaError_t resident(int* slots) {
   static int known[kMaxDevices] = {};  // 0: not asked yet; every thread finds the same number
   int dev = 0;
@@ -774,7 +934,7 @@ cudaError_t resident(int* slots) {
     n = sms;
     if (PAIR) {
       using C = Cfg<F8, PAIR>;
-      const auto kernel = product_kernel<MODE, F8, PAIR>;
+      const auto kernel = product_kernel<MODE, F8, PAIR, ACT>;
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10);
       if (e != cudaSuccess) return e;
       cudaLaunchConfig_t c{};
@@ -798,7 +958,7 @@ cudaError_t resident(int* slots) {
   return cudaSuccess;
 }
 
-template <int MODE, bool F8, bool PAIR>
+template <int MODE, bool F8, bool PAIR, int ACT>
 cudaError_t launch_product(Product& P, int problems, cudaStream_t s) {
   using C = Cfg<F8, PAIR>;
   constexpr int COLS = MODE == FWD ? C::BN / 2 : C::BN;
@@ -816,15 +976,18 @@ cudaError_t launch_product(Product& P, int problems, cudaStream_t s) {
   if (P.M * 1 > (int64_t)P.N * (MODE == FWD ? 2 : 1) || gn > P.n_tiles) gn = P.n_tiles;
   P.group_n = (int)gn;
   int slots = 0;
-  const cudaError_t e = resident<MODE, F8, PAIR>(&slots);
+  const cudaError_t e = resident<MODE, F8, PAIR, ACT>(&slots);
   if (e != cudaSuccess) return e;
   const int n = P.items < slots ? P.items : slots;
-  return launch_kernel(product_kernel<MODE, F8, PAIR>, dim3(PAIR ? 2 * n : n), dim3(kThreads), C::SMEM, s, PAIR ? 2 : 1, true, P);
+  return launch_kernel(product_kernel<MODE, F8, PAIR, ACT>, dim3(PAIR ? 2 * n : n), dim3(kThreads), C::SMEM, s, PAIR ? 2 : 1, true, P);
 }
 template <int MODE, bool F8>
 cudaError_t run_product(Product& P, const Split& sp, int problems, cudaStream_t s) {
   P.splits = sp.splits;
-  return sp.pair ? launch_product<MODE, F8, true>(P, problems, s) : launch_product<MODE, F8, false>(P, problems, s);
+  if constexpr (MODE == FWD)
+    if (P.act == DIT_ACT_GELU)
+      return sp.pair ? launch_product<MODE, F8, true, DIT_ACT_GELU>(P, problems, s) : launch_product<MODE, F8, false, DIT_ACT_GELU>(P, problems, s);
+  return sp.pair ? launch_product<MODE, F8, true, DIT_ACT_SILU>(P, problems, s) : launch_product<MODE, F8, false, DIT_ACT_SILU>(P, problems, s);
 }
 
 // rows x width elements: boxes of 128 bytes (box_x elements) by box_rows rows
@@ -877,8 +1040,40 @@ cudaError_t pack_operands(const dit_gated_ffn_args& a, Plan& p, char* ws, cudaSt
                   : launch_kernel(pack_kernel<uint16_t>, grid, dim3(256), 0, s, 1, false, k);
 }
 
+template <bool F8, bool F16, int NT>
+cudaError_t launch_few(const Few& k, bool whole, int act, cudaStream_t s) {
+  const auto kernel = act == DIT_ACT_SILU
+                          ? whole ? few_rows_kernel<F8, F16, NT, true, DIT_ACT_SILU> : few_rows_kernel<F8, F16, NT, false, DIT_ACT_SILU>
+                          : whole ? few_rows_kernel<F8, F16, NT, true, DIT_ACT_GELU> : few_rows_kernel<F8, F16, NT, false, DIT_ACT_GELU>;
+  return launch_kernel(kernel, dim3((k.F + 15) / 16), dim3(32 * kFewWarps), 0, s, 1, true, k);
+}
+template <bool F8, bool F16>
+cudaError_t launch_few(const Few& k, bool whole, int act, cudaStream_t s) {
+  if (k.M <= 8) return launch_few<F8, F16, 1>(k, whole, act, s);
+  if (k.M <= 16) return launch_few<F8, F16, 2>(k, whole, act, s);
+  return launch_few<F8, F16, 4>(k, whole, act, s);
+}
+cudaError_t few_rows(const dit_gated_ffn_args& a, cudaStream_t s) {
+  const bool f8 = a.operand_dtype == DIT_DTYPE_E4M3, f16 = a.dtype == DIT_DTYPE_F16;
+  const int esz = f8 ? 1 : 2;
+  Few k{};
+  k.x = static_cast<const uint8_t*>(a.x), k.w[0] = static_cast<const uint8_t*>(a.w_gate), k.w[1] = static_cast<const uint8_t*>(a.w_up);
+  k.ldx = a.rows > 1 ? a.x_stride * esz : 0;
+  k.ldw[0] = a.hidden > 1 ? a.w_gate_stride * esz : 0, k.ldw[1] = a.hidden > 1 ? a.w_up_stride * esz : 0;
+  k.x_scale = a.x_scale, k.scale[0] = a.gate_scale, k.scale[1] = a.up_scale;
+  k.bias[0] = a.bias_gate, k.bias[1] = a.bias_up;
+  k.out[0] = static_cast<uint16_t*>(a.out), k.out[1] = static_cast<uint16_t*>(a.gate), k.out[2] = static_cast<uint16_t*>(a.up);
+  k.ldo[0] = a.out_stride, k.ldo[1] = a.gate_stride, k.ldo[2] = a.up_stride;
+  k.M = (int)a.rows, k.D = a.width, k.F = a.hidden;
+  const uint64_t all = (uintptr_t)k.x | (uintptr_t)k.w[0] | (uintptr_t)k.w[1] | (uint64_t)(k.ldx | k.ldw[0] | k.ldw[1]) | (uint64_t)(a.width * esz);
+  const bool whole = (all & 15) == 0;
+  if (f8) return f16 ? launch_few<true, true>(k, whole, a.act, s) : launch_few<true, false>(k, whole, a.act, s);
+  return f16 ? launch_few<false, true>(k, whole, a.act, s) : launch_few<false, false>(k, whole, a.act, s);
+}
+
 cudaError_t forward(const dit_gated_ffn_args& a, char* ws, cudaStream_t s) {
   Plan p = make_plan(a, false);
+  if (p.few) return few_rows(a, s);
   cudaError_t e = pack_operands(a, p, ws, s);
   if (e != cudaSuccess) return e;
   const bool f8 = a.operand_dtype == DIT_DTYPE_E4M3;
@@ -902,6 +1097,17 @@ cudaError_t forward(const dit_gated_ffn_args& a, char* ws, cudaStream_t s) {
   output(P, 2, a.up, a.up_stride);
   e = f8 ? run_product<FWD, true>(P, p.fwd, 1, s) : run_product<FWD, false>(P, p.fwd, 1, s);
   return e != cudaSuccess || P.splits == 1 ? e : join<true>(P, 1, s);
+}
+
+template <typename T>
+cudaError_t run_slopes(const Slopes& g, int act, cudaStream_t s) {
+  const uintptr_t all = (uintptr_t)g.gate | (uintptr_t)g.up | (uintptr_t)g.dout;
+  const int64_t steps = g.M > 1 ? g.ld_gate | g.ld_up | g.ld_dout : 0;
+  const bool aligned = !(all % 16) && !(steps % 8) && g.F % 8 == 0;
+  const dim3 grid((unsigned)((g.M + g.rows_per_block - 1) / g.rows_per_block), (unsigned)((g.F + 255) / 256));
+  const auto kernel = act == DIT_ACT_SILU ? aligned ? slopes_kernel<T, DIT_ACT_SILU, true> : slopes_kernel<T, DIT_ACT_SILU, false>
+                                          : aligned ? slopes_kernel<T, DIT_ACT_GELU, true> : slopes_kernel<T, DIT_ACT_GELU, false>;
+  return launch_kernel(kernel, grid, dim3(32, 8), 0, s, 1, true, g);
 }
 
 cudaError_t zero_rows(void* p, int64_t rows, int64_t width, int64_t stride, cudaStream_t s) {
@@ -928,12 +1134,12 @@ cudaError_t backward(const dit_gated_ffn_args& a, char* ws, cudaStream_t s) {
   g.pitch = 2 * p.slope_pitch;
   g.dgate = reinterpret_cast<uint16_t*>(ws + p.slopes), g.dup = g.dgate + p.slope_pitch;
   g.partial = p.sums >= 0 ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
-  g.M = a.rows, g.F = a.hidden, g.rows_per_block = (int)p.rows_per_block, g.f16 = f16, g.act = a.act;
-  e = launch_kernel(slopes_kernel, dim3((unsigned)p.sum_blocks, (unsigned)((a.hidden + 255) / 256)), dim3(32, 8), 0, s, 1, false, g);
+  g.M = a.rows, g.F = a.hidden, g.rows_per_block = (int)p.rows_per_block;
+  e = f16 ? run_slopes<__half>(g, a.act, s) : run_slopes<__nv_bfloat16>(g, a.act, s);
   if (e != cudaSuccess) return e;
   if (g.partial) {
     ColumnSums c{g.partial, p.sum_blocks, 2 * p.slope_pitch, a.hidden, p.slope_pitch, {a.dbias_gate, a.dbias_up}};
-    e = launch_kernel(column_sums_kernel<0>, dim3((a.hidden + 31) / 32, 2), dim3(32, 32), 0, s, 1, false, c);
+    e = column_sums(c, s);
     if (e != cudaSuccess) return e;
   }
   Product P{};

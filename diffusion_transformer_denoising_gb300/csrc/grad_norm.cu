@@ -1,13 +1,13 @@
 // The norm of many tensors together, and their clipping to it.
 //
 // Mathematics.  norm = sqrt(sum g^2) over every value of every tensor; where it is
-// above max_norm, out = g (max_norm / norm).  The squares of a thread's vectors are
-// summed in fp32 while they are in range, in fp64 where a vector's are not (values
-// above 1e15 or all below 1e-15), and the threads' sums are joined in fp64 in a fixed order.
+// above max_norm, out = g (max_norm / norm).  The squares of a thread's vectors of a
+// piece are summed in fp32 while they are in range, in fp64 where a vector's are not
+// (values above 1e15 or all below 1e-15), and joined in fp64 in a fixed order.
 //
-// What bounds it: HBM.  Two passes, since the factor needs every value: the sums
-// of fixed pieces of the tensors, then the factor (each block adds up the pieces'
-// sums for itself) and the products.  The second pass walks the pieces backwards,
+// What bounds it: HBM.  Two passes, since the factor needs every value: the sums of
+// the pieces that a block has (always the same ones), then the factor (each block
+// adds up the blocks' sums for itself) and the products.  The second pass walks the pieces backwards,
 // so it begins with what the first has left in L2.
 #include <math.h>
 
@@ -22,6 +22,7 @@ namespace {
 constexpr int kPiece = 16384;    // values a block takes at a time
 constexpr int kTensors = 640;    // of a launch: its parameters hold their descriptions (32764 bytes at most)
 constexpr int kGradThreads = 256;
+constexpr int kGradBlocks = 152 * 3;  // of a pass over the squares: the sums' order does not depend on the device
 
 struct Tensors {
   const void* grad[kTensors];
@@ -31,8 +32,9 @@ struct Tensors {
   int16_t dtype[kTensors];
   int n;
   uint32_t first;                // pieces of the launches before
-  uint32_t pieces;               // of all launches
-  double* sums;                  // [pieces]
+  uint32_t parts;                // sums of all launches
+  uint32_t first_part;
+  double* sums;                  // [parts]
   float* norm;
   float max_norm;
   int write_norm;
@@ -119,17 +121,17 @@ DIT_DEV double piece_squares(const T* p, int n) {
 __global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid_constant__ Tensors t) {
   __shared__ double shared[kGradThreads / 32];
   const uint32_t last = t.end[t.n - 1];
+  double v = 0.;
   for (uint32_t piece = t.first + blockIdx.x; piece < last; piece += gridDim.x) {
     const int i = tensor_of(t, piece);
     const int64_t begin = (int64_t)(piece - (i ? t.end[i - 1] : t.first)) * kPiece;
     const int n = (int)min((int64_t)kPiece, t.numel[i] - begin);
-    double v;
-    if (t.dtype[i] == DIT_DTYPE_F32) v = piece_squares(static_cast<const float*>(t.grad[i]) + begin, n);
-    else if (t.dtype[i] == DIT_DTYPE_BF16) v = piece_squares(static_cast<const __nv_bfloat16*>(t.grad[i]) + begin, n);
-    else v = piece_squares(static_cast<const __half*>(t.grad[i]) + begin, n);
-    v = block_sum(v, shared);
-    if (threadIdx.x == 0) t.sums[piece] = v;
+    if (t.dtype[i] == DIT_DTYPE_F32) v += piece_squares(static_cast<const float*>(t.grad[i]) + begin, n);
+    else if (t.dtype[i] == DIT_DTYPE_BF16) v += piece_squares(static_cast<const __nv_bfloat16*>(t.grad[i]) + begin, n);
+    else v += piece_squares(static_cast<const __half*>(t.grad[i]) + begin, n);
   }
+  v = block_sum(v, shared);
+  if (threadIdx.x == 0) t.sums[t.first_part + blockIdx.x] = v;
 }
 
 template <typename T>
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
   __shared__ double shared[kGradThreads / 32];
   wait_previous();
   double v = 0.;
-  for (uint32_t i = threadIdx.x; i < t.pieces; i += kGradThreads) v += t.sums[i];
+  for (uint32_t i = threadIdx.x; i < t.parts; i += kGradThreads) v += t.sums[i];
   v = block_sum(v, shared);
   const float norm = (float)sqrt(v);
   if (t.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *t.norm = norm;
@@ -181,51 +183,66 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
 
 int64_t pieces_of(const dit_grad_tensor& t) { return (t.numel + kPiece - 1) / kPiece; }
 
+// One launch's tensors, from tensor i on.
+struct Batch {
+  int64_t next, pieces;
+  int n;
+};
+Batch batch_of(const dit_grad_tensor* t, int64_t n, int64_t i) {
+  Batch b{i, 0, 0};
+  for (; b.next < n && b.n < kTensors; ++b.next)
+    if (t[b.next].numel > 0) b.pieces += pieces_of(t[b.next]), ++b.n;
+  return b;
+}
+int64_t parts_of(const Batch& b) { return b.pieces < kGradBlocks ? b.pieces : kGradBlocks; }
+int64_t all_parts(const dit_grad_tensor* t, int64_t n) {
+  int64_t parts = 0;
+  for (int64_t i = 0; i < n;) {
+    const Batch b = batch_of(t, n, i);
+    parts += parts_of(b);
+    i = b.next;
+  }
+  return parts;
+}
+
 }  // namespace
 
 int64_t grad_norm_workspace(const dit_grad_tensor* t, int64_t n) {
-  int64_t pieces = 0;
-  for (int64_t i = 0; i < n; ++i) pieces += pieces_of(t[i]);
-  return (pieces > 0 ? pieces : 1) * (int64_t)sizeof(double);
+  const int64_t parts = all_parts(t, n);
+  return (parts > 0 ? parts : 1) * (int64_t)sizeof(double);
 }
 
 cudaError_t grad_norm_run(const dit_grad_tensor* t, int64_t n, float max_norm, float* norm, void* workspace, cudaStream_t s) {
-  const int64_t pieces = grad_norm_workspace(t, n) / (int64_t)sizeof(double);
-  bool products = false, any = false;
-  for (int64_t i = 0; i < n; ++i) {
-    any |= t[i].numel > 0;
-    products |= t[i].out != nullptr;
-  }
+  bool products = false;
+  for (int64_t i = 0; i < n; ++i) products |= t[i].numel > 0 && t[i].out;
   // squares of every launch first, then products of every launch
   for (int pass = 0; pass < 2; ++pass) {
-    uint32_t before = 0;
+    Tensors p;
+    p.first = p.first_part = 0;
+    p.parts = (uint32_t)all_parts(t, n);
+    p.sums = static_cast<double*>(workspace), p.norm = norm, p.max_norm = max_norm;
+    p.write_norm = 1;
     int64_t i = 0;
-    bool first = true;
     do {
-      Tensors p;
-      p.n = 0;
-      p.first = before;
-      for (; i < n && p.n < kTensors; ++i) {
+      const Batch b = batch_of(t, n, i);
+      uint32_t end = p.first;
+      for (p.n = 0; i < b.next; ++i) {
         if (t[i].numel == 0) continue;
-        before += (uint32_t)pieces_of(t[i]);
         p.grad[p.n] = t[i].grad, p.out[p.n] = t[i].out, p.numel[p.n] = t[i].numel;
-        p.dtype[p.n] = (int16_t)t[i].dtype, p.end[p.n] = before;
+        p.dtype[p.n] = (int16_t)t[i].dtype, p.end[p.n] = end += (uint32_t)pieces_of(t[i]);
         ++p.n;
       }
-      p.pieces = any ? (uint32_t)pieces : 0;
-      p.sums = static_cast<double*>(workspace), p.norm = norm, p.max_norm = max_norm;
-      p.write_norm = first;
-      const int64_t own = before - p.first;
       cudaError_t e = cudaSuccess;
-      if (pass == 0 && p.n) {
-        e = launch_kernel(grad_squares_kernel, dim3((unsigned)(own < 152 * 8 ? own : 152 * 8)), dim3(kGradThreads), 0, s, 1, false, p);
-      } else if (pass == 1 && (first || products)) {
-        const int64_t blocks = products ? (own < 152 * 8 ? own : 152 * 8) : 1;
+      if (pass == 0) {
+        if (b.n) e = launch_kernel(grad_squares_kernel, dim3((unsigned)parts_of(b)), dim3(kGradThreads), 0, s, 1, false, p);
+      } else {
+        const int64_t blocks = !products ? 1 : b.pieces < 152 * 8 ? b.pieces : 152 * 8;
         e = launch_kernel(grad_clip_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kGradThreads), 0, s, 1, true, p);
       }
       if (e != cudaSuccess) return e;
-      first = false;
-    } while (i < n);
+      p.first = end, p.first_part += (uint32_t)parts_of(b);
+      p.write_norm = 0;
+    } while (i < n && (pass == 0 || products));
   }
   return cudaSuccess;
 }

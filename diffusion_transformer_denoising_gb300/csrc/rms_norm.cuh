@@ -1,0 +1,686 @@
+// RMS norm over channels with the residual's addition in front of it, into the
+// activations' type or into e4m3 with a scale for each row, and its gradient.
+//
+// Mathematics.  v = x + residual rounded to the type, r = (mean v^2 + eps)^-1/2,
+// y = v r w.  e4m3: scale = max |y| / 448, y / scale rounded to nearest even.
+// Gradient: g = dy w, dx = dtotal + r (g - v r^2 mean(g v)), dw = sum dy v r: the two
+// row sums (v^2 and g v) are taken together.
+//
+// What bounds it: HBM.  Every row is read once and written once.  Up to 2048 channels
+// of 16 bits (1024 of 32) a warp takes a row, out of a ring of its own in shared
+// memory that asynchronous copies fill: while it works on a row the next one is on
+// its way, whatever the registers hold.  Wider rows are held in the registers of a block.
+#pragma once
+#include <math.h>
+
+#include "column_sums.cuh"
+#include "launch.cuh"
+#include "operators.h"
+#include "vec.cuh"
+
+namespace dit {
+
+namespace norm {
+
+enum NormMode { SAME, E4M3, GRAD };
+enum { AL_X = 1, AL_RES = 2, AL_TOTAL = 4, AL_DY = 8, AL_OUT = 16, AL_W = 32 };
+
+struct Norm {
+  const void *x, *res, *dy;
+  void *total, *out;
+  int64_t sx[2], sres[2], stotal[2], sdy[2], sout[2];
+  float* scale;
+  const float* w;
+  float* partial;  // GRAD: [block][channels] sums of the block's rows, or NULL
+  uint32_t rows, tokens;
+  int C;
+  float eps;
+  int aligned;     // AL_*: 16-byte rows (AL_OUT of e4m3: 8-byte rows for chunks of 8, 4 for 4)
+  int words;       // AL_*: rows of 4-byte words at least
+};
+
+// max(a, |b|, |c|), NaN if one of them is
+DIT_DEV float max_abs(float a, float2 b) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b.x), "f"(b.y));
+  return d;
+}
+DIT_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// What an e4m3 row is held in: top is max |v w|, y = v r w.
+struct RowScale {
+  float scale, factor;  // out = v w factor
+  bool finite;
+};
+DIT_DEV RowScale row_scale(float top, float r) {
+  RowScale q;
+  top *= r;
+  q.finite = top <= 3.402823466e38f;
+  // below 448 x 2^-126 the scale stays a normal number, so that its reciprocal is finite
+  q.scale = !q.finite ? __int_as_float(0x7fffffff) : top > 0.f ? fmaxf(top / kE4M3Max, 1.17549435e-38f) : 1.f;
+  q.factor = q.finite ? r / q.scale : 0.f;
+  return q;
+}
+
+// A 16-byte chunk's values as pairs, for the packed fp32 instructions (the first
+// kernels' scalar ones took the gradient of the video case 104 us).
+template <typename T>
+struct Pairs {
+  static constexpr int E = 16 / sizeof(T), N = E / 2;
+  float2 v[N];
+  DIT_DEV float2& operator[](int j) { return v[j]; }
+  DIT_DEV const float2& operator[](int j) const { return v[j]; }
+};
+template <typename T>
+DIT_DEV Pairs<T> pairs(const uint4& r) {
+  Pairs<T> p;
+  const uint32_t* w = &r.x;
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) {
+    if constexpr (sizeof(T) == 4) p[j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    else p[j] = unpack2<T>(w[j]);
+  }
+  return p;
+}
+template <typename T>
+DIT_DEV uint4 packed(const Pairs<T>& p) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x), __float_as_uint(p[1].y));
+  else
+    return make_uint4(pack2<T>(p[0].x, p[0].y), pack2<T>(p[1].x, p[1].y), pack2<T>(p[2].x, p[2].y), pack2<T>(p[3].x, p[3].y));
+}
+
+// The chunk at p, of which n elements are there (zeros behind them).
+template <typename T, bool WHOLE>
+DIT_DEV uint4 load_chunk(const T* p, int n, bool aligned) {
+  constexpr int E = 16 / sizeof(T);
+  if (WHOLE || (aligned && n >= E)) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4] = {0, 0, 0, 0};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j < n) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j < n) w[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T, bool WHOLE>
+DIT_DEV void store_chunk(T* p, int n, bool aligned, const uint4& r) {
+  constexpr int E = 16 / sizeof(T);
+  if (WHOLE || (aligned && n >= E)) {
+    *reinterpret_cast<uint4*>(p) = r;
+    return;
+  }
+  const uint32_t* w = &r.x;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    if (j >= n) continue;
+    if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+    else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+  }
+}
+template <typename T, bool WHOLE>
+DIT_DEV void store_e4m3(uint8_t* p, int n, bool aligned, const Pairs<T>& v) {
+  constexpr int E = 16 / sizeof(T);
+  uint32_t w[E / 4];
+#pragma unroll
+  for (int j = 0; j < E / 4; ++j) w[j] = pack_e4m3x4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+  if (WHOLE || (aligned && n >= E)) {
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if (j < n) p[j] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
+}
+// v *= the weights of channels c on (zeros behind the last)
+template <typename T, bool WHOLE>
+DIT_DEV void times_weight(Pairs<T>& v, const float* w, int c, int n, bool aligned) {
+  constexpr int E = 16 / sizeof(T);
+  if (!WHOLE && !w) return;
+  if (WHOLE || (aligned && n >= E)) {
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(w + c + j));
+      v[j / 2] = fmul2(v[j / 2], make_float2(t.x, t.y));
+      v[j / 2 + 1] = fmul2(v[j / 2 + 1], make_float2(t.z, t.w));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; j += 2)
+      v[j / 2] = fmul2(v[j / 2], make_float2(j < n ? __ldg(w + c + j) : 0.f, j + 1 < n ? __ldg(w + c + j + 1) : 0.f));
+  }
+}
+template <typename T>
+DIT_DEV void scale_by(Pairs<T>& v, float k) {
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) v[j] = fmul2(v[j], make_float2(k, k));
+}
+// sum += a b, pair by pair
+template <typename T>
+DIT_DEV void add_products(float2& sum, const Pairs<T>& a, const Pairs<T>& b) {
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) sum = ffma2(a[j], b[j], sum);
+}
+template <typename T>
+DIT_DEV void add_to(Pairs<T>& a, const Pairs<T>& b) {
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) a[j] = fadd2(a[j], b[j]);
+}
+// g = dy, gw = dy w and v of a chunk: dw += g v r, gw becomes r (gw - k v)
+template <typename T>
+DIT_DEV void norm_gradient(const Pairs<T>& g, Pairs<T>& gw, const Pairs<T>& v, float r, float k, Pairs<T>& dw) {
+  const float2 r2 = make_float2(r, r), k2 = make_float2(-k, -k);
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) {
+    dw[j] = ffma2(g[j], fmul2(v[j], r2), dw[j]);
+    gw[j] = fmul2(r2, ffma2(k2, v[j], gw[j]));
+  }
+}
+
+DIT_DEV float2 warp_sum2(float2 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  return v;
+}
+DIT_DEV float warp_sum1(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+DIT_DEV float warp_max1(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Asynchronous copies of `bytes` <= N bytes, zeros behind them.
+DIT_DEV void copy_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DIT_DEV void copy_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DIT_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DIT_DEV void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int kRingRows = 4, kRingStages = 2;
+// RW warps hold a row, NV chunks of 16 bytes a thread.
+template <int RW, int NV, int MODE, bool RES>
+struct Ring {
+  static constexpr int INPUTS = (MODE == GRAD ? 2 : 1) + (RES ? 1 : 0);
+  static constexpr int ROW = RW * NV * 512;  // bytes
+  static constexpr int STAGE = INPUTS * ROW;
+  static constexpr int SMEM = kRingRows * kRingStages * STAGE;
+};
+// Blocks of a ring kernel that an SM holds (registers allow them too: launch bounds).
+constexpr int ring_blocks(int rw, int nv, int inputs) {
+  const int n = (227 << 10) / (kRingRows * kRingStages * inputs * rw * nv * 512 + 1024), most = 8 / rw > 4 ? 4 : 8 / rw;
+  return n > most ? most : n;
+}
+
+// The warps of a row wait for each other.
+template <int RW>
+DIT_DEV void row_sync() {
+  if constexpr (RW == 1) __syncwarp();
+  else named_bar_sync(1 + threadIdx.x / (32 * RW), 32 * RW);
+}
+
+// The channels of a row into a slot of shared memory, zeros up to its last chunk's
+// end.  Rows of 16-byte vectors: each lane fetches what it reads; else any lane any word.
+template <typename T, int RW, int NV>
+DIT_DEV void fetch_row(uint8_t* slot, const T* row, int C, bool aligned, bool words) {
+  const int lane = threadIdx.x & (32 * RW - 1), bytes = C * (int)sizeof(T);
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(row);
+  const uint32_t dst = smem_u32(slot);
+  if (aligned) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = (lane + 32 * RW * i) * 16;
+      if (at < bytes) copy_async16(dst + at, src + at, min(16, bytes - at));
+    }
+    return;
+  }
+  const int end = (bytes + 15) & ~15;
+  if (words) {
+    for (int at = lane * 4; at < end; at += 128 * RW) {
+      const int n = max(0, min(4, bytes - at));
+      copy_async4(dst + at, n ? src + at : src, n);
+    }
+    return;
+  }
+  for (int at = lane * 2; at < end; at += 64 * RW)
+    *reinterpret_cast<uint16_t*>(slot + at) = at < bytes ? *reinterpret_cast<const uint16_t*>(src + at) : (uint16_t)0;
+}
+// A row that every lane has written to a slot, out to global memory in words or elements.
+template <typename T, int RW>
+DIT_DEV void put_row(T* row, const uint8_t* slot, int C, bool words) {
+  const int lane = threadIdx.x & (32 * RW - 1), bytes = C * (int)sizeof(T);
+  uint8_t* dst = reinterpret_cast<uint8_t*>(row);
+  row_sync<RW>();
+  if (words) {
+    for (int at = lane * 4; at + 4 <= bytes; at += 128 * RW) *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(slot + at);
+    if (lane == 0 && (bytes & 2)) *reinterpret_cast<uint16_t*>(dst + bytes - 2) = *reinterpret_cast<const uint16_t*>(slot + bytes - 2);
+  } else {
+    for (int at = lane * 2; at < bytes; at += 64 * RW) *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(slot + at);
+  }
+  row_sync<RW>();
+}
+
+// RW warps a row, NV chunks of 16 bytes a thread: chunk lane + 32 RW i.  WHOLE: a weight,
+// every tensor in rows of whole 16-byte vectors (no branch is left in a row then, and
+// its loads are issued together: the video gradient 90 us without it).
+template <typename T, int RW, int NV, int MODE, bool RES, bool WHOLE>
+__global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<RW, NV, MODE, RES>::INPUTS)) norm_ring_kernel(const Norm a) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr int ALL = WHOLE ? ~0 : 0;
+  const int aligned = a.aligned | ALL;
+  constexpr int TPR = 32 * RW;
+  using R = Ring<RW, NV, MODE, RES>;
+  extern __shared__ uint4 ring_smem[];  // the ring; of several warps a row, their sums behind it
+  const int lane = threadIdx.x & (TPR - 1), mine_row = threadIdx.x / TPR;
+  uint8_t* const mine = reinterpret_cast<uint8_t*>(ring_smem) + mine_row * kRingStages * R::STAGE;
+  const uint32_t step = gridDim.x * kRingRows;
+  float2* const parts = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ring_smem) + R::SMEM) + mine_row * 2 * RW;
+  int turn = 0;
+  auto row_sum = [&](float2 v) {
+    v = MODE == GRAD ? warp_sum2(v) : make_float2(warp_sum1(v.x), 0.f);
+    if constexpr (RW > 1) {
+      if ((lane & 31) == 0) parts[turn * RW + (lane >> 5)] = v;
+      row_sync<RW>();
+      v = parts[turn * RW];
+#pragma unroll
+      for (int i = 1; i < RW; ++i) v = fadd2(v, parts[turn * RW + i]);
+      turn ^= 1;
+    }
+    return v;
+  };
+  auto row_max = [&](float v) {
+    v = warp_max1(v);
+    if constexpr (RW > 1) {
+      if ((lane & 31) == 0) parts[turn * RW + (lane >> 5)].x = v;
+      row_sync<RW>();
+      v = parts[turn * RW].x;
+#pragma unroll
+      for (int i = 1; i < RW; ++i) v = max_nan(v, parts[turn * RW + i].x);
+      turn ^= 1;
+    }
+    return v;
+  };
+  const int C = a.C;
+  const float inv_c = 1.f / (float)C;
+  auto offset = [&](uint32_t row, const int64_t (&s)[2]) {
+    const uint32_t b = row / a.tokens;
+    return (int64_t)b * s[0] + (int64_t)(row - b * a.tokens) * s[1];
+  };
+  auto fetch = [&](int stage, uint32_t row) {
+    uint8_t* slot = mine + stage * R::STAGE;
+    fetch_row<T, RW, NV>(slot, static_cast<const T*>(a.x) + offset(row, a.sx), C, aligned & AL_X, a.words & AL_X);
+    if constexpr (MODE == GRAD)
+      fetch_row<T, RW, NV>(slot + R::ROW, static_cast<const T*>(a.dy) + offset(row, a.sdy), C, aligned & AL_DY, a.words & AL_DY);
+    if constexpr (RES)
+      fetch_row<T, RW, NV>(slot + (R::INPUTS - 1) * R::ROW, static_cast<const T*>(a.res) + offset(row, a.sres), C,
+                       aligned & AL_RES, a.words & AL_RES);
+  };
+  Pairs<T> dw[MODE == GRAD ? NV : 1] = {};
+  uint32_t row = blockIdx.x * kRingRows + mine_row;
+  if (row < a.rows) fetch(0, row);
+  copy_commit();
+  int stage = 0;
+  for (; row < a.rows; row += step, stage ^= 1) {
+    const bool more = step < a.rows - row;
+    if (more) fetch(stage ^ 1, row + step);
+    copy_commit();
+    copy_wait<1>();
+    if constexpr (!WHOLE) row_sync<RW>();  // WHOLE: a thread reads what it has fetched
+    uint8_t* const slot = mine + stage * R::STAGE;
+    uint8_t* const res_slot = slot + (R::INPUTS - 1) * R::ROW;
+    auto chunk = [&](uint8_t* s, int i) -> uint4& { return *reinterpret_cast<uint4*>(s + (lane + TPR * i) * 16); };
+    if constexpr (MODE == GRAD) {
+      float2 square = make_float2(0.f, 0.f), dot = square;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
+        if (n <= 0) continue;
+        const Pairs<T> v = pairs<T>(chunk(slot, i));
+        Pairs<T> g = pairs<T>(chunk(slot + R::ROW, i));
+        times_weight<T, WHOLE>(g, a.w, c, n, aligned & AL_W);
+        add_products<T>(square, v, v);
+        add_products<T>(dot, g, v);
+      }
+      const float2 sums = row_sum(make_float2(square.x + square.y, dot.x + dot.y));
+      const float r = rsqrtf(fmaf(sums.x, inv_c, a.eps)), k = r * r * (sums.y * inv_c);
+      T* out = static_cast<T*>(a.out) + offset(row, a.sout);
+      const bool direct = aligned & AL_OUT;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
+        if (n <= 0) continue;
+        const Pairs<T> v = pairs<T>(chunk(slot, i)), g = pairs<T>(chunk(slot + R::ROW, i));
+        Pairs<T> d = g;
+        times_weight<T, WHOLE>(d, a.w, c, n, aligned & AL_W);
+        norm_gradient<T>(g, d, v, r, k, dw[i]);
+        if constexpr (RES) add_to<T>(d, pairs<T>(chunk(res_slot, i)));
+        // a lane's chunk of the slot is read by it alone
+        if (direct) store_chunk<T, WHOLE>(out + c, n, true, packed<T>(d));
+        else chunk(res_slot, i) = packed<T>(d);
+      }
+      if (!direct) put_row<T, RW>(out, res_slot, C, a.words & AL_OUT);
+    } else {
+      Pairs<T> v[NV];
+      float2 square = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
+        v[i] = Pairs<T>{};
+        if (n <= 0) continue;
+        v[i] = pairs<T>(chunk(slot, i));
+        if constexpr (RES) {
+          add_to<T>(v[i], pairs<T>(chunk(res_slot, i)));
+          const uint4 sum = packed<T>(v[i]);
+          v[i] = pairs<T>(sum);  // the norm is of the sum as it is kept
+          if (a.total) {
+            if (aligned & AL_TOTAL) store_chunk<T, WHOLE>(static_cast<T*>(a.total) + offset(row, a.stotal) + c, n, true, sum);
+            else chunk(slot, i) = sum;
+          }
+        }
+        add_products<T>(square, v[i], v[i]);
+      }
+      if constexpr (RES)
+        if (a.total && !(aligned & AL_TOTAL)) put_row<T, RW>(static_cast<T*>(a.total) + offset(row, a.stotal), slot, C, a.words & AL_TOTAL);
+      const float r = rsqrtf(fmaf(row_sum(make_float2(square.x + square.y, 0.f)).x, inv_c, a.eps));
+      float factor = r, top = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
+        if (n <= 0) continue;
+        times_weight<T, WHOLE>(v[i], a.w, c, n, aligned & AL_W);
+        if constexpr (MODE == E4M3)
+#pragma unroll
+          for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[i][j]);
+      }
+      if constexpr (MODE == E4M3) {
+        const RowScale q = row_scale(row_max(top), r);
+        factor = q.factor, finite = q.finite;
+        if (lane == 0) a.scale[row] = q.scale;
+      }
+      T* out = static_cast<T*>(a.out) + offset(row, a.sout);
+      uint8_t* out8 = static_cast<uint8_t*>(a.out) + offset(row, a.sout);
+      const bool direct = aligned & AL_OUT;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
+        if (n <= 0) continue;
+        scale_by<T>(v[i], factor);
+        if constexpr (MODE == E4M3) store_e4m3<T, WHOLE>(out8 + c, n, direct, finite ? v[i] : Pairs<T>{});
+        else if (direct) store_chunk<T, WHOLE>(out + c, n, true, packed<T>(v[i]));
+        else chunk(res_slot, i) = packed<T>(v[i]);
+      }
+      if (MODE == SAME && !direct) put_row<T, RW>(out, res_slot, C, a.words & AL_OUT);
+    }
+    if constexpr (!WHOLE) row_sync<RW>();  // the slot may be filled again
+    if (!more) break;  // row + step may pass 32 bits
+  }
+  if constexpr (MODE == GRAD) {
+    if (!a.partial) return;
+    // the sums of the block's rows, through the ring
+    copy_wait<0>();
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(ring_smem);  // [row][channel]
+    constexpr int WIDTH = NV * TPR * E;
+    static_assert(kRingRows * WIDTH * 4 <= R::SMEM, "room for the join");
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < E / 2; j += 2)
+        *reinterpret_cast<float4*>(join + mine_row * WIDTH + (lane + TPR * i) * E + 2 * j) = make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
+    __syncthreads();
+    for (int c = threadIdx.x; c < C; c += TPR * kRingRows) {
+      float s = join[c];
+#pragma unroll
+      for (int g = 1; g < kRingRows; ++g) s += join[g * WIDTH + c];
+      a.partial[(int64_t)blockIdx.x * C + c] = s;
+    }
+  }
+}
+
+constexpr int kRowWarps = 8;
+
+// W warps hold a row in registers, NV chunks of 16 bytes a thread: chunk tid + 32 W i.
+// One warp a row: kRowWarps rows a block.
+template <typename T, int W, int NV, int MODE, bool WHOLE>
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W) norm_kernel(const Norm a) {
+  const int aligned = a.aligned | (WHOLE ? ~0 : 0);
+  constexpr int E = 16 / sizeof(T), TPR = 32 * W, ROWS = W == 1 ? kRowWarps : 1;
+  __shared__ float2 parts[2][W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = W == 1 ? lane : threadIdx.x;
+  int turn = 0;
+  // over the threads of a row
+  auto row_sum = [&](float2 v) {
+    v = MODE == GRAD ? warp_sum2(v) : make_float2(warp_sum1(v.x), 0.f);
+    if constexpr (W > 1) {
+      if (lane == 0) parts[turn][warp] = v;
+      __syncthreads();
+      v = parts[turn][0];
+#pragma unroll
+      for (int i = 1; i < W; ++i) v = fadd2(v, parts[turn][i]);
+      turn ^= 1;
+    }
+    return v;
+  };
+  auto row_max = [&](float v) {
+    v = warp_max1(v);
+    if constexpr (W > 1) {
+      if (lane == 0) parts[turn][warp].x = v;
+      __syncthreads();
+      v = parts[turn][0].x;
+#pragma unroll
+      for (int i = 1; i < W; ++i) v = max_nan(v, parts[turn][i].x);
+      turn ^= 1;
+    }
+    return v;
+  };
+  const float inv_c = 1.f / (float)a.C;
+  Pairs<T> dw[MODE == GRAD ? NV : 1] = {};
+  for (int64_t at_row = (int64_t)blockIdx.x * ROWS + (W == 1 ? warp : 0); at_row < a.rows; at_row += (int64_t)gridDim.x * ROWS) {
+    const uint32_t row = (uint32_t)at_row, b = row / a.tokens, t = row - b * a.tokens;
+    auto at = [&](const int64_t (&s)[2]) { return (int64_t)b * s[0] + (int64_t)t * s[1]; };
+    const T* x = static_cast<const T*>(a.x) + at(a.sx);
+    const T* res = a.res ? static_cast<const T*>(a.res) + at(a.sres) : nullptr;
+    uint4 x_raw[NV], res_raw[NV], dy_raw[MODE == GRAD ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+      x_raw[i] = make_uint4(0, 0, 0, 0);
+      if (n > 0) x_raw[i] = load_chunk<T, WHOLE>(x + c, n, aligned & AL_X);
+    }
+    if (res) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        res_raw[i] = make_uint4(0, 0, 0, 0);
+        if (n > 0) res_raw[i] = load_chunk<T, WHOLE>(res + c, n, aligned & AL_RES);
+      }
+    }
+    if constexpr (MODE == GRAD) {
+      const T* dy = static_cast<const T*>(a.dy) + at(a.sdy);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        dy_raw[i] = make_uint4(0, 0, 0, 0);
+        if (n > 0) dy_raw[i] = load_chunk<T, WHOLE>(dy + c, n, aligned & AL_DY);
+      }
+      float2 square = make_float2(0.f, 0.f), dot = square;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        const Pairs<T> v = pairs<T>(x_raw[i]);
+        Pairs<T> g = pairs<T>(dy_raw[i]);
+        times_weight<T, WHOLE>(g, a.w, c, n, aligned & AL_W);
+        add_products<T>(square, v, v);
+        add_products<T>(dot, g, v);
+      }
+      const float2 sums = row_sum(make_float2(square.x + square.y, dot.x + dot.y));
+      const float r = rsqrtf(fmaf(sums.x, inv_c, a.eps)), k = r * r * (sums.y * inv_c);
+      T* out = static_cast<T*>(a.out) + at(a.sout);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        if (n <= 0) continue;
+        const Pairs<T> v = pairs<T>(x_raw[i]), g = pairs<T>(dy_raw[i]);
+        Pairs<T> d = g;
+        times_weight<T, WHOLE>(d, a.w, c, n, aligned & AL_W);
+        norm_gradient<T>(g, d, v, r, k, dw[i]);
+        if (res) add_to<T>(d, pairs<T>(res_raw[i]));
+        store_chunk<T, WHOLE>(out + c, n, aligned & AL_OUT, packed<T>(d));
+      }
+    } else {
+      Pairs<T> v[NV];
+      float2 square = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        v[i] = pairs<T>(x_raw[i]);
+        if (res) {
+          add_to<T>(v[i], pairs<T>(res_raw[i]));
+          const uint4 sum = packed<T>(v[i]);
+          v[i] = pairs<T>(sum);  // the norm is of the sum as it is kept
+          if (a.total && n > 0) store_chunk<T, WHOLE>(static_cast<T*>(a.total) + at(a.stotal) + c, n, aligned & AL_TOTAL, sum);
+        }
+        add_products<T>(square, v[i], v[i]);
+      }
+      const float r = rsqrtf(fmaf(row_sum(make_float2(square.x + square.y, 0.f)).x, inv_c, a.eps));
+      float factor = r, top = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        times_weight<T, WHOLE>(v[i], a.w, c, n, aligned & AL_W);
+        if constexpr (MODE == E4M3)
+#pragma unroll
+          for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[i][j]);
+      }
+      if constexpr (MODE == E4M3) {
+        const RowScale q = row_scale(row_max(top), r);
+        factor = q.factor, finite = q.finite;
+        if (tid == 0) a.scale[row] = q.scale;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        if (n <= 0) continue;
+        scale_by<T>(v[i], factor);
+        if constexpr (MODE == E4M3) store_e4m3<T, WHOLE>(static_cast<uint8_t*>(a.out) + at(a.sout) + c, n, aligned & AL_OUT, finite ? v[i] : Pairs<T>{});
+        else store_chunk<T, WHOLE>(static_cast<T*>(a.out) + at(a.sout) + c, n, aligned & AL_OUT, packed<T>(v[i]));
+      }
+    }
+  }
+  if constexpr (MODE == GRAD) {
+    if (!a.partial) return;
+    float* partial = a.partial + (int64_t)blockIdx.x * a.C;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = (tid + TPR * i) * E + j;
+        if (c < a.C) partial[c] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+      }
+    }
+  }
+}
+
+// Rows that one strand of a weight sum adds up one after the other, at most.
+constexpr int64_t kSerialRows = 256;
+constexpr int kNormSms = 152;
+
+inline int chunks_of(const dit_rms_norm_args& a) { return (a.channels + (a.dtype == DIT_DTYPE_F32 ? 3 : 7)) / (a.dtype == DIT_DTYPE_F32 ? 4 : 8); }
+// Warps a row and chunks a thread of a ring kernel; none: a block holds a row in registers.
+struct Width {
+  int rw, nv;
+};
+inline Width ring_width(int chunks) {
+  for (const Width w : {Width{1, 1}, {1, 2}, {2, 2}, {2, 3}, {4, 2}, {4, 4}})
+    if (chunks <= 32 * w.rw * w.nv) return w;
+  return {0, 0};
+}
+// Blocks: what the card holds at once; of the gradient enough that no strand is longer than kSerialRows.
+inline int64_t blocks_of(const dit_rms_norm_args& a, bool backward) {
+  const Width w = ring_width(chunks_of(a));
+  const int64_t rows = a.batch * a.tokens, group = w.rw ? kRingRows : 1, most = (rows + group - 1) / group;
+  int64_t n = kNormSms * (w.rw ? ring_blocks(w.rw, w.nv, 1 + (backward ? 1 : 0) + (a.residual ? 1 : 0)) : backward ? 2 : 64);
+  const int64_t least = (rows + group * kSerialRows - 1) / (group * kSerialRows);
+  if (backward && n < least) n = least;
+  return n < most ? n : most;
+}
+
+template <typename T, int RW, int NV, int MODE, bool RES, bool WHOLE>
+cudaError_t launch_ring(const Norm& p, int64_t blocks, cudaStream_t s) {
+  return launch_kernel(norm_ring_kernel<T, RW, NV, MODE, RES, WHOLE>, dim3((unsigned)blocks), dim3(32 * RW * kRingRows),
+                       Ring<RW, NV, MODE, RES>::SMEM + kRingRows * 2 * RW * sizeof(float2), s, 1, false, p);
+}
+template <typename T, int RW, int NV, int MODE>
+cudaError_t ring(const Norm& p, bool whole, int64_t blocks, cudaStream_t s) {
+  if constexpr (MODE == GRAD)
+    if (whole) return p.res ? launch_ring<T, RW, NV, MODE, true, true>(p, blocks, s) : launch_ring<T, RW, NV, MODE, false, true>(p, blocks, s);
+  return p.res ? launch_ring<T, RW, NV, MODE, true, false>(p, blocks, s) : launch_ring<T, RW, NV, MODE, false, false>(p, blocks, s);
+}
+template <typename T, int W, int NV, int MODE, bool WHOLE>
+cudaError_t launch_rows(const Norm& p, int64_t blocks, cudaStream_t s) {
+  if (W == 1) blocks = (p.rows + kRowWarps - 1) / kRowWarps;
+  return launch_kernel(norm_kernel<T, W, NV, MODE, WHOLE>, dim3((unsigned)blocks), dim3(W == 1 ? 32 * kRowWarps : 32 * W), 0, s, 1, false, p);
+}
+template <typename T, int MODE>
+cudaError_t by_width(const Norm& p, int64_t blocks, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  const int chunks = (p.C + E - 1) / E;
+  const int need = AL_X | AL_OUT | AL_W | (p.res ? AL_RES : 0) | (p.total ? AL_TOTAL : 0) | (MODE == GRAD ? AL_DY : 0);
+  const bool whole = (p.aligned & need) == need && p.C % E == 0 && p.w;
+  if constexpr (MODE != GRAD) {
+    if (whole) {
+      if (chunks <= 32) return launch_rows<T, 1, 1, MODE, true>(p, blocks, s);
+      if (chunks <= 64) return launch_rows<T, 1, 2, MODE, true>(p, blocks, s);
+      if (chunks <= 128) return launch_rows<T, 1, 4, MODE, true>(p, blocks, s);
+      if (chunks <= 192) return launch_rows<T, 1, 6, MODE, true>(p, blocks, s);
+      if (chunks <= 256) return launch_rows<T, 1, 8, MODE, true>(p, blocks, s);
+      blocks = p.rows < kNormSms * 64u ? p.rows : kNormSms * 64u;
+      if (chunks <= 512) return launch_rows<T, 4, 4, MODE, true>(p, blocks, s);
+      if (chunks <= 1024) return launch_rows<T, 8, 4, MODE, true>(p, blocks, s);
+      if (chunks <= 2048) return launch_rows<T, 16, 4, MODE, true>(p, blocks, s);
+      if constexpr (E == 4) return launch_rows<T, 32, 4, MODE, true>(p, blocks, s);
+    }
+  }
+  if (chunks <= 32) return ring<T, 1, 1, MODE>(p, whole, blocks, s);
+  if (chunks <= 64) return ring<T, 1, 2, MODE>(p, whole, blocks, s);
+  if (chunks <= 128) return ring<T, 2, 2, MODE>(p, whole, blocks, s);
+  if (chunks <= 192) return ring<T, 2, 3, MODE>(p, whole, blocks, s);
+  if (chunks <= 256) return ring<T, 4, 2, MODE>(p, whole, blocks, s);
+  if (chunks <= 512) return ring<T, 4, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 1024) return launch_rows<T, 8, 4, MODE, false>(p, blocks, s);
+  if (chunks <= 2048) return launch_rows<T, 16, 4, MODE, false>(p, blocks, s);
+  if constexpr (E == 4) return launch_rows<T, 32, 4, MODE, false>(p, blocks, s);
+  return cudaErrorInvalidValue;
+}
+
+// All kernels of one activation type; an instance in a source file of its own.
+template <typename T>
+cudaError_t by_mode(const Norm& p, int mode, int64_t blocks, cudaStream_t s) {
+  return mode == GRAD ? by_width<T, GRAD>(p, blocks, s) : mode == E4M3 ? by_width<T, E4M3>(p, blocks, s) : by_width<T, SAME>(p, blocks, s);
+}
+extern template cudaError_t by_mode<float>(const Norm&, int, int64_t, cudaStream_t);
+extern template cudaError_t by_mode<__nv_bfloat16>(const Norm&, int, int64_t, cudaStream_t);
+extern template cudaError_t by_mode<__half>(const Norm&, int, int64_t, cudaStream_t);
+
+}  // namespace norm
+
+}  // namespace dit

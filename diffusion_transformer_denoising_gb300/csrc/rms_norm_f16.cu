@@ -1,0 +1,4 @@
+// The RMS norm's kernels on f16 activations.
+#include "rms_norm.cuh"
+
+template cudaError_t dit::norm::by_mode<__half>(const dit::norm::Norm&, int, int64_t, cudaStream_t);
