@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kSumColumns * kSumStrands) column_sums_kernel(
   const int col = threadIdx.x % kSumColumns, strand = threadIdx.x / kSumColumns;
   const int c = blockIdx.x * kSumColumns + col;
   wait_previous();
+  start_next();
   if (!out) return;
   LongSum s;
   if (c < a.n) {

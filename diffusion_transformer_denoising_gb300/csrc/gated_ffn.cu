@@ -75,9 +75,9 @@ struct Product {
 };
 
 // ---------------------------------------------------------------- activation
-// z = g (SiLU) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (GELU, tanh form): act(g) = g sigmoid(z).
-// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by ex2.approx and rcp.approx, a few 2^-22 of
-// itself (the results are rounded to 16 bits), 0 below z = -87.
+// z = g (SiLU) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (GELU, tanh form): act(g) = g sigmoid(z),
+// by ex2.approx and rcp.approx.  The rounding of the exponent z log2 e counts most:
+// 2^-16 of the value at |z| = 90, against the 2^-11 (fp16) of rounding it.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 DIT_DEV float rcp_approx(float x) {
@@ -85,9 +85,34 @@ DIT_DEV float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// act(g) u of two columns
+DIT_DEV float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int ACT>
+DIT_DEV float argument(float g) {
+  return ACT == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, g * g, kGelu2);
+}
+// sigmoid(z) and 1 - sigmoid(z), each on its own scale: subnormal numbers are kept.
+DIT_DEV float2 sigmoids(float z) {
+  const float m = fminf(z * kLog2e, 126.f);
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(m));
+  const float r = rcp_approx(1.f + e);
+  return make_float2(e * r, m < 126.f ? r : 0.f);
+}
+// act(g) u of two columns.
 template <int ACT>
 DIT_DEV float2 gated2(float2 g, float2 u) {
+  return make_float2(g.x * sigmoids(argument<ACT>(g.x)).x * u.x, g.y * sigmoids(argument<ACT>(g.y)).x * u.y);
+}
+// The same in fewer instructions for g above kFar, where 2^-z stays in range (below,
+// sigmoid(z) would go to 0 too early: the result is g times it).
+template <int ACT>
+constexpr float kFar = ACT == DIT_ACT_SILU ? -80.f : -9.6f;
+template <int ACT>
+DIT_DEV float2 gated2_near(float2 g, float2 u) {
   float2 m;  // -z log2 e
   if constexpr (ACT == DIT_ACT_SILU) {
     m = fmul2(g, make_float2(-kLog2e, -kLog2e));
@@ -101,14 +126,12 @@ DIT_DEV float2 gated2(float2 g, float2 u) {
 // act(g) and act'(g) = s + g s (1 - s) z'
 template <int ACT>
 DIT_DEV float2 activation_slope(float g) {
-  const float q = g * g;
-  const float z = ACT == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, q, kGelu2);
-  const float e = ex2_approx(fminf(-z * kLog2e, 126.f));
-  const float s = rcp_approx(1.f + e), gs = g * s, rest = e * s;  // rest = 1 - s
-  if constexpr (ACT == DIT_ACT_SILU) return make_float2(gs, fmaf(gs, rest, s));
-  // far out rest is 0 and z' may be infinite: the limit of their product is 0
-  const float zp = fmaf(3.f * 0.044715f * kGelu2, q, kGelu2);
-  return make_float2(gs, rest == 0.f ? s : fmaf(gs * rest, zp, s));
+  const float2 s = sigmoids(argument<ACT>(g));
+  const float gs = g * s.x;
+  if constexpr (ACT == DIT_ACT_SILU) return make_float2(gs, fmaf(gs, s.y, s.x));
+  // far out 1 - s is 0 and z' may be infinite: the limit of their product is 0
+  const float zp = fmaf(3.f * 0.044715f * kGelu2, g * g, kGelu2);
+  return make_float2(gs, s.y == 0.f || s.x == 0.f ? s.x : fmaf(gs * s.y, zp, s.x));
 }
 
 DIT_DEV uint32_t pack16(int f16, float lo, float hi) { return f16 ? pack2<__half>(lo, hi) : pack_bf16x2(lo, hi); }
@@ -277,10 +300,21 @@ DIT_DEV void drain(const Product& P, const Tile& t, uint32_t tacc, int64_t row0,
             if (last && hh == 1) done();
             finish32<F8>(g, P, 0, row_scale, col0 + hh * 32);
             finish32<F8>(v, P, 1, row_scale, col0 + hh * 32);
+            float low = g[0];
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 h = gated2<ACT>(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
-              v[j] = h.x, v[j + 1] = h.y;
+            for (int j = 0; j < 32; j += 2) low = fmin3(low, g[j], g[j + 1]);
+            if (__any_sync(0xffffffffu, low < kFar<ACT>)) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 h = gated2<ACT>(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
+                v[j] = h.x, v[j + 1] = h.y;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 h = gated2_near<ACT>(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
+                v[j] = h.x, v[j + 1] = h.y;
+              }
             }
           } else {
             load32(at + (o - 1) * (BN / 2), v);
@@ -356,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if constexpr (PAIR) st_cluster_u32(cluster_map((const void*)abort_flag, rank ^ 1u), 1u);
   };
   wait_previous();  // operands that a kernel of the same call wrote
+  start_next();
   const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
 
@@ -580,6 +615,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) few_rows_kernel(const Few a
   constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 ? 2 : 4;
   __shared__ float sums[2][kFewWarps][NT][16][9];
   wait_previous();
+  start_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int f0 = blockIdx.x * 16;
   const int steps = (a.D + STEP - 1) / STEP;
@@ -677,6 +713,7 @@ DIT_DEV void sum_planes(const float* p, int64_t step, int n, float (&v)[4]) {
 template <bool GATED>
 __global__ void __launch_bounds__(256) join_kernel(const Join J) {
   wait_previous();
+  start_next();
   const int64_t groups = J.ldp / 4, total = J.M * groups;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / groups;
@@ -726,6 +763,7 @@ struct Pack {
 template <typename E>
 __global__ void __launch_bounds__(256) pack_kernel(const Pack a) {
   wait_previous();
+  start_next();
   const int o = blockIdx.y;
   if (!a.src[o]) return;
   const E* src = reinterpret_cast<const E*>(a.src[o]);
@@ -764,6 +802,7 @@ __global__ void __launch_bounds__(256) slopes_kernel(const Slopes a) {
   constexpr int ROWS = 2;
   __shared__ float sums[8][2][32][9];
   wait_previous();
+  start_next();
   const int lane = threadIdx.x, ty = threadIdx.y;
   const int c = (blockIdx.y * 32 + lane) * 8;
   const int n = a.F - c;

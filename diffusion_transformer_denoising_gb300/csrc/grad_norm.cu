@@ -19,18 +19,23 @@ namespace dit {
 
 namespace {
 
-constexpr int kPiece = 16384;    // values a block takes at a time
-constexpr int kTensors = 640;    // of a launch: its parameters hold their descriptions (32764 bytes at most)
+// Values a block takes at a time: few where there are few, so that they spread over the card.
+constexpr int kPieceSmall = 2048, kPieceLarge = 16384;
+constexpr int64_t kFew = (int64_t)1 << 22;
+// Tensors of a launch: its parameters hold their descriptions (32764 bytes at most).
+// Few are described in fewer bytes, which every launch copies.
+constexpr int kTensors = 640, kFewTensors = 32;
 constexpr int kGradThreads = 256;
 constexpr int kGradBlocks = 152 * 3;  // of a pass over the squares: the sums' order does not depend on the device
 
+template <int N>
 struct Tensors {
-  const void* grad[kTensors];
-  void* out[kTensors];
-  int64_t numel[kTensors];
-  uint32_t end[kTensors];        // pieces up to and with tensor i, counted over all launches
-  int16_t dtype[kTensors];
-  int n;
+  const void* grad[N];
+  void* out[N];
+  int64_t numel[N];
+  uint32_t end[N];               // pieces up to and with tensor i, counted over all launches
+  int16_t dtype[N];
+  int n, piece;                  // tensors; values of a piece
   uint32_t first;                // pieces of the launches before
   uint32_t parts;                // sums of all launches
   uint32_t first_part;
@@ -39,10 +44,11 @@ struct Tensors {
   float max_norm;
   int write_norm;
 };
-static_assert(sizeof(Tensors) <= 32764, "parameters of a launch");
+static_assert(sizeof(Tensors<kTensors>) <= 32764, "parameters of a launch");
 
 // The tensor of a piece: the first whose end is above it.
-DIT_DEV int tensor_of(const Tensors& t, uint32_t piece) {
+template <int N>
+DIT_DEV int tensor_of(const Tensors<N>& t, uint32_t piece) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -93,7 +99,7 @@ DIT_DEV double block_sum(double v, double* shared) {
 
 template <typename T>
 DIT_DEV double piece_squares(const T* p, int n) {
-  constexpr int E = 16 / sizeof(T), PER = kPiece / (E * kGradThreads);  // vectors a thread
+  constexpr int E = 16 / sizeof(T), PER = kPieceLarge / (E * kGradThreads);  // vectors a thread
   double rest = 0.;
   float fine = 0.f;
   // values in front of the first 16-byte boundary, then whole vectors, then the rest
@@ -118,14 +124,15 @@ DIT_DEV double piece_squares(const T* p, int n) {
   return rest + (double)fine;
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid_constant__ Tensors t) {
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid_constant__ Tensors<N> t) {
   __shared__ double shared[kGradThreads / 32];
   const uint32_t last = t.end[t.n - 1];
   double v = 0.;
   for (uint32_t piece = t.first + blockIdx.x; piece < last; piece += gridDim.x) {
     const int i = tensor_of(t, piece);
-    const int64_t begin = (int64_t)(piece - (i ? t.end[i - 1] : t.first)) * kPiece;
-    const int n = (int)min((int64_t)kPiece, t.numel[i] - begin);
+    const int64_t begin = (int64_t)(piece - (i ? t.end[i - 1] : t.first)) * t.piece;
+    const int n = (int)min((int64_t)t.piece, t.numel[i] - begin);
     if (t.dtype[i] == DIT_DTYPE_F32) v += piece_squares(static_cast<const float*>(t.grad[i]) + begin, n);
     else if (t.dtype[i] == DIT_DTYPE_BF16) v += piece_squares(static_cast<const __nv_bfloat16*>(t.grad[i]) + begin, n);
     else v += piece_squares(static_cast<const __half*>(t.grad[i]) + begin, n);
@@ -156,7 +163,8 @@ DIT_DEV void scale_piece(const T* p, T* out, int n, float k) {
   }
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ Tensors t) {
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ Tensors<N> t) {
   __shared__ double shared[kGradThreads / 32];
   wait_previous();
   double v = 0.;
@@ -173,32 +181,37 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     const uint32_t piece = last - 1 - j;
     const int i = tensor_of(t, piece);
     if (!clip && t.out[i] == t.grad[i]) continue;
-    const int64_t begin = (int64_t)(piece - (i ? t.end[i - 1] : t.first)) * kPiece;
-    const int n = (int)min((int64_t)kPiece, t.numel[i] - begin);
+    const int64_t begin = (int64_t)(piece - (i ? t.end[i - 1] : t.first)) * t.piece;
+    const int n = (int)min((int64_t)t.piece, t.numel[i] - begin);
     if (t.dtype[i] == DIT_DTYPE_F32) scale_piece(static_cast<const float*>(t.grad[i]) + begin, static_cast<float*>(t.out[i]) + begin, n, k);
     else if (t.dtype[i] == DIT_DTYPE_BF16) scale_piece(static_cast<const __nv_bfloat16*>(t.grad[i]) + begin, static_cast<__nv_bfloat16*>(t.out[i]) + begin, n, k);
     else scale_piece(static_cast<const __half*>(t.grad[i]) + begin, static_cast<__half*>(t.out[i]) + begin, n, k);
   }
 }
 
-int64_t pieces_of(const dit_grad_tensor& t) { return (t.numel + kPiece - 1) / kPiece; }
+int piece_size(const dit_grad_tensor* t, int64_t n) {
+  int64_t all = 0;
+  for (int64_t i = 0; i < n; ++i) all += t[i].numel;
+  return all <= kFew ? kPieceSmall : kPieceLarge;
+}
+int64_t pieces_of(const dit_grad_tensor& t, int piece) { return (t.numel + piece - 1) / piece; }
 
 // One launch's tensors, from tensor i on.
 struct Batch {
   int64_t next, pieces;
   int n;
 };
-Batch batch_of(const dit_grad_tensor* t, int64_t n, int64_t i) {
+Batch batch_of(const dit_grad_tensor* t, int64_t n, int64_t i, int piece) {
   Batch b{i, 0, 0};
   for (; b.next < n && b.n < kTensors; ++b.next)
-    if (t[b.next].numel > 0) b.pieces += pieces_of(t[b.next]), ++b.n;
+    if (t[b.next].numel > 0) b.pieces += pieces_of(t[b.next], piece), ++b.n;
   return b;
 }
 int64_t parts_of(const Batch& b) { return b.pieces < kGradBlocks ? b.pieces : kGradBlocks; }
-int64_t all_parts(const dit_grad_tensor* t, int64_t n) {
+int64_t all_parts(const dit_grad_tensor* t, int64_t n, int piece) {
   int64_t parts = 0;
   for (int64_t i = 0; i < n;) {
-    const Batch b = batch_of(t, n, i);
+    const Batch b = batch_of(t, n, i, piece);
     parts += parts_of(b);
     i = b.next;
   }
@@ -208,36 +221,40 @@ int64_t all_parts(const dit_grad_tensor* t, int64_t n) {
 }  // namespace
 
 int64_t grad_norm_workspace(const dit_grad_tensor* t, int64_t n) {
-  const int64_t parts = all_parts(t, n);
+  const int64_t parts = all_parts(t, n, piece_size(t, n));
   return (parts > 0 ? parts : 1) * (int64_t)sizeof(double);
 }
 
-cudaError_t grad_norm_run(const dit_grad_tensor* t, int64_t n, float max_norm, float* norm, void* workspace, cudaStream_t s) {
+namespace {
+
+template <int N>
+cudaError_t run(const dit_grad_tensor* t, int64_t n, float max_norm, float* norm, void* workspace, cudaStream_t s) {
   bool products = false;
   for (int64_t i = 0; i < n; ++i) products |= t[i].numel > 0 && t[i].out;
+  Tensors<N> p;
+  p.piece = piece_size(t, n);
+  p.parts = (uint32_t)all_parts(t, n, p.piece);
+  p.sums = static_cast<double*>(workspace), p.norm = norm, p.max_norm = max_norm;
   // squares of every launch first, then products of every launch
   for (int pass = 0; pass < 2; ++pass) {
-    Tensors p;
     p.first = p.first_part = 0;
-    p.parts = (uint32_t)all_parts(t, n);
-    p.sums = static_cast<double*>(workspace), p.norm = norm, p.max_norm = max_norm;
     p.write_norm = 1;
     int64_t i = 0;
     do {
-      const Batch b = batch_of(t, n, i);
+      const Batch b = batch_of(t, n, i, p.piece);
       uint32_t end = p.first;
       for (p.n = 0; i < b.next; ++i) {
         if (t[i].numel == 0) continue;
         p.grad[p.n] = t[i].grad, p.out[p.n] = t[i].out, p.numel[p.n] = t[i].numel;
-        p.dtype[p.n] = (int16_t)t[i].dtype, p.end[p.n] = end += (uint32_t)pieces_of(t[i]);
+        p.dtype[p.n] = (int16_t)t[i].dtype, p.end[p.n] = end += (uint32_t)pieces_of(t[i], p.piece);
         ++p.n;
       }
       cudaError_t e = cudaSuccess;
       if (pass == 0) {
-        if (b.n) e = launch_kernel(grad_squares_kernel, dim3((unsigned)parts_of(b)), dim3(kGradThreads), 0, s, 1, false, p);
+        if (b.n) e = launch_kernel(grad_squares_kernel<N>, dim3((unsigned)parts_of(b)), dim3(kGradThreads), 0, s, 1, false, p);
       } else {
         const int64_t blocks = !products ? 1 : b.pieces < 152 * 8 ? b.pieces : 152 * 8;
-        e = launch_kernel(grad_clip_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kGradThreads), 0, s, 1, true, p);
+        e = launch_kernel(grad_clip_kernel<N>, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kGradThreads), 0, s, 1, true, p);
       }
       if (e != cudaSuccess) return e;
       p.first = end, p.first_part += (uint32_t)parts_of(b);
@@ -245,6 +262,14 @@ cudaError_t grad_norm_run(const dit_grad_tensor* t, int64_t n, float max_norm, f
     } while (i < n && (pass == 0 || products));
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t grad_norm_run(const dit_grad_tensor* t, int64_t n, float max_norm, float* norm, void* workspace, cudaStream_t s) {
+  int64_t some = 0;
+  for (int64_t i = 0; i < n; ++i) some += t[i].numel > 0;
+  return some <= kFewTensors ? run<kFewTensors>(t, n, max_norm, norm, workspace, s) : run<kTensors>(t, n, max_norm, norm, workspace, s);
 }
 
 }  // namespace dit

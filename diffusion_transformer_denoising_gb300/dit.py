@@ -191,12 +191,12 @@ def flow_euler_step(x, v, sigma: float, sigma_next: float, n: int, stream=None):
 
 
 # ------------------------------------------------------------- operators
-# dit_rope_args and dit_group_norm_args of include/dit.h, packed in one go
+# the argument structures of include/dit.h, packed in one go
 _ROPE_ARGS = struct.Struct("<2q8i2fQ2q2i" + 2 * "2iQ3qQ3qQ3q2Q")
 _GN_ARGS = struct.Struct("<2q4ifiQ2qQ2qQ2q6Q")
 _NORM_ARGS = struct.Struct("<2q3if" + 5 * "Q2q" + "3Q")
 _FFN_ARGS = struct.Struct("<q6i" + 3 * "Qq" + "5Q" + 6 * "Qq" + "2Q")
-_GRAD_TENSOR = struct.Struct("<2Qq2i")
+_INF = float("inf")
 _NO_VIEW = (0, 0, 0, 0)
 _torch = None          # the module, its dtypes as dit.h names them and its grad mode, on first use
 _dtype_codes = {}
@@ -470,43 +470,54 @@ def dit_group_norm_workspace_bytes(x, groups: int, backward: bool) -> int:
     return n
 
 
-def _any_requires_grad(*tensors):
-    return any(t is not None and t.requires_grad for t in tensors)
-
-
 def _token_view(name, t, shape, dtype):
     """(pointer, batch stride, token stride) of a [..., channels] view: one axis in front of the channels is tokens of one
     batch element, of several the first is the batch."""
     if t is None:
         return 0, 0, 0
+    if t.shape == shape and t.dtype is dtype and len(shape) == 3:
+        sb, st, sc = t.stride()
+        if sc == 1:
+            return t.data_ptr(), sb, st
     if len(shape) >= 3:
         return _pixel_view(name, t, shape, dtype)
-    if t.shape != shape or t.dtype is not dtype or (t.numel() and t.stride(-1) != 1 and shape[-1] > 1):
-        if t.shape == shape and t.dtype is dtype:
-            _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous")
+    if t.shape != shape or t.dtype is not dtype:
         _bad_view(name, t, shape, dtype)
+    if t.numel() and t.stride(-1) != 1 and shape[-1] > 1:
+        _refuse(DIT_ERR_SHAPE, f"{name}: channels must be contiguous")
     return (t.data_ptr(), 0, t.stride(0) if len(shape) == 2 else 0) if t.numel() else (0, 0, 0)
+
+
+def _norm_rows(shape):
+    """batch, tokens and channels of a [..., channels] shape"""
+    if len(shape) == 3:
+        return shape
+    if len(shape) < 1:
+        _refuse(DIT_ERR_SHAPE, "x must be [..., channels]")
+    B, N = (shape[0] if len(shape) > 3 else 1), 1
+    for v in shape[1:-1] if len(shape) > 3 else shape[:-1]:
+        N *= v
+    return B, N, shape[-1]
 
 
 def _norm_args(x, residual, total, dy, out, out_dtype, scale, weight, dweight, eps):
     torch = _torch or _use_torch()
-    if out is not None and _grad_mode() and _any_requires_grad(x, residual, dy, weight):
+    if _grad_mode() and (x.requires_grad or residual is not None and residual.requires_grad or
+                         weight is not None and weight.requires_grad or dy is not None and dy.requires_grad):
         _refuse_autograd()
     shape, dtype = x.shape, x.dtype
-    if len(shape) < 1:
-        _refuse(DIT_ERR_SHAPE, "x must be [..., channels]")
-    B, N = (shape[0] if len(shape) > 2 else 1), 1
-    for v in shape[1:-1] if len(shape) > 2 else shape[:-1]:
-        N *= v
+    B, N, C = _norm_rows(shape)
     code = _dtype_code(dtype)
     if out_dtype is not dtype and out_dtype is not torch.float8_e4m3fn:
         _refuse(DIT_ERR_INVALID_ARG, f"out is {out_dtype}: {dtype} or float8_e4m3fn is wanted")
     try:
-        return _NORM_ARGS.pack(B, N, shape[-1], code, code if out_dtype is dtype else DTYPE_E4M3, eps,
+        return _NORM_ARGS.pack(B, N, C, code, code if out_dtype is dtype else DTYPE_E4M3, eps,
                                *_token_view("x", x, shape, dtype), *_token_view("residual", residual, shape, dtype),
                                *_token_view("total", total, shape, dtype), *_token_view("dy", dy, shape, dtype),
-                               *_token_view("out", out, shape, out_dtype), _param("scale", scale, shape[:-1]),
-                               _param("weight", weight, shape[-1:]), _param("dweight", dweight, shape[-1:]))
+                               *_token_view("out", out, shape, out_dtype),
+                               0 if scale is None else _param("scale", scale, shape[:-1]),
+                               0 if weight is None else _param("weight", weight, (C,)),
+                               0 if dweight is None else _param("dweight", dweight, (C,)))
     except (struct.error, OverflowError) as e:
         _refuse_scalar(e)
 
@@ -539,16 +550,18 @@ def dit_rms_norm_backward(total, dout, dx, *, dtotal=None, weight=None, dweight=
 
 def dit_rms_norm_workspace_bytes(total) -> int:
     """Workspace of a dit_rms_norm_backward with dweight on tensors of this shape and type."""
-    torch = _torch or _use_torch()
-    shape = total.shape
-    B, N = (shape[0] if len(shape) > 2 else 1), 1
-    for v in shape[1:-1] if len(shape) > 2 else shape[:-1]:
-        N *= v
+    _torch or _use_torch()
     code = _dtype_code(total.dtype)
-    n = lib().dit_rms_norm_workspace_bytes(_NORM_ARGS.pack(B, N, shape[-1], code, code, 0.0, *(0,) * 15, 0, 16, 32))
+    n = lib().dit_rms_norm_workspace_bytes(_NORM_ARGS.pack(*_norm_rows(total.shape), code, code, 0.0, *(0,) * 15, 0, 16, 32))
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
     return n
+
+
+def _grad_mode_of(*tensors):
+    """Whether grad mode is on and one of the tensors requires grad."""
+    _torch or _use_torch()
+    return _grad_mode() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def _matrix(name, t, shape, dtype):
@@ -557,6 +570,10 @@ def _matrix(name, t, shape, dtype):
         return 0, 0
     if t.shape != shape or t.dtype is not dtype:
         _bad_view(name, t, shape, dtype)
+    if len(shape) == 2:
+        step, column = t.stride()
+        if column == 1:
+            return t.data_ptr(), step
     if t.numel() == 0:
         return 0, 0
     stride = t.stride()
@@ -576,11 +593,12 @@ def _matrix(name, t, shape, dtype):
     return t.data_ptr(), step or 0
 
 
-def _ffn_args(x, w_gate, w_up, out, gate, up, act, scales=(None,) * 3, biases=(None,) * 2, dx=None, dw_gate=None,
-              dw_up=None, dbias_gate=None, dbias_up=None):
+def _ffn_args(x, w_gate, w_up, out, gate, up, act, x_scale=None, gate_scale=None, up_scale=None, bias_gate=None,
+              bias_up=None, dx=None, dw_gate=None, dw_up=None, dbias_gate=None, dbias_up=None):
     _torch or _use_torch()
-    if _grad_mode() and _any_requires_grad(x, w_gate, w_up, *biases, *((gate, up, out) if dx is not None or
-                                           dw_gate is not None or dw_up is not None else ())):
+    if _grad_mode() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad or
+                         bias_gate is not None and bias_gate.requires_grad or
+                         bias_up is not None and bias_up.requires_grad):
         _refuse_autograd()
     xs, ws = x.shape, w_gate.shape
     if len(xs) < 1 or len(ws) != 2 or ws[1] != xs[-1]:
@@ -595,13 +613,17 @@ def _ffn_args(x, w_gate, w_up, out, gate, up, act, scales=(None,) * 3, biases=(N
         _refuse(DIT_ERR_INVALID_ARG, f"unsupported dtype {dtype if codes[0] is None else operand}")
     try:
         return _FFN_ARGS.pack(rows, D, F, *codes, act, 0, *_matrix("x", x, xs, operand), *_matrix("w_gate", w_gate, ws, operand),
-                              *_matrix("w_up", w_up, ws, operand), _param("x_scale", scales[0], xs[:-1]),
-                              _param("gate_scale", scales[1], ws[:1]), _param("up_scale", scales[2], ws[:1]),
-                              _param("bias_gate", biases[0], ws[:1]), _param("bias_up", biases[1], ws[:1]),
+                              *_matrix("w_up", w_up, ws, operand),
+                              0 if x_scale is None else _param("x_scale", x_scale, xs[:-1]),
+                              0 if gate_scale is None else _param("gate_scale", gate_scale, (F,)),
+                              0 if up_scale is None else _param("up_scale", up_scale, (F,)),
+                              0 if bias_gate is None else _param("bias_gate", bias_gate, (F,)),
+                              0 if bias_up is None else _param("bias_up", bias_up, (F,)),
                               *_matrix("gate", gate, hs, dtype), *_matrix("up", up, hs, dtype),
                               *_matrix("out", out, hs, dtype), *_matrix("dx", dx, xs, dtype),
                               *_matrix("dw_gate", dw_gate, ws, dtype), *_matrix("dw_up", dw_up, ws, dtype),
-                              _param("dbias_gate", dbias_gate, ws[:1]), _param("dbias_up", dbias_up, ws[:1]))
+                              0 if dbias_gate is None else _param("dbias_gate", dbias_gate, (F,)),
+                              0 if dbias_up is None else _param("dbias_up", dbias_up, (F,)))
     except (struct.error, OverflowError) as e:
         _refuse_scalar(e)
 
@@ -616,7 +638,7 @@ def dit_gated_ffn_forward(x, w_gate, w_up, out, *, gate=None, up=None, bias_gate
     ACT_GELU (tanh form).  workspace: a contiguous tensor of
     dit_gated_ffn_workspace_bytes, or None to take one from torch's allocator
     where the call needs it (only on torch's current stream)."""
-    args = _ffn_args(x, w_gate, w_up, out, gate, up, act, (x_scale, gate_scale, up_scale), (bias_gate, bias_up))
+    args = _ffn_args(x, w_gate, w_up, out, gate, up, act, x_scale, gate_scale, up_scale, bias_gate, bias_up)
     L, s = lib(), _raw_stream(x, stream)
     ws, n, owner = _workspace(x, workspace, stream, L.dit_gated_ffn_workspace_bytes(args, 0))
     _check(L.dit_gated_ffn_forward(args, ws, n, s))
@@ -627,6 +649,8 @@ def dit_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, *, dx=None, dw_gate=
     """Gradient of dit_gated_ffn_forward from the gate and up that it kept.  Each
     of dx, dw_gate, dw_up (of the inputs' type) and dbias_gate, dbias_up (float32
     [hidden]) is overwritten where given."""
+    if _grad_mode_of(gate, up, dout):
+        _refuse_autograd()
     args = _ffn_args(x, w_gate, w_up, dout, gate, up, act, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dbias_gate=dbias_gate,
                      dbias_up=dbias_up)
     L, s = lib(), _raw_stream(x, stream)
@@ -659,22 +683,32 @@ def dit_gated_ffn_synchronize(stream=None):
 
 
 def _grad_tensors(grads, clipped):
-    torch = _torch or _use_torch()
-    pack, codes, parts, ref = _GRAD_TENSOR.pack, _dtype_codes, [], None
-    for i, g in enumerate(grads):
-        if g is None:
-            continue
-        o = None if clipped is None else clipped[i]
-        code = codes.get(g.dtype)
-        if code is None:
-            _refuse(DIT_ERR_INVALID_ARG, f"gradient {i} is {g.dtype}")
-        if not g.is_contiguous():
-            _refuse(DIT_ERR_SHAPE, f"gradient {i} must be contiguous")
-        if o is not None and o is not g and (o.shape != g.shape or o.dtype is not g.dtype or not o.is_contiguous()):
-            _refuse(DIT_ERR_SHAPE, f"the output of gradient {i} must be contiguous, of its shape and type")
-        if g.numel():
-            parts.append(pack(g.data_ptr(), 0 if o is None else o.data_ptr(), g.numel(), code, 0))
-    return b"".join(parts), len(parts)
+    """The packed dit_grad_tensors of the entries that are not None, and their number."""
+    T = (_torch or _use_torch()).Tensor
+    live = [g for g in grads if g is not None]
+    # whole lists at a time: a model has hundreds of gradients
+    codes, sizes = [_dtype_codes.get(g.dtype) for g in live], list(map(T.numel, live))
+    if None in codes:
+        _refuse(DIT_ERR_INVALID_ARG, f"a gradient is {live[codes.index(None)].dtype}")
+    if not all(map(T.is_contiguous, live)):
+        _refuse(DIT_ERR_SHAPE, "gradients must be contiguous")
+    if _grad_mode() and any([g.requires_grad for g in live]):
+        _refuse_autograd()
+    pointers = list(map(T.data_ptr, live))
+    if clipped is None:
+        outs = [0] * len(live)
+    elif clipped is grads:
+        outs = pointers
+    else:
+        made = [c for c in clipped if c is not None]
+        if (len(clipped) != len(grads) or len(made) != len(live) or list(map(T.numel, made)) != sizes or
+                [_dtype_codes.get(c.dtype) for c in made] != codes or not all(map(T.is_contiguous, made))):
+            _refuse(DIT_ERR_SHAPE, "clipped must hold a contiguous tensor of the size and type of each gradient")
+        outs = list(map(T.data_ptr, made))
+    n = len(live)
+    fields = [0] * (4 * n)
+    fields[0::4], fields[1::4], fields[2::4], fields[3::4] = pointers, outs, sizes, codes
+    return struct.pack("<" + n * "2Q2q", *fields), n  # the type and the reserved field as one number
 
 
 def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, stream=None):
@@ -685,35 +719,30 @@ def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, s
     are.  workspace: a contiguous tensor of dit_grad_norm_workspace_bytes, or
     None to take one from torch's allocator (only on torch's current stream)."""
     torch = _torch or _use_torch()
-    grads = list(grads)
+    limit = _INF
     if max_norm is None:
         if clipped is not None:
             _refuse(DIT_ERR_INVALID_ARG, "clipped without max_norm")
-    elif clipped is None:
-        clipped = grads
     else:
-        clipped = list(clipped)
-        if len(clipped) != len(grads) or any((c is None) != (g is None) for c, g in zip(clipped, grads)):
-            _refuse(DIT_ERR_SHAPE, "clipped must hold one tensor for each gradient")
+        try:
+            limit = C.c_float(max_norm).value
+        except TypeError as e:
+            _refuse_scalar(e)
+        if limit == _INF:
+            _refuse(DIT_ERR_INVALID_ARG, "max_norm must be finite (None: the norm only)")
+        if clipped is None:
+            clipped = grads
     if norm.dtype is not torch.float32 or norm.numel() != 1:
         _refuse(DIT_ERR_INVALID_ARG, "norm must be one float32")
-    if _grad_mode() and _any_requires_grad(*grads):
-        _refuse_autograd()
     tensors, n = _grad_tensors(grads, clipped)
     L, s = lib(), _raw_stream(norm, stream)
     ws, size, owner = _workspace(norm, workspace, stream, L.dit_grad_norm_workspace_bytes(tensors, n))
-    try:
-        limit = C.c_float(float("inf") if max_norm is None else max_norm)
-    except TypeError as e:
-        _refuse_scalar(e)
-    if max_norm is not None and limit.value == float("inf"):
-        _refuse(DIT_ERR_INVALID_ARG, "max_norm must be finite (None: the norm only)")
     _check(L.dit_grad_norm(tensors, n, limit, norm.data_ptr(), ws, size, s))
 
 
 def dit_grad_norm_workspace_bytes(grads) -> int:
     """Workspace of a dit_grad_norm call on these tensors."""
-    n = lib().dit_grad_norm_workspace_bytes(*_grad_tensors(list(grads), None))
+    n = lib().dit_grad_norm_workspace_bytes(*_grad_tensors(grads, None))
     if n < 0:
         raise DitError(DIT_ERR_SHAPE, lib().dit_last_error().decode())
     return n
