@@ -15,6 +15,7 @@ struct ColumnSums {
   int n;
   int64_t second;       // floats from the first sum's columns to the second's
   float* out[2];
+  int late;             // the kernels before the previous one have written what is read
 };
 constexpr int kSumColumns = 8, kSumStrands = 64;
 template <int UNUSED = 0>
@@ -23,11 +24,10 @@ __global__ void __launch_bounds__(kSumColumns * kSumStrands) column_sums_kernel(
   float* out = a.out[blockIdx.y];
   const int col = threadIdx.x % kSumColumns, strand = threadIdx.x / kSumColumns;
   const int c = blockIdx.x * kSumColumns + col;
-  wait_previous();
+  if (!a.late) wait_previous();
   start_next();
-  if (!out) return;
   LongSum s;
-  if (c < a.n) {
+  if (out && c < a.n) {
     const float* p = a.partial + blockIdx.y * a.second + c;
     constexpr int U = 8;  // loads under way
     for (int64_t r = strand; r < a.rows; r += U * kSumStrands) {
@@ -41,11 +41,13 @@ __global__ void __launch_bounds__(kSumColumns * kSumStrands) column_sums_kernel(
   strands[col][strand] = s.value();
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp >= kSumColumns) return;
-  float v = strands[warp][lane] + strands[warp][lane + 32];
+  if (out && warp < kSumColumns) {
+    float v = strands[warp][lane] + strands[warp][lane + 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0 && blockIdx.x * kSumColumns + warp < a.n) out[blockIdx.x * kSumColumns + warp] = v;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * kSumColumns + warp < a.n) out[blockIdx.x * kSumColumns + warp] = v;
+  }
+  if (a.late) wait_previous();  // the call's end is the end of all its kernels
 }
 inline cudaError_t column_sums(const ColumnSums& a, cudaStream_t s) {
   return launch_kernel(column_sums_kernel<0>, dim3((a.n + kSumColumns - 1) / kSumColumns, a.out[1] ? 2 : 1),

@@ -50,7 +50,7 @@ cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* works
   p.partial = a.dweight ? workspace : nullptr;
   const cudaError_t e = by_type(a.dtype, p, GRAD, blocks, s);
   if (e != cudaSuccess || !a.dweight) return e;
-  return column_sums(ColumnSums{workspace, blocks, a.channels, a.channels, 0, {a.dweight, nullptr}}, s);
+  return column_sums(ColumnSums{workspace, blocks, a.channels, a.channels, 0, {a.dweight, nullptr}, 0}, s);
 }
 
 }  // namespace dit

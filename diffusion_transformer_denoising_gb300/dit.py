@@ -558,12 +558,6 @@ def dit_rms_norm_workspace_bytes(total) -> int:
     return n
 
 
-def _grad_mode_of(*tensors):
-    """Whether grad mode is on and one of the tensors requires grad."""
-    _torch or _use_torch()
-    return _grad_mode() and any(t is not None and t.requires_grad for t in tensors)
-
-
 def _matrix(name, t, shape, dtype):
     """(pointer, row stride) of a [..., columns] view whose leading axes have one common stride."""
     if t is None:
@@ -649,8 +643,10 @@ def dit_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, *, dx=None, dw_gate=
     """Gradient of dit_gated_ffn_forward from the gate and up that it kept.  Each
     of dx, dw_gate, dw_up (of the inputs' type) and dbias_gate, dbias_up (float32
     [hidden]) is overwritten where given."""
-    if _grad_mode_of(gate, up, dout):
-        _refuse_autograd()
+    if gate.requires_grad or up.requires_grad or dout.requires_grad:
+        _torch or _use_torch()
+        if _grad_mode():
+            _refuse_autograd()
     args = _ffn_args(x, w_gate, w_up, dout, gate, up, act, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dbias_gate=dbias_gate,
                      dbias_up=dbias_up)
     L, s = lib(), _raw_stream(x, stream)

@@ -131,7 +131,7 @@ def test_gated_ffn_workspace(L):
     assert bytes_of(x_s=0) == 64 * 32 * 2                                          # one row for all: no matrix for the copies
     assert bytes_of(width=33, x_s=40, wg_s=40, wu_s=33) == 48 * 40 * 2
     assert bytes_of(**F8) == 0 and bytes_of(x_s=40, **F8) == 64 * 32
-    assert bytes_of(1, **BWD) == 64 * 48 * 2 * 2 + 2 * 2 * 48 * 4
+    assert bytes_of(1, **BWD) == 64 * 48 * 2 * 2 + 4 * 2 * 48 * 4
     assert bytes_of(1, **{**BWD, "dbg": 0, "dbu": 0}) == 64 * 48 * 2 * 2
     assert bytes_of(rows=64, width=8192, hidden=256) > 0                           # K split, sums joined in fp32
     assert bytes_of(hidden=0) == -1 and bytes_of(1, bg=64, **BWD) == -1
