@@ -16,7 +16,8 @@ cudaError_t by_type(int dtype, const Norm& p, int mode, int64_t blocks, cudaStre
 }  // namespace
 
 int64_t rms_norm_workspace(const dit_rms_norm_args& a) {
-  return a.dweight && a.batch * a.tokens ? blocks_of(a, true) * a.channels * (int64_t)sizeof(float) : 0;
+  // whole rows take more blocks
+  return a.dweight && a.batch * a.tokens ? blocks_of(a, true, true) * a.channels * (int64_t)sizeof(float) : 0;
 }
 
 cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* workspace, cudaStream_t s) {
@@ -36,17 +37,15 @@ cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* works
   p.aligned = (aligned(p.x, p.sx, esz, 16) ? AL_X : 0) | (aligned(p.res, p.sres, esz, 16) ? AL_RES : 0) |
               (aligned(p.total, p.stotal, esz, 16) ? AL_TOTAL : 0) | (aligned(p.dy, p.sdy, esz, 16) ? AL_DY : 0) |
               (aligned(p.out, p.sout, out_esz, out_bytes) ? AL_OUT : 0) | (((uintptr_t)a.weight & 15) == 0 ? AL_W : 0);
-  p.words = (aligned(p.x, p.sx, esz, 4) ? AL_X : 0) | (aligned(p.res, p.sres, esz, 4) ? AL_RES : 0) |
-            (aligned(p.total, p.stotal, esz, 4) ? AL_TOTAL : 0) | (aligned(p.dy, p.sdy, esz, 4) ? AL_DY : 0) |
-            (aligned(p.out, p.sout, out_esz, 4) ? AL_OUT : 0);
   p.scale = a.scale, p.w = a.weight;
   p.rows = (uint32_t)rows, p.tokens = (uint32_t)a.tokens;
   p.C = a.channels, p.eps = a.eps;
+  const bool whole = whole_rows(p, 16 / esz);
   if (!backward) {
-    const int64_t blocks = blocks_of(a, false);
+    const int64_t blocks = blocks_of(a, false, whole);
     return by_type(a.dtype, p, a.out_dtype == DIT_DTYPE_E4M3 ? E4M3 : SAME, blocks, s);
   }
-  const int64_t blocks = blocks_of(a, true);
+  const int64_t blocks = blocks_of(a, true, whole);
   p.partial = a.dweight ? workspace : nullptr;
   const cudaError_t e = by_type(a.dtype, p, GRAD, blocks, s);
   if (e != cudaSuccess || !a.dweight) return e;

@@ -36,7 +36,6 @@ struct Norm {
   int C;
   float eps;
   int aligned;     // AL_*: 16-byte rows (AL_OUT of e4m3: 8-byte rows for chunks of 8, 4 for 4)
-  int words;       // AL_*: rows of 4-byte words at least
 };
 
 // max(a, |b|, |c|), NaN if one of them is
@@ -202,29 +201,30 @@ DIT_DEV float warp_max1(float v) {
   return v;
 }
 
-// Asynchronous copies of `bytes` <= N bytes, zeros behind them.
+// Asynchronous copy of 16 bytes, of which `bytes` are there, zeros behind them.
 DIT_DEV void copy_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-DIT_DEV void copy_async4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 DIT_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 DIT_DEV void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-constexpr int kRingRows = 4, kRingStages = 2;
-// RW warps hold a row, NV chunks of 16 bytes a thread.
-template <int RW, int NV, int MODE, bool RES>
+constexpr int kRingStages = 2;
+// RW warps hold a row, NV chunks of 16 bytes a thread; ROWS rows a block.
+template <int RW, int NV, int ROWS, int MODE, bool RES, bool WHOLE>
 struct Ring {
   static constexpr int INPUTS = (MODE == GRAD ? 2 : 1) + (RES ? 1 : 0);
-  static constexpr int ROW = RW * NV * 512;  // bytes
-  static constexpr int STAGE = INPUTS * ROW;
-  static constexpr int SMEM = kRingRows * kRingStages * STAGE;
+  static constexpr int ROW = RW * NV * 512;            // bytes
+  static constexpr int SLOT = ROW + (WHOLE ? 0 : 16);  // a row that begins inside a vector
+  static constexpr int STAGE = INPUTS * SLOT;
+  static constexpr int SMEM = ROWS * kRingStages * STAGE;
 };
 // Blocks of a ring kernel that an SM holds (registers allow them too: launch bounds).
-constexpr int ring_blocks(int rw, int nv, int inputs) {
-  const int n = (227 << 10) / (kRingRows * kRingStages * inputs * rw * nv * 512 + 1024), most = 8 / rw > 4 ? 4 : 8 / rw;
+// The gradient of rows that are not whole keeps them in registers: half as many warps.
+constexpr int ring_blocks(int rw, int nv, int rows, int inputs, bool half) {
+  const int n = (227 << 10) / (rows * kRingStages * inputs * (rw * nv * 512 + 16) + 1024);
+  int most = (nv >= 4 || rw == 1 || half ? 16 : 32) / (rw * rows);
+  if (most < 1) most = 1;
   return n > most ? most : n;
 }
 
@@ -235,61 +235,98 @@ DIT_DEV void row_sync() {
   else named_bar_sync(1 + threadIdx.x / (32 * RW), 32 * RW);
 }
 
-// The channels of a row into a slot of shared memory, zeros up to its last chunk's
-// end.  Rows of 16-byte vectors: each lane fetches what it reads; else any lane any word.
-template <typename T, int RW, int NV>
-DIT_DEV void fetch_row(uint8_t* slot, const T* row, int C, bool aligned, bool words) {
-  const int lane = threadIdx.x & (32 * RW - 1), bytes = C * (int)sizeof(T);
-  const uint8_t* src = reinterpret_cast<const uint8_t*>(row);
+// A row of 16-byte vectors into a slot of shared memory, zeros up to its last chunk's
+// end: each thread fetches the chunks that it reads.
+template <int RW, int NV>
+DIT_DEV void fetch_vectors(uint8_t* slot, const uint8_t* src, int bytes) {
+  const int lane = threadIdx.x & (32 * RW - 1);
   const uint32_t dst = smem_u32(slot);
-  if (aligned) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = (lane + 32 * RW * i) * 16;
-      if (at < bytes) copy_async16(dst + at, src + at, min(16, bytes - at));
-    }
-    return;
+  for (int i = 0; i < NV; ++i) {
+    const int at = (lane + 32 * RW * i) * 16;
+    if (at < bytes) copy_async16(dst + at, src + at, min(16, bytes - at));
   }
-  const int end = (bytes + 15) & ~15;
-  if (words) {
-    for (int at = lane * 4; at < end; at += 128 * RW) {
-      const int n = max(0, min(4, bytes - at));
-      copy_async4(dst + at, n ? src + at : src, n);
-    }
-    return;
-  }
-  for (int at = lane * 2; at < end; at += 64 * RW)
-    *reinterpret_cast<uint16_t*>(slot + at) = at < bytes ? *reinterpret_cast<const uint16_t*>(src + at) : (uint16_t)0;
 }
-// A row that every lane has written to a slot, out to global memory in words or elements.
-template <typename T, int RW>
-DIT_DEV void put_row(T* row, const uint8_t* slot, int C, bool words) {
-  const int lane = threadIdx.x & (32 * RW - 1), bytes = C * (int)sizeof(T);
-  uint8_t* dst = reinterpret_cast<uint8_t*>(row);
-  row_sync<RW>();
-  if (words) {
-    for (int at = lane * 4; at + 4 <= bytes; at += 128 * RW) *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(slot + at);
-    if (lane == 0 && (bytes & 2)) *reinterpret_cast<uint16_t*>(dst + bytes - 2) = *reinterpret_cast<const uint16_t*>(slot + bytes - 2);
-  } else {
-    for (int at = lane * 2; at < bytes; at += 64 * RW) *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(slot + at);
+// A row of any alignment into a slot, at the place in its first vector that it has in
+// memory: the vectors between its ends by asynchronous copies, each byte of the
+// vectors that it shares with its neighbours by a load of its own, which is put into
+// the slot when the row's turn comes.  (Copies of 4 and loads of 2 bytes for the whole
+// row took 234 us for 68311 rows of 1535 bf16 channels, 326 us for the gradient.)
+struct Edge {
+  uint32_t value;
+  int at;  // byte of the slot, -1: none
+};
+template <int RW>
+DIT_DEV Edge fetch_bytes(uint8_t* slot, const uint8_t* src, int bytes) {
+  const int lane = threadIdx.x & (32 * RW - 1), o = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+  const uint8_t* base = src - o;
+  const int first = o ? 1 : 0, end = (o + bytes) >> 4;
+  const uint32_t dst = smem_u32(slot);
+  for (int v = first + lane; v < end; v += 32 * RW) copy_async16(dst + v * 16, base + v * 16, 16);
+  Edge e{0, -1};
+  if (o && lane < min(16 - o, bytes)) e.at = o + lane;
+  const int tail = max(first, end) * 16;  // a row inside one vector has no tail
+  if (lane >= 16 && lane - 16 < o + bytes - tail && lane < 32) e.at = tail + lane - 16;
+  if (e.at >= 0) e.value = base[e.at];
+  return e;
+}
+// 16 bytes from byte at + s of a slot on (at a multiple of 16, s < 16 the same for the row).
+DIT_DEV uint4 window(const uint8_t* slot, int at, int s) {
+  const uint4 a = *reinterpret_cast<const uint4*>(slot + at);
+  if (s == 0) return a;
+  const uint4 b = *reinterpret_cast<const uint4*>(slot + at + 16);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (s & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
   }
-  row_sync<RW>();
+  if (s & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int bits = (s & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+// The first n elements of a chunk, zeros behind them.
+template <typename T>
+DIT_DEV uint4 first_of(uint4 r, int n) {
+  constexpr int E = 16 / sizeof(T);
+  if (n >= E) return r;
+  uint32_t* w = &r.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) w[j] = j < n ? w[j] : 0u;
+    else w[j] = 2 * j + 1 < n ? w[j] : 2 * j < n ? w[j] & 0xffffu : 0u;
+  }
+  return r;
+}
+// A row that lies from a slot's begin on, out to memory of any alignment.
+template <int RW>
+DIT_DEV void put_bytes(uint8_t* dst, const uint8_t* slot, int bytes) {
+  const int lane = threadIdx.x & (32 * RW - 1), o = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
+  uint8_t* base = dst - o;
+  const int first = o ? 1 : 0, end = (o + bytes) >> 4;
+  for (int v = first + lane; v < end; v += 32 * RW) *reinterpret_cast<uint4*>(base + v * 16) = window(slot, (v - first) * 16, (16 - o) & 15);
+  int at = -1;
+  if (o && lane < min(16 - o, bytes)) at = o + lane;
+  const int tail = max(first, end) * 16;
+  if (lane >= 16 && lane - 16 < o + bytes - tail && lane < 32) at = tail + lane - 16;
+  if (at >= 0) base[at] = slot[at - o];
 }
 
 // RW warps a row, NV chunks of 16 bytes a thread: chunk lane + 32 RW i.  WHOLE: a weight,
 // every tensor in rows of whole 16-byte vectors (no branch is left in a row then, and
 // its loads are issued together: the video gradient 90 us without it).
-template <typename T, int RW, int NV, int MODE, bool RES, bool WHOLE>
-__global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<RW, NV, MODE, RES>::INPUTS)) norm_ring_kernel(const Norm a) {
-  constexpr int E = 16 / sizeof(T);
-  constexpr int ALL = WHOLE ? ~0 : 0;
-  const int aligned = a.aligned | ALL;
-  constexpr int TPR = 32 * RW;
-  using R = Ring<RW, NV, MODE, RES>;
+template <typename T, int RW, int NV, int ROWS, int MODE, bool RES, bool WHOLE>
+__global__ void __launch_bounds__(32 * RW * ROWS, ring_blocks(RW, NV, ROWS, Ring<RW, NV, ROWS, MODE, RES, WHOLE>::INPUTS, MODE == GRAD && !WHOLE))
+    norm_ring_kernel(const Norm a) {
+  constexpr int E = 16 / sizeof(T), TPR = 32 * RW;
+  using R = Ring<RW, NV, ROWS, MODE, RES, WHOLE>;
   extern __shared__ uint4 ring_smem[];  // the ring; of several warps a row, their sums behind it
   const int lane = threadIdx.x & (TPR - 1), mine_row = threadIdx.x / TPR;
   uint8_t* const mine = reinterpret_cast<uint8_t*>(ring_smem) + mine_row * kRingStages * R::STAGE;
-  const uint32_t step = gridDim.x * kRingRows;
+  const uint32_t step = gridDim.x * ROWS;
   float2* const parts = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ring_smem) + R::SMEM) + mine_row * 2 * RW;
   int turn = 0;
   auto row_sum = [&](float2 v) {
@@ -316,65 +353,105 @@ __global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<
     }
     return v;
   };
-  const int C = a.C;
+  const int C = a.C, bytes = C * (int)sizeof(T);
   const float inv_c = 1.f / (float)C;
   auto offset = [&](uint32_t row, const int64_t (&s)[2]) {
     const uint32_t b = row / a.tokens;
     return (int64_t)b * s[0] + (int64_t)(row - b * a.tokens) * s[1];
   };
+  // inputs 0: x, then dy, then residual; where each row begins in its first vector
+  constexpr int RESIDUAL = R::INPUTS - 1;
+  Edge edge[R::INPUTS], next_edge[R::INPUTS];
+  int begin[R::INPUTS], next_begin[R::INPUTS];
+#pragma unroll
+  for (int i = 0; i < R::INPUTS; ++i) edge[i].at = next_edge[i].at = -1, begin[i] = next_begin[i] = 0;
+  auto fetch_one = [&](int i, uint8_t* slot, const T* p, int flag) {
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(p);
+    if (WHOLE || (a.aligned & flag)) {
+      fetch_vectors<RW, NV>(slot + i * R::SLOT, src, bytes);
+    } else {
+      next_edge[i] = fetch_bytes<RW>(slot + i * R::SLOT, src, bytes);
+      next_begin[i] = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+    }
+  };
   auto fetch = [&](int stage, uint32_t row) {
     uint8_t* slot = mine + stage * R::STAGE;
-    fetch_row<T, RW, NV>(slot, static_cast<const T*>(a.x) + offset(row, a.sx), C, aligned & AL_X, a.words & AL_X);
-    if constexpr (MODE == GRAD)
-      fetch_row<T, RW, NV>(slot + R::ROW, static_cast<const T*>(a.dy) + offset(row, a.sdy), C, aligned & AL_DY, a.words & AL_DY);
-    if constexpr (RES)
-      fetch_row<T, RW, NV>(slot + (R::INPUTS - 1) * R::ROW, static_cast<const T*>(a.res) + offset(row, a.sres), C,
-                       aligned & AL_RES, a.words & AL_RES);
+    fetch_one(0, slot, static_cast<const T*>(a.x) + offset(row, a.sx), AL_X);
+    if constexpr (MODE == GRAD) fetch_one(1, slot, static_cast<const T*>(a.dy) + offset(row, a.sdy), AL_DY);
+    if constexpr (RES) fetch_one(RESIDUAL, slot, static_cast<const T*>(a.res) + offset(row, a.sres), AL_RES);
   };
   Pairs<T> dw[MODE == GRAD ? NV : 1] = {};
-  uint32_t row = blockIdx.x * kRingRows + mine_row;
+  uint32_t row = blockIdx.x * ROWS + mine_row;
   if (row < a.rows) fetch(0, row);
   copy_commit();
   int stage = 0;
   for (; row < a.rows; row += step, stage ^= 1) {
+    uint8_t* const slot = mine + stage * R::STAGE;
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < R::INPUTS; ++i) edge[i] = next_edge[i], begin[i] = next_begin[i];
+    }
     const bool more = step < a.rows - row;
     if (more) fetch(stage ^ 1, row + step);
     copy_commit();
     copy_wait<1>();
-    if constexpr (!WHOLE) row_sync<RW>();  // WHOLE: a thread reads what it has fetched
-    uint8_t* const slot = mine + stage * R::STAGE;
-    uint8_t* const res_slot = slot + (R::INPUTS - 1) * R::ROW;
-    auto chunk = [&](uint8_t* s, int i) -> uint4& { return *reinterpret_cast<uint4*>(s + (lane + TPR * i) * 16); };
+    if constexpr (!WHOLE) {  // (WHOLE: a thread reads what it has fetched)
+#pragma unroll
+      for (int i = 0; i < R::INPUTS; ++i)
+        if (edge[i].at >= 0) slot[i * R::SLOT + edge[i].at] = (uint8_t)edge[i].value;
+      row_sync<RW>();
+    }
+    // the chunk of channels c .. c + n of an input's row
+    auto chunk = [&](int input, int i, int n) {
+      const uint8_t* s = slot + input * R::SLOT;
+      const int at = (lane + TPR * i) * 16;
+      if constexpr (WHOLE) return *reinterpret_cast<const uint4*>(s + at);
+      else return first_of<T>(window(s, at, begin[input]), n);
+    };
+    // results that are not stored as vectors go out through a slot, from its begin on
+    auto put = [&](int input, int i) -> uint4& { return *reinterpret_cast<uint4*>(slot + input * R::SLOT + (lane + TPR * i) * 16); };
+    const bool direct = WHOLE || (a.aligned & AL_OUT);
     if constexpr (MODE == GRAD) {
       float2 square = make_float2(0.f, 0.f), dot = square;
+      uint4 x_held[WHOLE ? 1 : NV], dy_held[WHOLE ? 1 : NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
-        const Pairs<T> v = pairs<T>(chunk(slot, i));
-        Pairs<T> g = pairs<T>(chunk(slot + R::ROW, i));
-        times_weight<T, WHOLE>(g, a.w, c, n, aligned & AL_W);
+        const uint4 x_raw = chunk(0, i, n), dy_raw = chunk(1, i, n);
+        if constexpr (!WHOLE) x_held[i] = x_raw, dy_held[i] = dy_raw;
+        const Pairs<T> v = pairs<T>(x_raw);
+        Pairs<T> g = pairs<T>(dy_raw);
+        times_weight<T, WHOLE>(g, a.w, c, n, a.aligned & AL_W);
         add_products<T>(square, v, v);
         add_products<T>(dot, g, v);
       }
       const float2 sums = row_sum(make_float2(square.x + square.y, dot.x + dot.y));
       const float r = rsqrtf(fmaf(sums.x, inv_c, a.eps)), k = r * r * (sums.y * inv_c);
       T* out = static_cast<T*>(a.out) + offset(row, a.sout);
-      const bool direct = aligned & AL_OUT;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
-        const Pairs<T> v = pairs<T>(chunk(slot, i)), g = pairs<T>(chunk(slot + R::ROW, i));
+        const Pairs<T> v = pairs<T>(WHOLE ? chunk(0, i, n) : x_held[WHOLE ? 0 : i]);
+        const Pairs<T> g = pairs<T>(WHOLE ? chunk(1, i, n) : dy_held[WHOLE ? 0 : i]);
         Pairs<T> d = g;
-        times_weight<T, WHOLE>(d, a.w, c, n, aligned & AL_W);
+        times_weight<T, WHOLE>(d, a.w, c, n, a.aligned & AL_W);
         norm_gradient<T>(g, d, v, r, k, dw[i]);
-        if constexpr (RES) add_to<T>(d, pairs<T>(chunk(res_slot, i)));
-        // a lane's chunk of the slot is read by it alone
+        if constexpr (RES) add_to<T>(d, pairs<T>(chunk(RESIDUAL, i, n)));
         if (direct) store_chunk<T, WHOLE>(out + c, n, true, packed<T>(d));
-        else chunk(res_slot, i) = packed<T>(d);
+        else x_held[WHOLE ? 0 : i] = packed<T>(d);
       }
-      if (!direct) put_row<T, RW>(out, res_slot, C, a.words & AL_OUT);
+      if constexpr (!WHOLE) {
+        if (!direct) {
+          row_sync<RW>();  // the row's windows have been read
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if ((lane + TPR * i) * E < C) put(0, i) = x_held[i];
+          row_sync<RW>();
+          put_bytes<RW>(reinterpret_cast<uint8_t*>(out), slot, bytes);
+        }
+      }
     } else {
       Pairs<T> v[NV];
       float2 square = make_float2(0.f, 0.f);
@@ -383,28 +460,35 @@ __global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         v[i] = Pairs<T>{};
         if (n <= 0) continue;
-        v[i] = pairs<T>(chunk(slot, i));
+        v[i] = pairs<T>(chunk(0, i, n));
         if constexpr (RES) {
-          add_to<T>(v[i], pairs<T>(chunk(res_slot, i)));
+          add_to<T>(v[i], pairs<T>(chunk(RESIDUAL, i, n)));
           const uint4 sum = packed<T>(v[i]);
           v[i] = pairs<T>(sum);  // the norm is of the sum as it is kept
-          if (a.total) {
-            if (aligned & AL_TOTAL) store_chunk<T, WHOLE>(static_cast<T*>(a.total) + offset(row, a.stotal) + c, n, true, sum);
-            else chunk(slot, i) = sum;
-          }
+          if (a.total && (a.aligned & AL_TOTAL)) store_chunk<T, WHOLE>(static_cast<T*>(a.total) + offset(row, a.stotal) + c, n, true, sum);
         }
         add_products<T>(square, v[i], v[i]);
       }
-      if constexpr (RES)
-        if (a.total && !(aligned & AL_TOTAL)) put_row<T, RW>(static_cast<T*>(a.total) + offset(row, a.stotal), slot, C, a.words & AL_TOTAL);
       const float r = rsqrtf(fmaf(row_sum(make_float2(square.x + square.y, 0.f)).x, inv_c, a.eps));
+      const bool put_total = RES && a.total && !(a.aligned & AL_TOTAL);
+      if (put_total || !direct) {
+        row_sync<RW>();  // the row's windows have been read
+        if (put_total) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if ((lane + TPR * i) * E < C) put(0, i) = packed<T>(v[i]);  // exact: v is of the type
+          row_sync<RW>();
+          put_bytes<RW>(reinterpret_cast<uint8_t*>(static_cast<T*>(a.total) + offset(row, a.stotal)), slot, bytes);
+          if (RESIDUAL == 0) row_sync<RW>();
+        }
+      }
       float factor = r, top = 0.f;
       bool finite = true;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
-        times_weight<T, WHOLE>(v[i], a.w, c, n, aligned & AL_W);
+        times_weight<T, WHOLE>(v[i], a.w, c, n, a.aligned & AL_W);
         if constexpr (MODE == E4M3)
 #pragma unroll
           for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[i][j]);
@@ -416,17 +500,26 @@ __global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<
       }
       T* out = static_cast<T*>(a.out) + offset(row, a.sout);
       uint8_t* out8 = static_cast<uint8_t*>(a.out) + offset(row, a.sout);
-      const bool direct = aligned & AL_OUT;
+      uint8_t* const out_slot = slot + RESIDUAL * R::SLOT;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
         scale_by<T>(v[i], factor);
-        if constexpr (MODE == E4M3) store_e4m3<T, WHOLE>(out8 + c, n, direct, finite ? v[i] : Pairs<T>{});
-        else if (direct) store_chunk<T, WHOLE>(out + c, n, true, packed<T>(v[i]));
-        else chunk(res_slot, i) = packed<T>(v[i]);
+        if constexpr (MODE == E4M3) {
+          const Pairs<T> q = finite ? v[i] : Pairs<T>{};
+          if (direct) store_e4m3<T, WHOLE>(out8 + c, n, true, q);
+          else store_e4m3<T, true>(out_slot + c, E, true, q);
+        } else if (direct) {
+          store_chunk<T, WHOLE>(out + c, n, true, packed<T>(v[i]));
+        } else {
+          put(RESIDUAL, i) = packed<T>(v[i]);
+        }
       }
-      if (MODE == SAME && !direct) put_row<T, RW>(out, res_slot, C, a.words & AL_OUT);
+      if (!direct) {
+        row_sync<RW>();
+        put_bytes<RW>(MODE == E4M3 ? out8 : reinterpret_cast<uint8_t*>(out), out_slot, MODE == E4M3 ? C : bytes);
+      }
     }
     if constexpr (!WHOLE) row_sync<RW>();  // the slot may be filled again
     if (!more) break;  // row + step may pass 32 bits
@@ -438,18 +531,122 @@ __global__ void __launch_bounds__(32 * RW * kRingRows, ring_blocks(RW, NV, Ring<
     __syncthreads();
     float* join = reinterpret_cast<float*>(ring_smem);  // [row][channel]
     constexpr int WIDTH = NV * TPR * E;
-    static_assert(kRingRows * WIDTH * 4 <= R::SMEM, "room for the join");
+    static_assert(ROWS * WIDTH * 4 <= R::SMEM, "room for the join");
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < E / 2; j += 2)
         *reinterpret_cast<float4*>(join + mine_row * WIDTH + (lane + TPR * i) * E + 2 * j) = make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
     __syncthreads();
-    for (int c = threadIdx.x; c < C; c += TPR * kRingRows) {
+    for (int c = threadIdx.x; c < C; c += TPR * ROWS) {
       float s = join[c];
 #pragma unroll
-      for (int g = 1; g < kRingRows; ++g) s += join[g * WIDTH + c];
+      for (int g = 1; g < ROWS; ++g) s += join[g * WIDTH + c];
       a.partial[(int64_t)blockIdx.x * C + c] = s;
+    }
+  }
+}
+
+// Narrow rows: LPR lanes hold a row, a chunk each, 32 / LPR rows a warp, kNarrowBatch
+// of such groups of rows under way at once.  (A warp a row took 375 us for 1.6 M rows
+// of 64 bf16 channels, 493 us for the gradient.)
+constexpr int kNarrowWarps = 4, kNarrowBatch = 4;
+template <typename T, int LPR, int MODE>
+__global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const Norm a) {
+  constexpr int E = 16 / sizeof(T), RPW = 32 / LPR, U = kNarrowBatch;
+  __shared__ float join[MODE == GRAD ? kNarrowWarps : 1][LPR * E];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = (lane % LPR) * E, n = a.C - c;
+  const float inv_c = 1.f / (float)a.C;
+  Pairs<T> w, dw = {};
+#pragma unroll
+  for (int j = 0; j < Pairs<T>::N; ++j) w[j] = make_float2(1.f, 1.f);
+  times_weight<T, false>(w, a.w, c, n, false);
+  auto row_sum = [](float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  const int64_t step = (int64_t)gridDim.x * kNarrowWarps * RPW * U;
+  for (int64_t base = ((int64_t)blockIdx.x * kNarrowWarps + warp) * RPW * U; base < a.rows; base += step) {
+    uint4 x[U], res[U], dy[MODE == GRAD ? U : 1];
+    uint32_t b[U], t[U];
+    bool there[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = base + u * RPW + lane / LPR;
+      there[u] = row < a.rows && n > 0;
+      b[u] = (uint32_t)row / a.tokens, t[u] = (uint32_t)row - b[u] * a.tokens;
+      x[u] = res[u] = make_uint4(0, 0, 0, 0);
+      if constexpr (MODE == GRAD) dy[u] = make_uint4(0, 0, 0, 0);
+      if (!there[u]) continue;
+      x[u] = load_chunk<T, false>(static_cast<const T*>(a.x) + b[u] * a.sx[0] + t[u] * a.sx[1] + c, n, a.aligned & AL_X);
+      if (a.res) res[u] = load_chunk<T, false>(static_cast<const T*>(a.res) + b[u] * a.sres[0] + t[u] * a.sres[1] + c, n, a.aligned & AL_RES);
+      if constexpr (MODE == GRAD) dy[u] = load_chunk<T, false>(static_cast<const T*>(a.dy) + b[u] * a.sdy[0] + t[u] * a.sdy[1] + c, n, a.aligned & AL_DY);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Pairs<T> v = pairs<T>(x[u]);
+      const int64_t at_out = b[u] * a.sout[0] + t[u] * a.sout[1] + c;
+      float2 square = make_float2(0.f, 0.f);
+      if constexpr (MODE == GRAD) {
+        const Pairs<T> g = pairs<T>(dy[u]);
+        Pairs<T> d = g;
+        float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < Pairs<T>::N; ++j) d[j] = fmul2(d[j], w[j]);
+        add_products<T>(square, v, v);
+        add_products<T>(dot, d, v);
+        const float r = rsqrtf(fmaf(row_sum(square.x + square.y), inv_c, a.eps)), k = r * r * (row_sum(dot.x + dot.y) * inv_c);
+        if (!there[u]) continue;
+        norm_gradient<T>(g, d, v, r, k, dw);
+        if (a.res) add_to<T>(d, pairs<T>(res[u]));
+        store_chunk<T, false>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(d));
+      } else {
+        if (a.res) {
+          add_to<T>(v, pairs<T>(res[u]));
+          const uint4 sum = packed<T>(v);
+          v = pairs<T>(sum);  // the norm is of the sum as it is kept
+          if (a.total && there[u]) store_chunk<T, false>(static_cast<T*>(a.total) + b[u] * a.stotal[0] + t[u] * a.stotal[1] + c, n, a.aligned & AL_TOTAL, sum);
+        }
+        add_products<T>(square, v, v);
+        const float r = rsqrtf(fmaf(row_sum(square.x + square.y), inv_c, a.eps));
+#pragma unroll
+        for (int j = 0; j < Pairs<T>::N; ++j) v[j] = fmul2(v[j], w[j]);
+        if constexpr (MODE == E4M3) {
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[j]);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const RowScale q = row_scale(top, r);
+          if (!there[u]) continue;
+          if (c == 0) a.scale[base + u * RPW + lane / LPR] = q.scale;
+          scale_by<T>(v, q.factor);
+          store_e4m3<T, false>(static_cast<uint8_t*>(a.out) + at_out, n, a.aligned & AL_OUT, q.finite ? v : Pairs<T>{});
+        } else {
+          if (!there[u]) continue;
+          scale_by<T>(v, r);
+          store_chunk<T, false>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(v));
+        }
+      }
+    }
+  }
+  if constexpr (MODE == GRAD) {
+    if (!a.partial) return;
+#pragma unroll
+    for (int j = 0; j < Pairs<T>::N; ++j) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1)
+        dw[j] = fadd2(dw[j], make_float2(__shfl_xor_sync(0xffffffffu, dw[j].x, o), __shfl_xor_sync(0xffffffffu, dw[j].y, o)));
+      if (lane < LPR) join[warp][c + 2 * j] = dw[j].x, join[warp][c + 2 * j + 1] = dw[j].y;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.C; i += 32 * kNarrowWarps) {
+      float s = join[0][i];
+#pragma unroll
+      for (int g = 1; g < kNarrowWarps; ++g) s += join[g][i];
+      a.partial[(int64_t)blockIdx.x * a.C + i] = s;
     }
   }
 }
@@ -604,48 +801,65 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W) norm_kernel(
 constexpr int64_t kSerialRows = 256;
 constexpr int kNormSms = 152;
 
-inline int chunks_of(const dit_rms_norm_args& a) { return (a.channels + (a.dtype == DIT_DTYPE_F32 ? 3 : 7)) / (a.dtype == DIT_DTYPE_F32 ? 4 : 8); }
-// Warps a row and chunks a thread of a ring kernel; none: a block holds a row in registers.
-struct Width {
-  int rw, nv;
+inline int chunks_of(int C, int esz) { return (C * esz + 15) / 16; }
+// How rows of so many chunks are held: narrow (lanes a row), a ring (warps a row, chunks
+// a thread, rows a block), or, fp32 rows past 8192 channels, the registers of a block.
+struct Shape {
+  int lanes, rw, nv, rows;
 };
-inline Width ring_width(int chunks) {
-  for (const Width w : {Width{1, 1}, {1, 2}, {2, 2}, {2, 3}, {4, 2}, {4, 4}})
+inline Shape shape_of(int chunks) {
+  for (const int lanes : {1, 4, 8, 16})
+    if (chunks <= lanes) return {lanes, 0, 0, kNarrowWarps * 32 / lanes};
+  for (const Shape w : {Shape{0, 1, 1, 4}, {0, 1, 2, 4}, {0, 2, 2, 4}, {0, 2, 3, 4}, {0, 4, 2, 4}, {0, 4, 4, 4}, {0, 8, 4, 1}, {0, 16, 4, 1}})
     if (chunks <= 32 * w.rw * w.nv) return w;
-  return {0, 0};
+  return {0, 0, 0, 1};
 }
 // Blocks: what the card holds at once; of the gradient enough that no strand is longer than kSerialRows.
-inline int64_t blocks_of(const dit_rms_norm_args& a, bool backward) {
-  const Width w = ring_width(chunks_of(a));
-  const int64_t rows = a.batch * a.tokens, group = w.rw ? kRingRows : 1, most = (rows + group - 1) / group;
-  int64_t n = kNormSms * (w.rw ? ring_blocks(w.rw, w.nv, 1 + (backward ? 1 : 0) + (a.residual ? 1 : 0)) : backward ? 2 : 64);
-  const int64_t least = (rows + group * kSerialRows - 1) / (group * kSerialRows);
+inline int64_t blocks_of(const dit_rms_norm_args& a, bool backward, bool whole) {
+  const Shape w = shape_of(chunks_of(a.channels, a.dtype == DIT_DTYPE_F32 ? 4 : 2));
+  const int64_t rows = a.batch * a.tokens, at_once = w.rows * (w.lanes ? kNarrowBatch : 1), most = (rows + at_once - 1) / at_once;
+  int64_t n = kNormSms * (w.lanes ? (backward ? 8 : 32) : w.rw ? ring_blocks(w.rw, w.nv, w.rows, 1 + (backward ? 1 : 0) + (a.residual ? 1 : 0), backward && !whole) : backward ? 2 : 64);
+  const int64_t least = (rows + w.rows * kSerialRows - 1) / (w.rows * kSerialRows);
   if (backward && n < least) n = least;
   return n < most ? n : most;
 }
 
-template <typename T, int RW, int NV, int MODE, bool RES, bool WHOLE>
+template <typename T, int RW, int NV, int ROWS, int MODE, bool RES, bool WHOLE>
 cudaError_t launch_ring(const Norm& p, int64_t blocks, cudaStream_t s) {
-  return launch_kernel(norm_ring_kernel<T, RW, NV, MODE, RES, WHOLE>, dim3((unsigned)blocks), dim3(32 * RW * kRingRows),
-                       Ring<RW, NV, MODE, RES>::SMEM + kRingRows * 2 * RW * sizeof(float2), s, 1, false, p);
+  return launch_kernel(norm_ring_kernel<T, RW, NV, ROWS, MODE, RES, WHOLE>, dim3((unsigned)blocks), dim3(32 * RW * ROWS),
+                       Ring<RW, NV, ROWS, MODE, RES, WHOLE>::SMEM + ROWS * 2 * RW * sizeof(float2), s, 1, false, p);
 }
-template <typename T, int RW, int NV, int MODE>
+template <typename T, int RW, int NV, int ROWS, int MODE>
 cudaError_t ring(const Norm& p, bool whole, int64_t blocks, cudaStream_t s) {
   if constexpr (MODE == GRAD)
-    if (whole) return p.res ? launch_ring<T, RW, NV, MODE, true, true>(p, blocks, s) : launch_ring<T, RW, NV, MODE, false, true>(p, blocks, s);
-  return p.res ? launch_ring<T, RW, NV, MODE, true, false>(p, blocks, s) : launch_ring<T, RW, NV, MODE, false, false>(p, blocks, s);
+    if (whole) return p.res ? launch_ring<T, RW, NV, ROWS, MODE, true, true>(p, blocks, s) : launch_ring<T, RW, NV, ROWS, MODE, false, true>(p, blocks, s);
+  return p.res ? launch_ring<T, RW, NV, ROWS, MODE, true, false>(p, blocks, s) : launch_ring<T, RW, NV, ROWS, MODE, false, false>(p, blocks, s);
+}
+template <typename T, int LPR, int MODE>
+cudaError_t narrow(const Norm& p, int64_t blocks, cudaStream_t s) {
+  return launch_kernel(norm_narrow_kernel<T, LPR, MODE>, dim3((unsigned)blocks), dim3(32 * kNarrowWarps), 0, s, 1, false, p);
 }
 template <typename T, int W, int NV, int MODE, bool WHOLE>
 cudaError_t launch_rows(const Norm& p, int64_t blocks, cudaStream_t s) {
   if (W == 1) blocks = (p.rows + kRowWarps - 1) / kRowWarps;
   return launch_kernel(norm_kernel<T, W, NV, MODE, WHOLE>, dim3((unsigned)blocks), dim3(W == 1 ? 32 * kRowWarps : 32 * W), 0, s, 1, false, p);
 }
+// Whether every tensor lies in rows of whole 16-byte vectors, and there is a weight.
+inline bool whole_rows(const Norm& p, int E) {
+  const int need = AL_X | AL_OUT | AL_W | (p.res ? AL_RES : 0) | (p.total ? AL_TOTAL : 0) | (p.dy ? AL_DY : 0);
+  return (p.aligned & need) == need && p.C % E == 0 && p.w;
+}
+// Whole rows of a forward call are held in registers, without copies (the video pair
+// 112 us, 129 us through the ring; e4m3 54 and 75); all others go through the ring.
 template <typename T, int MODE>
 cudaError_t by_width(const Norm& p, int64_t blocks, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  const int chunks = (p.C + E - 1) / E;
-  const int need = AL_X | AL_OUT | AL_W | (p.res ? AL_RES : 0) | (p.total ? AL_TOTAL : 0) | (MODE == GRAD ? AL_DY : 0);
-  const bool whole = (p.aligned & need) == need && p.C % E == 0 && p.w;
+  const int chunks = chunks_of(p.C, sizeof(T));
+  const bool whole = whole_rows(p, E);
+  if (chunks <= 1) return narrow<T, 1, MODE>(p, blocks, s);
+  if (chunks <= 4) return narrow<T, 4, MODE>(p, blocks, s);
+  if (chunks <= 8) return narrow<T, 8, MODE>(p, blocks, s);
+  if (chunks <= 16) return narrow<T, 16, MODE>(p, blocks, s);
   if constexpr (MODE != GRAD) {
     if (whole) {
       if (chunks <= 32) return launch_rows<T, 1, 1, MODE, true>(p, blocks, s);
@@ -660,14 +874,14 @@ cudaError_t by_width(const Norm& p, int64_t blocks, cudaStream_t s) {
       if constexpr (E == 4) return launch_rows<T, 32, 4, MODE, true>(p, blocks, s);
     }
   }
-  if (chunks <= 32) return ring<T, 1, 1, MODE>(p, whole, blocks, s);
-  if (chunks <= 64) return ring<T, 1, 2, MODE>(p, whole, blocks, s);
-  if (chunks <= 128) return ring<T, 2, 2, MODE>(p, whole, blocks, s);
-  if (chunks <= 192) return ring<T, 2, 3, MODE>(p, whole, blocks, s);
-  if (chunks <= 256) return ring<T, 4, 2, MODE>(p, whole, blocks, s);
-  if (chunks <= 512) return ring<T, 4, 4, MODE>(p, whole, blocks, s);
-  if (chunks <= 1024) return launch_rows<T, 8, 4, MODE, false>(p, blocks, s);
-  if (chunks <= 2048) return launch_rows<T, 16, 4, MODE, false>(p, blocks, s);
+  if (chunks <= 32) return ring<T, 1, 1, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 64) return ring<T, 1, 2, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 128) return ring<T, 2, 2, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 192) return ring<T, 2, 3, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 256) return ring<T, 4, 2, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 512) return ring<T, 4, 4, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 1024) return ring<T, 8, 4, 1, MODE>(p, whole, blocks, s);
+  if (chunks <= 2048) return ring<T, 16, 4, 1, MODE>(p, whole, blocks, s);
   if constexpr (E == 4) return launch_rows<T, 32, 4, MODE, false>(p, blocks, s);
   return cudaErrorInvalidValue;
 }

@@ -90,6 +90,8 @@ NORM_CASES = [
     ("bf16", (1, 29, 2056), True, True, 0), ("f32", (1, 29, 2050), True, True, 0), ("f16", (1, 23, 4096), True, True, 8),
     ("bf16", (1, 21, 5000), False, True, 1), ("f32", (1, 11, 8192), True, True, 0), ("bf16", (2, 5, 16384), True, True, 0),
     ("f32", (1, 5, 16384), True, True, 0), ("f16", (1, 5, 16383), True, False, 0), ("bf16", (5000, 1, 64), True, True, 0),
+    ("bf16", (3, 77, 100), True, True, 1), ("f32", (2, 501, 13), True, True, 0), ("f16", (1, 999, 24), False, False, 1),
+    ("bf16", (1, 9, 8200), True, True, 1), ("f32", (1, 13, 4099), True, True, 1), ("f16", (2, 11, 700), True, False, 3),
 ]
 
 
