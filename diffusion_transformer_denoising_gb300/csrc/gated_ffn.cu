@@ -222,14 +222,36 @@ DIT_DEV void store_unit(const Product& P, int o, uint8_t* stg, int64_t row0, int
     return;
   }
   __syncwarp();
-  uint16_t* out = static_cast<uint16_t*>(P.out[o]);
-  const int c = col0 + 2 * lane;
+  // Rows of any alignment.
+  uint16_t* out = static_cast<uint16_t*>(P.out[o]) + row0 * P.ldo[o] + col0;
+  const int rows = (int)min((int64_t)32, P.M - row0);
+  if (col0 + 64 <= P.N) {
+    // Eight lanes a row: the aligned vectors inside the row's 128 bytes, each out of two
+    // chunks; then the elements at its ends, eight lanes a row too: 16 stores a lane.
+    const int k = lane & 7;
+    auto chunk = [&](int r, int j) { return *reinterpret_cast<const uint4*>(stg + r * 128 + ((j ^ (r & 7)) << 4)); };
+#pragma unroll 2
+    for (int r = lane >> 3; r < rows; r += 4) {
+      uint16_t* row = out + r * P.ldo[o];
+      const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2;  // elements before the first vector
+      const uint4 v = chunk(r, k);
+      if (lead == 0) {
+        *reinterpret_cast<uint4*>(row + 8 * k) = v;
+        continue;
+      }
+      if (k < 7) *reinterpret_cast<uint4*>(row + lead + 8 * k) = shift16(v, chunk(r, k + 1), 2 * lead);
+      const int c = k < lead ? k : 56 + k;  // the ends' elements: [0, lead) and [lead + 56, 64)
+      row[c] = *reinterpret_cast<const uint16_t*>(stg + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+    }
+  } else {
+    const int c = 2 * lane;
 #pragma unroll 4
-  for (int r = 0; r < 32 && row0 + r < P.M; ++r) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-    uint16_t* at = out + (row0 + r) * P.ldo[o] + c;
-    if (c < P.N) at[0] = (uint16_t)w;
-    if (c + 1 < P.N) at[1] = (uint16_t)(w >> 16);
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+      uint16_t* at = out + r * P.ldo[o] + c;
+      if (col0 + c < P.N) at[0] = (uint16_t)w;
+      if (col0 + c + 1 < P.N) at[1] = (uint16_t)(w >> 16);
+    }
   }
   __syncwarp();
 }
@@ -578,13 +600,13 @@ DIT_DEV uint4 piece(const uint8_t* row, int k, int D) {
     if (k < D) return __ldg(reinterpret_cast<const uint4*>(row + k * (16 / E)));
     return make_uint4(0, 0, 0, 0);
   }
+  if constexpr (F8) return k < D ? load16(row, k, D) : make_uint4(0, 0, 0, 0);
+  // eight loads of 2 bytes: 92 us for 20 rows x 4095 x 8191, 104 by shifted vectors
+  // (of e4m3, sixteen loads of a byte: 97 us, by shifted vectors 61)
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    if (k + j >= D) continue;
-    if constexpr (F8) w[j / 4] |= (uint32_t)__ldg(row + k + j) << (8 * (j & 3));
-    else w[j / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + k + j) << (16 * (j & 1));
-  }
+  for (int j = 0; j < E; ++j)
+    if (k + j < D) w[(j / 2) & 3] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + k + j) << (16 * (j & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 DIT_DEV uint32_t widen(uint32_t two_e4m3) {
@@ -618,7 +640,7 @@ DIT_DEV void products(float (&c)[4], const uint4& lo, const uint4& hi, const uin
 // NT: groups of 8 tokens.  F16: the output's type, and of 16-bit operands theirs.
 template <bool F8, bool F16, int NT, bool WHOLE, int ACT>
 __global__ void __launch_bounds__(32 * kFewWarps, 4) few_rows_kernel(const Few a) {
-  constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 ? 2 : 4;
+  constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 || (F8 && !WHOLE) ? 2 : 4;
   __shared__ float sums[2][kFewWarps][NT][16][9];
   wait_previous();
   start_next();
@@ -776,10 +798,13 @@ __global__ void __launch_bounds__(256) pack_kernel(const Pack a) {
   if (!a.src[o]) return;
   const E* src = reinterpret_cast<const E*>(a.src[o]);
   E* dst = reinterpret_cast<E*>(a.dst[o]);
-  // a warp per row
+  // a warp per row, a vector a lane; the pitch is one of whole vectors
+  constexpr int PER = 16 / sizeof(E);
   const int lane = threadIdx.x & 31;
   for (int64_t r = (blockIdx.x * 256ll + threadIdx.x) >> 5; r < a.rows[o]; r += gridDim.x * 8ll)
-    for (int c = lane; c < a.width; c += 32) dst[r * a.pitch + c] = src[r * a.src_stride[o] + c];
+#pragma unroll 4
+    for (int c = lane * PER; c < a.width; c += 32 * PER)
+      *reinterpret_cast<uint4*>(dst + r * a.pitch + c) = load16(src + r * a.src_stride[o], c, a.width);
 }
 
 // ---------------------------------------------------------------- gradients of gate and up
@@ -795,6 +820,7 @@ struct Slopes {
 
 // Eight values at p, of which n are there (zeros behind them).  ALIGN: bytes that rows
 // and addresses are multiples of; at 16 and 4 the number of values is a multiple too.
+// (Shifted vectors at the alignment of 2 took the odd case's slopes 14 us, these 8.)
 template <int ALIGN>
 DIT_DEV uint4 load8(const uint16_t* p, int n) {
   if constexpr (ALIGN == 16) {

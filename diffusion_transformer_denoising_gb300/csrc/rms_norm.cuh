@@ -273,20 +273,7 @@ DIT_DEV Edge fetch_bytes(uint8_t* slot, const uint8_t* src, int bytes) {
 // 16 bytes from byte at + s of a slot on (at a multiple of 16, s < 16 the same for the row).
 DIT_DEV uint4 window(const uint8_t* slot, int at, int s) {
   const uint4 a = *reinterpret_cast<const uint4*>(slot + at);
-  if (s == 0) return a;
-  const uint4 b = *reinterpret_cast<const uint4*>(slot + at + 16);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (s & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (s & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const int bits = (s & 3) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                    __funnelshift_r(w[3], w[4], bits));
+  return s == 0 ? a : shift16(a, *reinterpret_cast<const uint4*>(slot + at + 16), s);
 }
 // The first n elements of a chunk, zeros behind them.
 template <typename T>

@@ -138,4 +138,40 @@ DIT_DEV void store_f32_stream(T* p, const float (&f)[N]) {
   store_f32<T, N, true>(p, f);
 }
 
+// Bytes s .. s + 15 of 32 (s < 16).
+DIT_DEV uint4 shift16(const uint4& a, const uint4& b, int s) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+  const int bits = (s & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+// 16 bytes of a row of n elements (1 or 2 bytes each) from element k on, zeros behind its
+// end, at any alignment: out of the two aligned vectors around them as far as these lie
+// inside the row (loads without a branch, so that several calls' are under way at
+// once), element by element at its ends.
+template <typename E>
+DIT_DEV uint4 load16(const E* row, int64_t k, int64_t n) {
+  constexpr int PER = 16 / sizeof(E);
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(row + k);
+  const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  const int64_t from = k * (int64_t)sizeof(E) - s, bytes = n * (int64_t)sizeof(E);
+  const bool low = from >= 0 && from + 16 <= bytes, high = s != 0 && from + 32 <= bytes;
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (low) a = __ldg(reinterpret_cast<const uint4*>(p - s));
+  if (high) b = __ldg(reinterpret_cast<const uint4*>(p - s + 16));
+  uint4 v = shift16(a, b, s);
+  if (!low || (s != 0 && !high)) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (k + j < n) w[j * sizeof(E) / 4] |= (uint32_t)__ldg(row + k + j) << (8 * (j * sizeof(E) % 4));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
 }  // namespace dit
