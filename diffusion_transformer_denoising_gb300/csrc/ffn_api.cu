@@ -9,6 +9,7 @@
 
 #include "operator_checks.h"
 #include "operators.h"
+#include "tmap.h"
 
 using namespace dit;
 
@@ -215,7 +216,7 @@ dit_status grad_norm_call(const dit_grad_tensor* t, int64_t n, float max_norm, f
   // anything else but the gradient that it takes the place of
   struct Range {
     uintptr_t begin, end;
-    int64_t tensor;  // -1: norm, workspace
+    const char* what;
     bool output;
   };
   std::vector<Range> ranges;
@@ -230,11 +231,11 @@ dit_status grad_norm_call(const dit_grad_tensor* t, int64_t n, float max_norm, f
       return fail(DIT_ERR_INVALID_ARG, "tensor %lld is not aligned to its type", (long long)i);
     const uintptr_t g = (uintptr_t)t[i].grad, o = (uintptr_t)t[i].out;
     const int64_t bytes = t[i].numel * elem;
-    ranges.push_back({g, g + bytes, i, o == g});
-    if (o && o != g) ranges.push_back({o, o + bytes, i, true});
+    ranges.push_back({g, g + bytes, "grad", o == g});
+    if (o && o != g) ranges.push_back({o, o + bytes, "out", true});
   }
-  ranges.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, -1, true});
-  ranges.push_back({(uintptr_t)ws, (uintptr_t)ws + need, -1, true});
+  ranges.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, "norm", true});
+  ranges.push_back({(uintptr_t)ws, (uintptr_t)ws + need, "workspace", true});
   std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
   uintptr_t any_end = 0, out_end = 0;  // furthest end of the ranges before, and of the outputs among them
   for (const Range& r : ranges) {
@@ -243,14 +244,15 @@ dit_status grad_norm_call(const dit_grad_tensor* t, int64_t n, float max_norm, f
     any_end = std::max(any_end, r.end);
     if (r.output) out_end = std::max(out_end, r.end);
   }
-  // Neighbours in one allocation are the common case: the owner is asked for once per range all the same.
-  for (int64_t i = 0; i < n; ++i) {
-    if (t[i].numel == 0) continue;
-    DIT_TRY(dev.add("grad", t[i].grad));
-    if (t[i].out != t[i].grad) DIT_TRY(dev.add("out", t[i].out));
+  // The owner of each allocation is looked up once for all ranges that begin in it (a
+  // lookup for each of a model's hundreds of tensors took longer than the kernels).
+  uintptr_t base = 0;
+  size_t size = 0;
+  for (const Range& r : ranges) {
+    if (r.begin - base < size) continue;
+    DIT_TRY(dev.add(r.what, reinterpret_cast<const void*>(r.begin)));
+    if (!allocation_of(reinterpret_cast<const void*>(r.begin), &base, &size)) size = 0;
   }
-  DIT_TRY(dev.add("norm", norm));
-  DIT_TRY(dev.add("workspace", ws));
   DIT_TRY(dev.enter());
   CU_TRY(grad_norm_run(t, n, max_norm, norm, ws, stream));
   return DIT_OK;

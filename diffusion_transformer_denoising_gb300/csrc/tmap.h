@@ -39,6 +39,23 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
+// The allocation that a device pointer lies in; false where the driver cannot say.
+inline bool allocation_of(const void* p, uintptr_t* base, size_t* size) {
+  static PFN_cuMemGetAddressRange_v3020 fn = nullptr;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &f, 3020, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(f);
+  }
+  CUdeviceptr at = 0;
+  if (fn(&at, size, (CUdeviceptr)(uintptr_t)p) != CUDA_SUCCESS) return false;
+  *base = (uintptr_t)at;
+  return true;
+}
+
 // Tensor of rank 2 or 3, dims innermost first, 128-byte swizzle unless told
 // otherwise, out-of-bounds elements read as zero.  Returns false if the driver
 // rejects it (base not 16-byte aligned, stride not a multiple of 16 bytes, a

@@ -8,7 +8,9 @@ raises instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
+import operator
 import os
 import struct
 
@@ -678,33 +680,38 @@ def dit_gated_ffn_synchronize(stream=None):
     _check(lib().dit_gated_ffn_synchronize(_stream(stream)))
 
 
+_dtype_of, _requires_grad_of = operator.attrgetter("dtype"), operator.attrgetter("requires_grad")
+
+
 def _grad_tensors(grads, clipped):
     """The packed dit_grad_tensors of the entries that are not None, and their number."""
     T = (_torch or _use_torch()).Tensor
     live = [g for g in grads if g is not None]
     # whole lists at a time: a model has hundreds of gradients
-    codes, sizes = [_dtype_codes.get(g.dtype) for g in live], list(map(T.numel, live))
+    dtypes, sizes, pointers = list(map(_dtype_of, live)), list(map(T.numel, live)), list(map(T.data_ptr, live))
+    codes = list(map(_dtype_codes.get, dtypes))
     if None in codes:
-        _refuse(DIT_ERR_INVALID_ARG, f"a gradient is {live[codes.index(None)].dtype}")
+        _refuse(DIT_ERR_INVALID_ARG, f"a gradient is {dtypes[codes.index(None)]}")
     if not all(map(T.is_contiguous, live)):
         _refuse(DIT_ERR_SHAPE, "gradients must be contiguous")
-    if _grad_mode() and any([g.requires_grad for g in live]):
+    if _grad_mode() and any(map(_requires_grad_of, live)):
         _refuse_autograd()
-    pointers = list(map(T.data_ptr, live))
+    n = len(live)
     if clipped is None:
-        outs = [0] * len(live)
+        outs = [0] * n
     elif clipped is grads:
         outs = pointers
     else:
         made = [c for c in clipped if c is not None]
-        if (len(clipped) != len(grads) or len(made) != len(live) or list(map(T.numel, made)) != sizes or
-                [_dtype_codes.get(c.dtype) for c in made] != codes or not all(map(T.is_contiguous, made))):
+        if (len(clipped) != len(grads) or len(made) != n or list(map(T.numel, made)) != sizes or
+                list(map(_dtype_of, made)) != dtypes or not all(map(T.is_contiguous, made))):
             _refuse(DIT_ERR_SHAPE, "clipped must hold a contiguous tensor of the size and type of each gradient")
         outs = list(map(T.data_ptr, made))
-    n = len(live)
-    fields = [0] * (4 * n)
-    fields[0::4], fields[1::4], fields[2::4], fields[3::4] = pointers, outs, sizes, codes
-    return struct.pack("<" + n * "2Q2q", *fields), n  # the type and the reserved field as one number
+    # structures of four 64-bit fields (the type and the reserved field as one)
+    fields = array.array("q", bytes(32 * n))
+    for i, column in enumerate((pointers, outs, sizes, codes)):
+        fields[i::4] = array.array("q", column)
+    return fields.tobytes(), n
 
 
 def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, stream=None):
