@@ -16,8 +16,13 @@ cudaError_t by_type(int dtype, const Norm& p, int mode, int64_t blocks, cudaStre
 }  // namespace
 
 int64_t rms_norm_workspace(const dit_rms_norm_args& a) {
-  // whole rows take more blocks
-  return a.dweight && a.batch * a.tokens ? blocks_of(a, true, true) * a.channels * (int64_t)sizeof(float) : 0;
+  if (!a.dweight || a.batch * a.tokens == 0) return 0;
+  int64_t most = 0;  // enough for rows of any alignment
+  for (const Rows kind : {WHOLE_ROWS, ALIGNED_ROWS, ODD_ROWS}) {
+    const int64_t n = blocks_of(a, true, kind);
+    most = n > most ? n : most;
+  }
+  return most * a.channels * (int64_t)sizeof(float);
 }
 
 cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* workspace, cudaStream_t s) {
@@ -40,12 +45,12 @@ cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* works
   p.scale = a.scale, p.w = a.weight;
   p.rows = (uint32_t)rows, p.tokens = (uint32_t)a.tokens;
   p.C = a.channels, p.eps = a.eps;
-  const bool whole = whole_rows(p, 16 / esz);
+  const Rows kind = rows_kind(p, 16 / esz);
   if (!backward) {
-    const int64_t blocks = blocks_of(a, false, whole);
+    const int64_t blocks = blocks_of(a, false, kind);
     return by_type(a.dtype, p, a.out_dtype == DIT_DTYPE_E4M3 ? E4M3 : SAME, blocks, s);
   }
-  const int64_t blocks = blocks_of(a, true, whole);
+  const int64_t blocks = blocks_of(a, true, kind);
   p.partial = a.dweight ? workspace : nullptr;
   const cudaError_t e = by_type(a.dtype, p, GRAD, blocks, s);
   if (e != cudaSuccess || !a.dweight) return e;

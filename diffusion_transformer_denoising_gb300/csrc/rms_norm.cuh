@@ -223,7 +223,7 @@ struct Ring {
 // The gradient of rows that are not whole keeps them in registers: half as many warps.
 constexpr int ring_blocks(int rw, int nv, int rows, int inputs, bool half) {
   const int n = (227 << 10) / (rows * kRingStages * inputs * (rw * nv * 512 + 16) + 1024);
-  int most = (nv >= 4 || rw == 1 || half ? 16 : 32) / (rw * rows);
+  int most = (nv >= 4 || (rw == 1 && nv > 1) || (half && nv > 1) ? 16 : 32) / (rw * rows);
   if (most < 1) most = 1;
   return n > most ? most : n;
 }
@@ -794,18 +794,26 @@ inline int chunks_of(int C, int esz) { return (C * esz + 15) / 16; }
 struct Shape {
   int lanes, rw, nv, rows;
 };
-inline Shape shape_of(int chunks) {
+// WHOLE: every tensor lies in rows of whole 16-byte vectors, and there is a weight;
+// ALIGNED: rows that begin at such vectors; ODD: any.
+enum Rows { WHOLE_ROWS, ALIGNED_ROWS, ODD_ROWS };
+// Odd rows of more than 20 chunks fare better with shifted windows (411206 rows of 255
+// bf16 channels 268 us, 457 element by element; of 130, 17 chunks, 513 and 475).
+inline Shape shape_of(int chunks, Rows kind) {
   for (const int lanes : {1, 4, 8, 16, 32})
-    if (chunks <= lanes) return {lanes, 0, 0, kNarrowWarps * 32 / lanes};
-  for (const Shape w : {Shape{0, 1, 2, 4}, {0, 2, 2, 4}, {0, 2, 3, 4}, {0, 4, 2, 4}, {0, 4, 4, 4}, {0, 8, 4, 1}, {0, 16, 4, 1}})
+    if (chunks <= lanes && (kind != ODD_ROWS || chunks <= 20)) return {lanes, 0, 0, kNarrowWarps * 32 / lanes};
+  for (const Shape w : {Shape{0, 1, 1, 4}, {0, 1, 2, 4}, {0, 2, 2, 4}, {0, 2, 3, 4}, {0, 4, 2, 4}, {0, 4, 4, 4}, {0, 8, 4, 1}, {0, 16, 4, 1}})
     if (chunks <= 32 * w.rw * w.nv) return w;
   return {0, 0, 0, 1};
 }
 // Blocks: what the card holds at once; of the gradient enough that no strand is longer than kSerialRows.
-inline int64_t blocks_of(const dit_rms_norm_args& a, bool backward, bool whole) {
-  const Shape w = shape_of(chunks_of(a.channels, a.dtype == DIT_DTYPE_F32 ? 4 : 2));
+inline int64_t blocks_of(const dit_rms_norm_args& a, bool backward, Rows kind) {
+  const Shape w = shape_of(chunks_of(a.channels, a.dtype == DIT_DTYPE_F32 ? 4 : 2), kind);
   const int64_t rows = a.batch * a.tokens, at_once = w.rows * (w.lanes ? kNarrowBatch : 1), most = (rows + at_once - 1) / at_once;
-  int64_t n = kNormSms * (w.lanes ? (backward ? 8 : 32) : w.rw ? ring_blocks(w.rw, w.nv, w.rows, 1 + (backward ? 1 : 0) + (a.residual ? 1 : 0), backward && !whole) : backward ? 2 : 64);
+  int64_t n = kNormSms * (w.lanes ? (backward ? 8 : 32) : w.rw ? ring_blocks(w.rw, w.nv, w.rows, 1 + (backward ? 1 : 0) + (a.residual ? 1 : 0), backward && kind != WHOLE_ROWS) : backward ? 2 : 64);
+  // the forward's last blocks wait less for each other when there are more of them
+  // (204800 odd rows of 512 172 us, 205 with one for each place)
+  if (!backward && w.rw) n *= 4;
   const int64_t least = (rows + w.rows * kSerialRows - 1) / (w.rows * kSerialRows);
   if (backward && n < least) n = least;
   return n < most ? n : most;
@@ -831,10 +839,10 @@ cudaError_t launch_rows(const Norm& p, int64_t blocks, cudaStream_t s) {
   if (W == 1) blocks = (p.rows + kRowWarps - 1) / kRowWarps;
   return launch_kernel(norm_kernel<T, W, NV, MODE, WHOLE>, dim3((unsigned)blocks), dim3(W == 1 ? 32 * kRowWarps : 32 * W), 0, s, 1, false, p);
 }
-// Whether every tensor lies in rows of whole 16-byte vectors, and there is a weight.
-inline bool whole_rows(const Norm& p, int E) {
-  const int need = AL_X | AL_OUT | AL_W | (p.res ? AL_RES : 0) | (p.total ? AL_TOTAL : 0) | (p.dy ? AL_DY : 0);
-  return (p.aligned & need) == need && p.C % E == 0 && p.w;
+inline Rows rows_kind(const Norm& p, int E) {
+  const int need = AL_X | AL_OUT | (p.res ? AL_RES : 0) | (p.total ? AL_TOTAL : 0) | (p.dy ? AL_DY : 0);
+  if ((p.aligned & need) != need) return ODD_ROWS;
+  return (p.aligned & AL_W) && p.C % E == 0 && p.w ? WHOLE_ROWS : ALIGNED_ROWS;
 }
 // Whole rows of a forward call are held in registers, without copies (the video pair
 // 112 us, 129 us through the ring; e4m3 54 and 75); all others go through the ring.
@@ -842,12 +850,14 @@ template <typename T, int MODE>
 cudaError_t by_width(const Norm& p, int64_t blocks, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   const int chunks = chunks_of(p.C, sizeof(T));
-  const bool whole = whole_rows(p, E);
+  const Rows kind = rows_kind(p, E);
+  const bool whole = kind == WHOLE_ROWS;
   if (chunks <= 1) return narrow<T, 1, MODE>(p, blocks, s);
   if (chunks <= 4) return narrow<T, 4, MODE>(p, blocks, s);
   if (chunks <= 8) return narrow<T, 8, MODE>(p, blocks, s);
   if (chunks <= 16) return narrow<T, 16, MODE>(p, blocks, s);
-  if (chunks <= 32) return narrow<T, 32, MODE>(p, blocks, s);
+  if (chunks <= (kind == ODD_ROWS ? 20 : 32)) return narrow<T, 32, MODE>(p, blocks, s);
+  if (chunks <= 32) return ring<T, 1, 1, 4, MODE>(p, false, blocks, s);
   if constexpr (MODE != GRAD) {
     if (whole) {
       // warps a row: 51200 rows of 2048 in e4m3 109 us on four, 136 on one; 68266 of 1536
