@@ -169,6 +169,48 @@ def test_rms_norm_in_place(C, pad):
         assert torch.equal(v[k], dx) and torch.equal(dw, dw2), k
 
 
+@pytest.mark.parametrize("dtype,C", [("bf16", 100), ("f16", 255), ("bf16", 768), ("f32", 1001), ("bf16", 1535), ("f16", 2056), ("bf16", 5000)])
+@pytest.mark.parametrize("pads", [(0, 1, 3, 8), (1, 0, 8, 3), (8, 8, 1, 0)], ids=str)
+def test_rms_norm_tensors_of_different_alignment(dtype, C, pads):
+    rng = np.random.default_rng(C + pads[0])
+    shape, w = (2, 19, C), torch.from_numpy(1 + 0.3 * rng.standard_normal(C)).float().cuda()
+    x, res = padded(rng, shape, dtype, pads[0]), padded(rng, shape, dtype, pads[1])
+    total, out = padded(rng, shape, dtype, pads[2], fill=False), padded(rng, shape, dtype, pads[3], fill=False)
+    dit.dit_rms_norm_forward(x, out, residual=res, total=total, weight=w)
+    near(total, n64(x) + n64(res), ULP * (np.abs(n64(x)) + np.abs(n64(res))), "total")
+    ref = O.rms_norm_forward(n64(total), n64(w))
+    near(out, ref, NSTEPS * ULP * np.abs(ref), "out")
+    q, scale = torch.empty((2, 19, C + pads[0]), dtype=E4M3, device="cuda")[..., pads[0]:], nans((2, 19), torch.float32)
+    total8 = padded(rng, shape, dtype, pads[3], fill=False)
+    dit.dit_rms_norm_forward(x, q, residual=res, total=total8, weight=w, scale=scale)
+    assert torch.equal(total8, total)
+    s = O.e4m3_scale(ref)
+    near(scale, s, NSTEPS * ULP * s, "scale")
+    near(q, ref / s[..., None], NSTEPS * ULP * np.abs(ref / s[..., None]), "e4m3")
+    dy, dx, dw = padded(rng, shape, dtype, pads[3]), padded(rng, shape, dtype, pads[1], fill=False), nans((C,), torch.float32)
+    dit.dit_rms_norm_backward(total, dy, dx, dtotal=x, weight=w, dweight=dw)
+    rdx, rdw = O.rms_norm_backward(n64(total), n64(dy), n64(w), 1e-6, n64(x))
+    r, tn = norm_scale(n64(total), None, 1e-6)
+    g = np.abs(n64(dy) * n64(w))
+    near(dx, rdx, NSTEPS * ULP * (r * (g + tn * np.mean(g * tn, -1, keepdims=True)) + np.abs(n64(x))), "dx")
+    near(dw, rdw, (NSTEPS + 38) * ULP * np.sum(np.abs(n64(dy)) * tn, (0, 1)), "dweight")
+
+
+@pytest.mark.parametrize("C", [30, 255, 1001, 2056, 5000])
+def test_rms_norm_leaves_what_lies_around_its_rows_alone(C):
+    rng = np.random.default_rng(C)
+    for pad in (1, 3, 8):
+        big = [torch.full((2, 9, C + pad + 16), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        view = [b[:, 1:-1, 5:5 + C] if pad != 8 else b[:, 1:-1, 8:8 + C] for b in big]
+        x, res = randn(rng, (2, 7, C), "bf16"), randn(rng, (2, 7, C), "bf16")
+        dit.dit_rms_norm_forward(x, view[0], residual=res, total=view[1])
+        dit.dit_rms_norm_backward(x, res, view[2])
+        for b, v in zip(big, view):
+            assert not (v == 7).all()
+            v.fill_(7.0)
+            assert (b == 7).all()
+
+
 def test_rms_norm_shared_inputs_and_shapes():
     # an input expanded over batch and tokens; one, two and four axes
     rng = np.random.default_rng(3)
@@ -298,6 +340,8 @@ FFN_CASES = [
     ("f16", 70, 2050, 30, "gelu", False, "odd"),
     ("bf16", 2600, 256, 1280, "silu", False, "plain"),   # pairs of CTAs, several tiles each
     ("bf16", 1111, 136, 2100, "gelu", True, "plain"),
+    ("bf16", 40, 64, 4096, "silu", True, "plain"),       # the gradients' K split: of dx,
+    ("f16", 3000, 64, 72, "gelu", True, "plain"),        # and of dW
 ]
 
 
@@ -739,6 +783,44 @@ def test_graphs_streams_and_repeated_calls_give_the_same_bits(M, side):
         for k in OUTPUTS:
             assert torch.equal(bits(t[k]), bits(ref[0][k])), k
     dit.dit_gated_ffn_synchronize()
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """No call needs one outside of a capture before it."""
+    code = """
+import torch
+from diffusion_transformer_denoising_gb300 import dit
+def go(out):
+    M, D, F = 300, 512, 768
+    r = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda") * 0.125
+    x, wg, wu, dout = r(1, M, D), r(F, D), r(F, D), r(1, M, F)
+    e = torch.empty_like
+    total, y, h, gate, up, dy, dx, dwg, dwu = e(x), e(x), e(dout), e(dout), e(dout), e(x), e(x), e(wg), e(wu)
+    w, dw, norm = torch.ones(D, device="cuda"), torch.empty(D, device="cuda"), torch.empty((), device="cuda")
+    def step():
+        dit.dit_rms_norm_forward(x, y, residual=x, total=total, weight=w)
+        dit.dit_gated_ffn_forward(y, wg, wu, h, gate=gate, up=up)
+        dit.dit_gated_ffn_backward(y, wg, wu, gate, up, dout, dx=dy, dw_gate=dwg, dw_up=dwu)
+        dit.dit_rms_norm_backward(total, dy, dx, weight=w, dweight=dw)
+        dit.dit_grad_norm([dwg, dwu, dw], norm, max_norm=0.5)
+    torch.cuda.synchronize()
+    if out:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        g.replay()
+    else:
+        step()
+    torch.cuda.synchronize()
+    return [v.double().sum().item() for v in (h, dx, dwg, dwu, dw, norm)]
+a = go(True)
+assert a == go(False), a
+print("same")
+"""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
 
 
 def test_host_threads_call_at_once():
