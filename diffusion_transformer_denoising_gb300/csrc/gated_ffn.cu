@@ -15,6 +15,19 @@
 // memory: x and W rows in the forward, W rows across in dx, both operands across
 // in dW.  Those tiles are loaded as they lie (64 channels x 64 K rows, 128-byte
 // swizzle) and the MMA reads them MN-major, so nothing is transposed.
+//
+// What bounds it: the tensor cores, under the power cap in longer runs.  Measured on
+// one GB300, 1536 x 8960 (device time of single launches): 32760 rows 940 to 960 us =
+// 1.9 PFLOP/s (1090 us = 1.65 in a row of calls, 0.97 of the sustained peak); from
+// e4m3 530 to 550 us = 3.3 PFLOP/s; gradient of 8190 rows: slopes 125 us (HBM), dx 261 us and dW
+// 252 us = 1.75 PFLOP/s.  One row 10 us, 0.81 of the copy bandwidth.
+//
+// Measured slower: dx and dW as one launch, so that the tiles of one fill the last
+// round of the other (568 us instead of 549 back to back: under the power cap idle SMs
+// cost nothing, and the mix reads more from DRAM); tensor memory drained 16 columns
+// at a time with the next ones on their way (e4m3 648 us, 578 at the time), or a
+// whole unit at once (826 us, spilled); column groups narrower than the
+// matrix (bf16 966 to 1057 us, 945 to 980 at the time).
 #include <math.h>
 
 #include "column_sums.cuh"
@@ -61,7 +74,7 @@ struct Product {
   CUtensorMap a[2], b[2], c[3];
   void* out[3];
   int64_t ldo[3];
-  int tma[3];           // output by tensor stores; else element by element
+  int tma[3];           // output by tensor stores; else by plain ones
   float* partial;       // splits > 1: fp32 planes [problem][split][gate, up][M][ldp]
   int64_t ldp, plane;
   const float *x_scale, *scale[2], *bias[2];

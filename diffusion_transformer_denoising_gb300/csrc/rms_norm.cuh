@@ -6,10 +6,18 @@
 // Gradient: g = dy w, dx = dtotal + r (g - v r^2 mean(g v)), dw = sum dy v r: the two
 // row sums (v^2 and g v) are taken together.
 //
-// What bounds it: HBM.  Every row is read once and written once.  Up to 2048 channels
-// of 16 bits (1024 of 32) a warp takes a row, out of a ring of its own in shared
-// memory that asynchronous copies fill: while it works on a row the next one is on
-// its way, whatever the registers hold.  Wider rows are held in the registers of a block.
+// What bounds it: HBM.  Every row is read once and written once.  A forward row of
+// whole 16-byte vectors is held in registers, by 1 to 16 warps.  The gradient holds
+// two or three tensors' rows and the weight's sums, too much for enough warps, so its
+// rows come through a ring in shared memory that asynchronous copies fill: while a
+// row is worked on the next is on its way, whatever the registers hold.  So do rows
+// of any other alignment, which are read and written through shifted windows.  Narrow
+// rows share a warp.
+//
+// Measured on one GB300 (bf16, 1536 channels, device time): 2 x 32760 rows with a
+// residual 112 us = 7.2 TB/s; 32760 into e4m3 54 us = 6.5 TB/s; their gradient 66 us =
+// 6.1 TB/s and 5 us for the weight's sums.  68311 odd rows of 1535: 173 us (floor 124),
+// gradient 240 (124).
 #pragma once
 #include <math.h>
 
@@ -220,10 +228,12 @@ struct Ring {
   static constexpr int SMEM = ROWS * kRingStages * STAGE;
 };
 // Blocks of a ring kernel that an SM holds (registers allow them too: launch bounds).
-// The gradient of rows that are not whole keeps them in registers: half as many warps.
-constexpr int ring_blocks(int rw, int nv, int rows, int inputs, bool half) {
+// `held`: the gradient of rows that are not whole keeps them in registers, and fewer
+// warps have room (with 24 of them, three chunks a thread spilled: 317 us instead of
+// 240 for 68311 rows of 1535 bf16 channels; two gain: 180 and 197 us for 52376 of 1001 in fp32).
+constexpr int ring_blocks(int rw, int nv, int rows, int inputs, bool held) {
   const int n = (227 << 10) / (rows * kRingStages * inputs * (rw * nv * 512 + 16) + 1024);
-  int most = (nv >= 4 || (rw == 1 && nv > 1) || (half && nv > 1) ? 16 : 32) / (rw * rows);
+  int most = (nv >= 4 || (rw == 1 && nv > 1) || (held && nv == 3) ? 16 : held && nv > 1 ? 24 : 32) / (rw * rows);
   if (most < 1) most = 1;
   return n > most ? most : n;
 }
@@ -802,7 +812,7 @@ enum Rows { WHOLE_ROWS, ALIGNED_ROWS, ODD_ROWS };
 inline Shape shape_of(int chunks, Rows kind) {
   for (const int lanes : {1, 4, 8, 16, 32})
     if (chunks <= lanes && (kind != ODD_ROWS || chunks <= 20)) return {lanes, 0, 0, kNarrowWarps * 32 / lanes};
-  for (const Shape w : {Shape{0, 1, 1, 4}, {0, 1, 2, 4}, {0, 2, 2, 4}, {0, 2, 3, 4}, {0, 4, 2, 4}, {0, 4, 4, 4}, {0, 8, 4, 1}, {0, 16, 4, 1}})
+  for (const Shape w : {Shape{0, 1, 1, 4}, {0, 1, 2, 4}, {0, 2, 2, 4}, {0, 2, 3, 4}, {0, 4, 2, 2}, {0, 4, 4, 2}, {0, 8, 4, 1}, {0, 16, 4, 1}})
     if (chunks <= 32 * w.rw * w.nv) return w;
   return {0, 0, 0, 1};
 }
@@ -878,8 +888,8 @@ cudaError_t by_width(const Norm& p, int64_t blocks, cudaStream_t s) {
   if (chunks <= 64) return ring<T, 1, 2, 4, MODE>(p, whole, blocks, s);
   if (chunks <= 128) return ring<T, 2, 2, 4, MODE>(p, whole, blocks, s);
   if (chunks <= 192) return ring<T, 2, 3, 4, MODE>(p, whole, blocks, s);
-  if (chunks <= 256) return ring<T, 4, 2, 4, MODE>(p, whole, blocks, s);
-  if (chunks <= 512) return ring<T, 4, 4, 4, MODE>(p, whole, blocks, s);
+  if (chunks <= 256) return ring<T, 4, 2, 2, MODE>(p, whole, blocks, s);
+  if (chunks <= 512) return ring<T, 4, 4, 2, MODE>(p, whole, blocks, s);
   if (chunks <= 1024) return ring<T, 8, 4, 1, MODE>(p, whole, blocks, s);
   if (chunks <= 2048) return ring<T, 16, 4, 1, MODE>(p, whole, blocks, s);
   if constexpr (E == 4) return launch_rows<T, 32, 4, MODE, false>(p, blocks, s);

@@ -366,7 +366,8 @@ int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backwar
  * max |y| / 448 (1 for a row of zeros), out = y / scale rounded to nearest even.
  * Such a row with a NaN or an infinity in it gets the scale NaN and zeros.  The
  * outputs total and out may be the very view of x or of residual (out only in
- * the type of x).  Arithmetic is fp32. */
+ * the type of x).  Arithmetic is fp32, the squares' sum too: a row with values
+ * of 1e19 and more counts as one of infinite norm, its y is 0. */
 enum { DIT_RMS_NORM_MAX_CHANNELS = 16384 };
 typedef struct {
   int64_t batch;
@@ -408,8 +409,9 @@ int64_t dit_rms_norm_workspace_bytes(const dit_rms_norm_args* a);
  * dtype) of x and the weights.  With operand_dtype DIT_DTYPE_E4M3, x and the
  * weights are e4m3, x * x_scale[row] and w * scale[channel] the values they
  * stand for; forward only.  Sums are fp32 on the tensor cores, every output is
- * rounded once.  Operands whose pointer or stride is no multiple of 16 bytes
- * are copied into the workspace first. */
+ * rounded once.  No output has a byte in common with an input.  Operands whose
+ * pointer or stride is no multiple of 16 bytes are copied into the workspace
+ * first, but for up to 32 rows in the forward call. */
 typedef struct {
   int64_t rows;
   int32_t width;             /* 1 .. 2^17                                                   */
