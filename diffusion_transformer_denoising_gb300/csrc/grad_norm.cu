@@ -113,7 +113,14 @@ DIT_DEV double piece_squares(const T* p, int n) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) add_squares<T, E>(r[i], fine, rest);
   } else {
-    for (int i = threadIdx.x; i < vectors; i += kGradThreads) add_squares<T, E>(load_raw<T, E>(p + head + i * E), fine, rest);
+    constexpr int U = 4;  // loads under way
+    for (int i = threadIdx.x; i < vectors; i += U * kGradThreads) {
+      Raw<T, E> r[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) r[k] = i + k * kGradThreads < vectors ? load_raw<T, E>(p + head + (i + k * kGradThreads) * E) : zero_raw<T, E>();
+#pragma unroll
+      for (int k = 0; k < U; ++k) add_squares<T, E>(r[k], fine, rest);
+    }
     const int tail = n - head - vectors * E;
     const int i = (int)threadIdx.x;
     if (i < head + tail) {
@@ -149,13 +156,21 @@ DIT_DEV void scale_piece(const T* p, T* out, int n, float k) {
   const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
   const int vectors = same ? (n - head) / E : 0;
   if (!same) head = n;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vectors; i += kGradThreads) {
-    float f[E];
-    unpack<T, E>(load_raw<T, E>(p + head + i * E), f);
+  constexpr int U = 4;  // loads under way before the stores, which may be to the same place
+  for (int i = threadIdx.x; i < vectors; i += U * kGradThreads) {
+    Raw<T, E> r[U];
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] *= k;
-    store_f32<T, E>(out + head + i * E, f);
+    for (int u = 0; u < U; ++u)
+      if (i + u * kGradThreads < vectors) r[u] = load_raw<T, E>(p + head + (i + u * kGradThreads) * E);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u * kGradThreads >= vectors) continue;
+      float f[E];
+      unpack<T, E>(r[u], f);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[j] *= k;
+      store_f32<T, E>(out + head + (i + u * kGradThreads) * E, f);
+    }
   }
   for (int i = threadIdx.x; i < n - vectors * E; i += kGradThreads) {
     const int at = i < head ? i : vectors * E + i;
