@@ -7,8 +7,10 @@
 //
 // What bounds it: HBM.  Two passes, since the factor needs every value: the sums of
 // the pieces that a block has (always the same ones), then the factor (each block
-// adds up the blocks' sums for itself) and the products.  The second pass walks the pieces backwards,
-// so it begins with what the first has left in L2.
+// adds up the blocks' sums for itself) and the products.  The second pass walks the
+// pieces backwards, so it begins with what the first has left in L2.  Measured on one
+// GB300: 0.83 G bf16 gradients 235 us = 7.0 TB/s and 500 us = 6.6 TB/s (with a sum for
+// each piece, which a block waited for and the second pass read, 468 and 575 us).
 #include <math.h>
 
 #include "launch.cuh"
