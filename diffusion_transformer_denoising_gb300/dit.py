@@ -722,6 +722,8 @@ def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, s
     are.  workspace: a contiguous tensor of dit_grad_norm_workspace_bytes, or
     None to take one from torch's allocator (only on torch's current stream)."""
     torch = _torch or _use_torch()
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
     limit = _INF
     if max_norm is None:
         if clipped is not None:
