@@ -82,6 +82,7 @@ struct Product {
   int N;
   int k_blocks, k_half; // DX: blocks of each half of K
   int m_tiles, n_tiles, group_n, splits, items;
+  int k_per;            // K blocks of a split; the last has the rest
   uint32_t idesc;
   int f16, act;
 };
@@ -202,8 +203,6 @@ DIT_DEV Tile tile_of(const Product& P, int item) {
   t.nb = g * P.group_n + in - t.mb * width;
   return t;
 }
-// First K block of a split (below 2^25 blocks and 16 splits).
-DIT_DEV int split_begin(const Product& P, int z) { return P.k_blocks * z / P.splits; }
 
 DIT_DEV void load32(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, reinterpret_cast<uint32_t(&)[32]>(v)); }
 DIT_DEV void wait32(float (&v)[32]) { tmem_ld_wait_regs(reinterpret_cast<uint32_t(&)[32]>(v)); }
@@ -446,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const Tile t = tile_of(P, item);
         const int a0 = PAIR ? (2 * t.mb + (int)rank) * C::BM : t.mb * C::BM;  // first row of A
         const int b0 = MODE == FWD ? t.nb * (C::BN / 2) : t.nb * C::BN + (int)rank * 128;
-        const int kb1 = P.splits > 1 ? split_begin(P, t.z + 1) : P.k_blocks;
-        for (int kb = P.splits > 1 ? split_begin(P, t.z) : 0; kb < kb1; ++kb) {
+        const int kb0 = t.z * P.k_per, kb1 = min(P.k_blocks, kb0 + P.k_per);
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, err, 11);
           if (!ok) break;
           uint8_t* sa = smem + stage * C::STAGE;
@@ -511,12 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::BN;
         // The issuer does without the tile's place where it can: with the divisions of
-        // tile_of and split_begin (64-bit ones at first) the tensor cores waited longer
+        // tile_of and of a split's bounds the tensor cores waited longer
         // between tiles: the video case took 978 us instead of 960, from e4m3 577 instead of 550.
         int kb0 = 0, kb1 = P.k_blocks;
         if (P.splits > 1) {
-          const int z = item / (P.m_tiles * P.n_tiles) % P.splits;
-          kb0 = split_begin(P, z), kb1 = split_begin(P, z + 1);
+          kb0 = item / (P.m_tiles * P.n_tiles) % P.splits * P.k_per;
+          kb1 = min(kb1, kb0 + P.k_per);
         }
         for (int kb = kb0; kb < kb1; ++kb) {
           ok = mbar_wait(&full[stage], phase, abort_flag, err, 13);
@@ -924,18 +923,26 @@ struct Split {
 // costs a pair 512 cycles on 256 x 256 (the tensor cores' rate), a single CTA
 // about 300 on 128 x 128 (256 at that rate); a launch fills and drains in about 4000,
 // and partial sums cost their traffic (written and read, fp32) and a launch.
+//
+// No split is longer than kLongest blocks: the tensor cores' fp32 sums lose up to 2^-23
+// of themselves at each step, to one side (16.8 M rows of terms of one sign, 1 M a
+// split: dW 6.6e-3 too small), and a wait for a tile has a limit in time.
+constexpr int64_t kLongest = 1024;
 Split choose(int64_t M, int64_t N, int64_t cols_per_n, int64_t k_blocks, int problems) {
   Split best{false, 1};
   double least = 0;
+  const int64_t fewest = (k_blocks + kLongest - 1) / kLongest;
   for (int pair = 0; pair < 2; ++pair)
-    for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && k_blocks / s < 4) break;
+    for (int64_t s = fewest > 1 ? fewest : 1; s <= fewest || s <= 16; ++s) {
+      if (s > 1 && s > fewest && k_blocks / s < 4) break;
+      const int64_t per = (k_blocks + s - 1) / s;
+      const int64_t splits = (k_blocks + per - 1) / per;  // none is empty
       const int64_t tm = pair ? 256 : 128, tn = (pair ? 256 : 128) / cols_per_n;
-      const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn) * problems * s;
+      const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn) * problems * splits;
       const int64_t slots = pair ? kSms / 2 : kSms;
-      double t = (double)((tiles + slots - 1) / slots) * (double)((k_blocks + s - 1) / s) * (pair ? 512. : 300.) + 4000.;
-      if (s > 1) t += 5000. + (double)M * N * cols_per_n * problems * s * 8. / 3500.;
-      if (least == 0 || t < least) least = t, best = Split{pair != 0, s};
+      double t = (double)((tiles + slots - 1) / slots) * (double)per * (pair ? 512. : 300.) + 4000.;
+      if (splits > 1) t += 5000. + (double)M * N * cols_per_n * problems * splits * 8. / 3500.;
+      if (least == 0 || t < least) least = t, best = Split{pair != 0, (int)splits};
     }
   return best;
 }
@@ -1073,6 +1080,7 @@ cudaError_t launch_product(Product& P, int problems, cudaStream_t s) {
 template <int MODE, bool F8>
 cudaError_t run_product(Product& P, const Split& sp, int problems, cudaStream_t s) {
   P.splits = sp.splits;
+  P.k_per = (P.k_blocks + sp.splits - 1) / sp.splits;
   if constexpr (MODE == FWD)
     if (P.act == DIT_ACT_GELU)
       return sp.pair ? launch_product<MODE, F8, true, DIT_ACT_GELU>(P, problems, s) : launch_product<MODE, F8, false, DIT_ACT_GELU>(P, problems, s);

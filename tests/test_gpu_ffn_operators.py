@@ -52,6 +52,10 @@ def near(got, ref, err32, name=""):
     g = n64(got)
     assert g.shape == ref.shape, (name, g.shape, ref.shape)
     assert np.array_equal(np.isnan(g), np.isnan(ref)), name
+    # past the type's largest number by more than its rounding and the error: infinite
+    past = np.abs(ref) - err32 > torch.finfo(got.dtype).max * (1 + half_step(got))
+    assert np.array_equal(g[past], np.sign(ref[past]) * np.inf), name
+    g, ref = np.where(past, 0, g), np.where(past, 0, ref)
     tol = half_step(got) * np.abs(ref) + np.asarray(err32) * (1 + half_step(got)) + subnormal(got)
     err = np.abs(g - ref)
     bad = err > tol
@@ -584,6 +588,29 @@ def test_gated_ffn_gradients_of_more_than_4_gb_of_slopes():
     for got, d in ((dwg, dg), (dwu, du)):
         near(got[cols], d.T @ n64(x), (2.0 ** -9 + 2.0 ** -15 + 2 * M * ULP) * (np.abs(d).T @ np.abs(n64(x))), "dw")
     near(db[cols], du.sum(0), (2.0 ** -15 + 48 * ULP) * np.abs(du).sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("size", [2e3, 2e2])
+@pytest.mark.parametrize("rows", [70_001, 3_000_001, 20_000_003])
+def test_gated_ffn_weight_gradient_of_very_many_rows(rows, size, dtype):
+    # act(32) = 32 and 32 * dout are exact, and all terms of one sign: what is left is the sum of the products
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    D, F, t = 8, 8, DT[dtype]
+    rand = lambda *s: torch.rand(s, device="cuda", generator=g)
+    x, dout = (1 + rand(rows, D)).to(t), ((1 + rand(rows, F)) * (size / rows)).to(t)
+    gate, up, w = torch.full((rows, F), 32.0, dtype=t, device="cuda"), torch.zeros(rows, F, dtype=t, device="cuda"), torch.zeros(F, D, dtype=t, device="cuda")
+    dw, db = nans((F, D), t), nans((F,), torch.float32)
+    dit.dit_gated_ffn_backward(x, w, w, gate, up, dout, dw_up=dw, dbias_up=db)
+    ref, sums = np.zeros((F, D)), np.zeros(F)
+    for i in range(0, rows, 1 << 22):
+        d = dout[i:i + (1 << 22)].double() * 32
+        ref += (d.t() @ x[i:i + (1 << 22)].double()).cpu().numpy()
+        sums += d.sum(0).cpu().numpy()
+    # 65536 rows are 4096 steps of the accumulator, each at most 2^-23 of the sum off, half of that on the way
+    near(dw, ref, (2048 * 2 + 64) * ULP * ref, "dw")
+    near(db, sums, 64 * ULP * sums, "dbias")
 
 
 # ------------------------------------------------------------------ gradient norm
