@@ -650,9 +650,10 @@ DIT_DEV void products(float (&c)[4], const uint4& lo, const uint4& hi, const uin
 }
 
 // NT: groups of 8 tokens.  F16: the output's type, and of 16-bit operands theirs.
-template <bool F8, bool F16, int NT, bool WHOLE, int ACT>
-__global__ void __launch_bounds__(32 * kFewWarps, 4) few_rows_kernel(const Few a) {
-  constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 || (F8 && !WHOLE) ? 2 : 4;
+// BLOCKS: an SM's; with five of them, fewer pieces are under way in each.
+template <bool F8, bool F16, int NT, bool WHOLE, int ACT, int BLOCKS>
+__global__ void __launch_bounds__(32 * kFewWarps, BLOCKS) few_rows_kernel(const Few a) {
+  constexpr int E = F8 ? 16 : 8, STEP = 4 * E, U = NT > 2 || (F8 && !WHOLE) || BLOCKS > 4 ? 2 : 4;
   __shared__ float sums[2][kFewWarps][NT][16][9];
   wait_previous();
   start_next();
@@ -1137,12 +1138,20 @@ cudaError_t pack_operands(const dit_gated_ffn_args& a, Plan& p, char* ws, cudaSt
                   : launch_kernel(pack_kernel<uint16_t>, grid, dim3(256), 0, s, 1, false, k);
 }
 
+// Five blocks an SM where four of each would be more than one round: 11008 channels
+// from width 4096 for 1 / 16 / 32 rows 31 / 32 / 37 us instead of 32 / 40 / 49; where
+// four are enough they are as good or better (8960 from 1536: 32 rows 13 us, 16 with five).
+template <bool F8, bool F16, int NT, int ACT>
+cudaError_t launch_few(const Few& k, bool whole, cudaStream_t s) {
+  const int blocks = (k.F + 15) / 16;
+  const auto kernel = !whole                ? few_rows_kernel<F8, F16, NT, false, ACT, 4>
+                      : blocks > 4 * kSms   ? few_rows_kernel<F8, F16, NT, true, ACT, 5>
+                                            : few_rows_kernel<F8, F16, NT, true, ACT, 4>;
+  return launch_kernel(kernel, dim3(blocks), dim3(32 * kFewWarps), 0, s, 1, true, k);
+}
 template <bool F8, bool F16, int NT>
 cudaError_t launch_few(const Few& k, bool whole, int act, cudaStream_t s) {
-  const auto kernel = act == DIT_ACT_SILU
-                          ? whole ? few_rows_kernel<F8, F16, NT, true, DIT_ACT_SILU> : few_rows_kernel<F8, F16, NT, false, DIT_ACT_SILU>
-                          : whole ? few_rows_kernel<F8, F16, NT, true, DIT_ACT_GELU> : few_rows_kernel<F8, F16, NT, false, DIT_ACT_GELU>;
-  return launch_kernel(kernel, dim3((k.F + 15) / 16), dim3(32 * kFewWarps), 0, s, 1, true, k);
+  return act == DIT_ACT_SILU ? launch_few<F8, F16, NT, DIT_ACT_SILU>(k, whole, s) : launch_few<F8, F16, NT, DIT_ACT_GELU>(k, whole, s);
 }
 template <bool F8, bool F16>
 cudaError_t launch_few(const Few& k, bool whole, int act, cudaStream_t s) {

@@ -337,6 +337,7 @@ FFN_CASES = [
     ("bf16", 1, 1536, 520, "silu", False, "plain"), ("f16", 1, 7, 5, "silu", True, "odd"), ("bf16", 2, 1, 1, "gelu", True, "plain"),
     ("bf16", 8, 64, 16, "silu", False, "pitch"), ("f16", 9, 100, 17, "gelu", True, "odd"), ("bf16", 16, 65, 33, "silu", True, "plain"),
     ("f16", 17, 96, 40, "silu", False, "plain"), ("bf16", 32, 333, 129, "gelu", True, "plain"),
+    ("bf16", 3, 64, 9760, "gelu", False, "plain"), ("f16", 30, 72, 9744, "silu", True, "plain"),   # more than one round of blocks
     ("bf16", 33, 64, 64, "silu", False, "plain"), ("f16", 33, 7, 5, "gelu", True, "odd"), ("bf16", 64, 1, 1, "silu", True, "plain"),
     ("bf16", 127, 65, 63, "silu", True, "pitch"), ("f16", 128, 64, 128, "gelu", False, "plain"), ("bf16", 129, 200, 130, "silu", True, "odd"),
     ("bf16", 255, 72, 264, "silu", False, "pitch"), ("f16", 257, 128, 257, "silu", True, "plain"), ("bf16", 300, 512, 520, "gelu", True, "plain"),
