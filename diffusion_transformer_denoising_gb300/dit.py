@@ -737,6 +737,8 @@ def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, s
             _refuse(DIT_ERR_INVALID_ARG, "max_norm must be finite (None: the norm only)")
         if clipped is None:
             clipped = grads
+        elif not isinstance(clipped, (list, tuple)):
+            clipped = list(clipped)
     if norm.dtype is not torch.float32 or norm.numel() != 1:
         _refuse(DIT_ERR_INVALID_ARG, "norm must be one float32")
     tensors, n = _grad_tensors(grads, clipped)
