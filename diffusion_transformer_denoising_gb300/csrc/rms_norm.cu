@@ -46,6 +46,9 @@ cudaError_t rms_norm_run(const dit_rms_norm_args& a, bool backward, float* works
   p.rows = (uint32_t)rows, p.tokens = (uint32_t)a.tokens;
   p.C = a.channels, p.eps = a.eps;
   const Rows kind = rows_kind(p, 16 / esz);
+  p.words = esz == 2 && (kind == ODD_ROWS || a.channels % 8) && aligned(p.x, p.sx, esz, 4) && aligned(p.res, p.sres, esz, 4) &&
+            aligned(p.total, p.stotal, esz, 4) && aligned(p.dy, p.sdy, esz, 4) &&
+            (a.out_dtype == DIT_DTYPE_E4M3 || aligned(p.out, p.sout, esz, 4));
   if (!backward) {
     const int64_t blocks = blocks_of(a, false, kind);
     return by_type(a.dtype, p, a.out_dtype == DIT_DTYPE_E4M3 ? E4M3 : SAME, blocks, s);

@@ -44,6 +44,7 @@ struct Norm {
   int C;
   float eps;
   int aligned;     // AL_*: 16-byte rows (AL_OUT of e4m3: 8-byte rows for chunks of 8, 4 for 4)
+  bool words;      // 16-bit rows of 4-byte words, not all of them of 16-byte vectors
 };
 
 // max(a, |b|, |c|), NaN if one of them is
@@ -101,8 +102,9 @@ DIT_DEV uint4 packed(const Pairs<T>& p) {
     return make_uint4(pack2<T>(p[0].x, p[0].y), pack2<T>(p[1].x, p[1].y), pack2<T>(p[2].x, p[2].y), pack2<T>(p[3].x, p[3].y));
 }
 
-// The chunk at p, of which n elements are there (zeros behind them).
-template <typename T, bool WHOLE>
+// The chunk at p, of which n elements are there (zeros behind them).  WORDS: rows of
+// 4-byte words, which go two 16-bit elements at a time.
+template <typename T, bool WHOLE, bool WORDS = false>
 DIT_DEV uint4 load_chunk(const T* p, int n, bool aligned) {
   constexpr int E = 16 / sizeof(T);
   if (WHOLE || (aligned && n >= E)) return *reinterpret_cast<const uint4*>(p);
@@ -111,6 +113,13 @@ DIT_DEV uint4 load_chunk(const T* p, int n, bool aligned) {
 #pragma unroll
     for (int j = 0; j < E; ++j)
       if (j < n) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+  } else if constexpr (WORDS) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j + 1 < n) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+      else if (2 * j < n) w[j] = q[2 * j];
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < E; ++j)
@@ -118,7 +127,7 @@ DIT_DEV uint4 load_chunk(const T* p, int n, bool aligned) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, bool WORDS = false>
 DIT_DEV void store_chunk(T* p, int n, bool aligned, const uint4& r) {
   constexpr int E = 16 / sizeof(T);
   if (WHOLE || (aligned && n >= E)) {
@@ -126,6 +135,14 @@ DIT_DEV void store_chunk(T* p, int n, bool aligned, const uint4& r) {
     return;
   }
   const uint32_t* w = &r.x;
+  if constexpr (WORDS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j + 1 < n) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+      else if (2 * j < n) reinterpret_cast<uint16_t*>(p)[2 * j] = (uint16_t)w[j];
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < E; ++j) {
     if (j >= n) continue;
@@ -546,9 +563,11 @@ __global__ void __launch_bounds__(32 * RW * ROWS, ring_blocks(RW, NV, ROWS, Ring
 
 // Narrow rows: LPR lanes hold a row, a chunk each, 32 / LPR rows a warp, kNarrowBatch
 // of such groups of rows under way at once.  (A warp a row took 375 us for 1.6 M rows
-// of 64 bf16 channels, 493 us for the gradient.)
+// of 64 bf16 channels, 493 us for the gradient.)  WORDS is a form of its own: with the
+// choice made at each chunk rows that are not of words took 570 us instead of 466.
+// Rows of words: 1.34 M of 78 channels 223 us, 449 by elements; gradients 289 and 721.
 constexpr int kNarrowWarps = 4, kNarrowBatch = 4;
-template <typename T, int LPR, int MODE>
+template <typename T, int LPR, int MODE, bool WORDS>
 __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const Norm a) {
   constexpr int E = 16 / sizeof(T), RPW = 32 / LPR, U = kNarrowBatch;
   __shared__ float join[MODE == GRAD ? kNarrowWarps : 1][LPR * E];
@@ -577,9 +596,9 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
       x[u] = res[u] = make_uint4(0, 0, 0, 0);
       if constexpr (MODE == GRAD) dy[u] = make_uint4(0, 0, 0, 0);
       if (!there[u]) continue;
-      x[u] = load_chunk<T, false>(static_cast<const T*>(a.x) + b[u] * a.sx[0] + t[u] * a.sx[1] + c, n, a.aligned & AL_X);
-      if (a.res) res[u] = load_chunk<T, false>(static_cast<const T*>(a.res) + b[u] * a.sres[0] + t[u] * a.sres[1] + c, n, a.aligned & AL_RES);
-      if constexpr (MODE == GRAD) dy[u] = load_chunk<T, false>(static_cast<const T*>(a.dy) + b[u] * a.sdy[0] + t[u] * a.sdy[1] + c, n, a.aligned & AL_DY);
+      x[u] = load_chunk<T, false, WORDS>(static_cast<const T*>(a.x) + b[u] * a.sx[0] + t[u] * a.sx[1] + c, n, a.aligned & AL_X);
+      if (a.res) res[u] = load_chunk<T, false, WORDS>(static_cast<const T*>(a.res) + b[u] * a.sres[0] + t[u] * a.sres[1] + c, n, a.aligned & AL_RES);
+      if constexpr (MODE == GRAD) dy[u] = load_chunk<T, false, WORDS>(static_cast<const T*>(a.dy) + b[u] * a.sdy[0] + t[u] * a.sdy[1] + c, n, a.aligned & AL_DY);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -598,13 +617,13 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
         if (!there[u]) continue;
         norm_gradient<T>(g, d, v, r, k, dw);
         if (a.res) add_to<T>(d, pairs<T>(res[u]));
-        store_chunk<T, false>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(d));
+        store_chunk<T, false, WORDS>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(d));
       } else {
         if (a.res) {
           add_to<T>(v, pairs<T>(res[u]));
           const uint4 sum = packed<T>(v);
           v = pairs<T>(sum);  // the norm is of the sum as it is kept
-          if (a.total && there[u]) store_chunk<T, false>(static_cast<T*>(a.total) + b[u] * a.stotal[0] + t[u] * a.stotal[1] + c, n, a.aligned & AL_TOTAL, sum);
+          if (a.total && there[u]) store_chunk<T, false, WORDS>(static_cast<T*>(a.total) + b[u] * a.stotal[0] + t[u] * a.stotal[1] + c, n, a.aligned & AL_TOTAL, sum);
         }
         add_products<T>(square, v, v);
         const float r = rsqrtf(fmaf(row_sum(square.x + square.y), inv_c, a.eps));
@@ -624,7 +643,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
         } else {
           if (!there[u]) continue;
           scale_by<T>(v, r);
-          store_chunk<T, false>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(v));
+          store_chunk<T, false, WORDS>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(v));
         }
       }
     }
@@ -808,7 +827,8 @@ struct Shape {
 // ALIGNED: rows that begin at such vectors; ODD: any.
 enum Rows { WHOLE_ROWS, ALIGNED_ROWS, ODD_ROWS };
 // Odd rows of more than 20 chunks fare better with shifted windows (411206 rows of 255
-// bf16 channels 268 us, 457 element by element; of 130, 17 chunks, 513 and 475).
+// bf16 channels 268 us, 457 element by element; of 130, 17 chunks, 513 and 475, and
+// 277 by words).
 inline Shape shape_of(int chunks, Rows kind) {
   for (const int lanes : {1, 4, 8, 16, 32})
     if (chunks <= lanes && (kind != ODD_ROWS || chunks <= 20)) return {lanes, 0, 0, kNarrowWarps * 32 / lanes};
@@ -842,7 +862,9 @@ cudaError_t ring(const Norm& p, bool whole, int64_t blocks, cudaStream_t s) {
 }
 template <typename T, int LPR, int MODE>
 cudaError_t narrow(const Norm& p, int64_t blocks, cudaStream_t s) {
-  return launch_kernel(norm_narrow_kernel<T, LPR, MODE>, dim3((unsigned)blocks), dim3(32 * kNarrowWarps), 0, s, 1, false, p);
+  if constexpr (sizeof(T) == 2)
+    if (p.words) return launch_kernel(norm_narrow_kernel<T, LPR, MODE, true>, dim3((unsigned)blocks), dim3(32 * kNarrowWarps), 0, s, 1, false, p);
+  return launch_kernel(norm_narrow_kernel<T, LPR, MODE, false>, dim3((unsigned)blocks), dim3(32 * kNarrowWarps), 0, s, 1, false, p);
 }
 template <typename T, int W, int NV, int MODE, bool WHOLE>
 cudaError_t launch_rows(const Norm& p, int64_t blocks, cudaStream_t s) {

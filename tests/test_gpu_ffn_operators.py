@@ -200,6 +200,46 @@ def test_rms_norm_tensors_of_different_alignment(dtype, C, pads):
     near(dw, rdw, (NSTEPS + 38) * ULP * np.sum(np.abs(n64(dy)) * tn, (0, 1)), "dweight")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("C", [1, 2, 9, 33, 34, 60, 77, 130, 159])
+@pytest.mark.parametrize("lefts", [(2, 2, 2, 2), (0, 2, 4, 6), (4, 0, 0, 2), (2, 2, 1, 2), (2, 3, 2, 2)], ids=str)
+def test_rms_norm_rows_of_words(dtype, C, lefts):
+    """Rows of an even stride that begin `left` channels into theirs: whole words, an odd last element, neighbours left alone."""
+    rng = np.random.default_rng(C + 10 * sum(lefts))
+    shape, w = (2, 35, C), torch.from_numpy(1 + 0.3 * rng.standard_normal(C)).float().cuda()
+    width = (C + 7) // 2 * 2 + 2
+
+    def rows(i, fill=True):
+        wide = randn(rng, (*shape[:-1], width), dtype) if fill else torch.full((*shape[:-1], width), 7.0, dtype=DT[dtype], device="cuda")
+        return wide, wide[..., lefts[i]:lefts[i] + C]
+
+    def alone(wide, i):
+        keep = wide.clone()
+        keep[..., lefts[i]:lefts[i] + C] = 7.0
+        assert torch.all(keep == 7.0)
+
+    x, res = rows(0)[1], rows(1)[1]
+    (wide_total, total), (wide_out, out) = rows(2, False), rows(3, False)
+    dit.dit_rms_norm_forward(x, out, residual=res, total=total, weight=w)
+    alone(wide_total, 2), alone(wide_out, 3)
+    near(total, n64(x) + n64(res), ULP * (np.abs(n64(x)) + np.abs(n64(res))), "total")
+    ref = O.rms_norm_forward(n64(total), n64(w))
+    near(out, ref, NSTEPS * ULP * np.abs(ref), "out")
+    q, scale = torch.empty(shape, dtype=E4M3, device="cuda"), nans((2, 35), torch.float32)
+    dit.dit_rms_norm_forward(x, q, residual=res, weight=w, scale=scale)
+    s = O.e4m3_scale(ref)
+    near(scale, s, NSTEPS * ULP * s, "scale")
+    near(q, ref / s[..., None], NSTEPS * ULP * np.abs(ref / s[..., None]), "e4m3")
+    dy, (wide_dx, dx), dw = rows(3)[1], rows(1, False), nans((C,), torch.float32)
+    dit.dit_rms_norm_backward(total, dy, dx, dtotal=x, weight=w, dweight=dw)
+    alone(wide_dx, 1)
+    rdx, rdw = O.rms_norm_backward(n64(total), n64(dy), n64(w), 1e-6, n64(x))
+    r, tn = norm_scale(n64(total), None, 1e-6)
+    g = np.abs(n64(dy) * n64(w))
+    near(dx, rdx, NSTEPS * ULP * (r * (g + tn * np.mean(g * tn, -1, keepdims=True)) + np.abs(n64(x))), "dx")
+    near(dw, rdw, (NSTEPS + 70) * ULP * np.sum(np.abs(n64(dy)) * tn, (0, 1)), "dweight")
+
+
 @pytest.mark.parametrize("C", [30, 255, 1001, 2056, 5000])
 def test_rms_norm_leaves_what_lies_around_its_rows_alone(C):
     rng = np.random.default_rng(C)
