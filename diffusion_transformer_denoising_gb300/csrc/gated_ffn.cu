@@ -107,9 +107,16 @@ template <int ACT>
 DIT_DEV float argument(float g) {
   return ACT == DIT_ACT_SILU ? g : g * fmaf(kGelu2 * 0.044715f, g * g, kGelu2);
 }
-// sigmoid(z) and 1 - sigmoid(z), each on its own scale: subnormal numbers are kept.
+// min(a, b), NaN if one of them is
+DIT_DEV float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// sigmoid(z) and 1 - sigmoid(z), each on its own scale: subnormal numbers are kept.  Of
+// NaN they are NaN and 0: GELU's slope takes sigmoid(z) alone where the other is 0.
 DIT_DEV float2 sigmoids(float z) {
-  const float m = fminf(z * kLog2e, 126.f);
+  const float m = min_nan(z * kLog2e, 126.f);
   float e;
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(m));
   const float r = rcp_approx(1.f + e);

@@ -981,3 +981,34 @@ def test_gradients_through_autograd_functions():
         gg = n64(g).reshape(v.shape)
         # intermediate values are rounded to fp16, a few 2^-11 of the gradient's size each way
         assert abs(np.sum(gg * d) - diff) <= 16 * 2.0 ** -11 * np.linalg.norm(gg) * 4, i
+
+
+# ------------------------------------------------------------------ gated feed-forward: a NaN in gate
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("F", [152, 150, 149])   # slopes by vectors, words and elements
+def test_gated_ffn_gradient_of_a_nan_gate(act, dtype, F):
+    rng = np.random.default_rng(F)
+    M, D = 70, 40
+    x, wg, wu = (randn(rng, s, dtype, 0.3) for s in ((M, D), (F, D), (F, D)))
+    gate, up, dout = (randn(rng, (M, F), dtype) for _ in range(3))
+    gate[2, 148] = float("nan")
+    args = (x, wg, wu, gate, up, dout)
+    made = dict(dx=torch.zeros_like(x), dw_gate=torch.zeros_like(wg), dw_up=torch.zeros_like(wu),
+                dbias_gate=torch.zeros(F, device="cuda"), dbias_up=torch.zeros(F, device="cuda"))
+    want = {k: torch.zeros_like(t, dtype=torch.bool) for k, t in made.items()}
+    for k, row in (("dx", 2), ("dw_gate", 148), ("dw_up", 148), ("dbias_gate", 148), ("dbias_up", 148)):
+        want[k][row] = True
+    dit.dit_gated_ffn_backward(*args, **made, act=ACT[act])
+    for k, t in made.items():
+        assert torch.equal(torch.isnan(t), want[k]), k
+    for k, t in made.items():
+        alone = torch.zeros_like(t)
+        dit.dit_gated_ffn_backward(*args, **{k: alone}, act=ACT[act])
+        assert torch.equal(torch.isnan(alone), want[k]), k
+    # and forward, whatever the weights of the other channels are
+    wg[7, 3] = float("nan")
+    for rows in (5, M):
+        out = torch.zeros(rows, F, dtype=DT[dtype], device="cuda")
+        dit.dit_gated_ffn_forward(x[:rows], wg, wu, out, act=ACT[act])
+        assert torch.isnan(out).any(0).nonzero().flatten().tolist() == [7] and torch.isnan(out[:, 7]).all()
