@@ -165,7 +165,9 @@ DIT_DEV void store_e4m3(uint8_t* p, int n, bool aligned, const Pairs<T>& v) {
   for (int j = 0; j < E; ++j)
     if (j < n) p[j] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
 }
-// v *= the weights of channels c on (zeros behind the last)
+// v *= the weights of channels c on (zeros behind the last; WHOLE: n is E or, behind the
+// row's end, not above 0).  Only the load stands under that condition: a branch around the
+// products or an index held to the last weights took the video pair 145 us, this 118.
 template <typename T, bool WHOLE>
 DIT_DEV void times_weight(Pairs<T>& v, const float* w, int c, int n, bool aligned) {
   constexpr int E = 16 / sizeof(T);
@@ -173,7 +175,8 @@ DIT_DEV void times_weight(Pairs<T>& v, const float* w, int c, int n, bool aligne
   if (WHOLE || (aligned && n >= E)) {
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(w + c + j));
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!WHOLE || n > 0) t = __ldg(reinterpret_cast<const float4*>(w + c + j));
       v[j / 2] = fmul2(v[j / 2], make_float2(t.x, t.y));
       v[j / 2 + 1] = fmul2(v[j / 2 + 1], make_float2(t.z, t.w));
     }

@@ -1012,3 +1012,32 @@ def test_gated_ffn_gradient_of_a_nan_gate(act, dtype, F):
         out = torch.zeros(rows, F, dtype=DT[dtype], device="cuda")
         dit.dit_gated_ffn_forward(x[:rows], wg, wu, out, act=ACT[act])
         assert torch.isnan(out).any(0).nonzero().flatten().tolist() == [7] and torch.isnan(out[:, 7]).all()
+
+
+# widths that fill no form's threads: the first behind the one before, of several rows a warp to a whole block
+@pytest.mark.parametrize("dtype,C", [*(("bf16", C) for C in (56, 248, 264, 520, 776, 1032, 1544, 2056, 4104, 8200)),
+                                     *(("f32", C) for C in (28, 124, 132, 260, 388, 516, 772, 1028, 2052, 4100, 8196))])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_reads_no_weight_behind_the_last(dtype, C, residual):
+    """NaN around the weight and the rows: only what lies between them counts."""
+    rng = np.random.default_rng(C)
+    around = nans((3, C + 32), torch.float32)
+    w = around[1, 16:16 + C]
+    w.copy_(torch.from_numpy(1 + 0.3 * rng.standard_normal(C)))
+    def rows():
+        wide = nans((9, C + 32), DT[dtype])
+        wide[1:8, 16:16 + C] = randn(rng, (7, C), dtype)
+        return wide[1:8, 16:16 + C]
+    x, res = rows(), rows() if residual else None
+    out, q, scale = nans((7, C), DT[dtype]), torch.empty((7, C), dtype=E4M3, device="cuda"), nans((7,), torch.float32)
+    dit.dit_rms_norm_forward(x, out, residual=res, weight=w)
+    v = n64(x) if res is None else n64((x.float() + res.float()).to(DT[dtype]))
+    ref = O.rms_norm_forward(v, n64(w))
+    near(out, ref, NSTEPS * ULP * np.abs(ref), "out")
+    dit.dit_rms_norm_forward(x, q, residual=res, weight=w, scale=scale)
+    s = O.e4m3_scale(ref)
+    near(scale, s, NSTEPS * ULP * s, "scale")
+    near(q, ref / s[..., None], NSTEPS * ULP * np.abs(ref / s[..., None]), "e4m3")
+    dy, dx, dw = rows(), nans((7, C), DT[dtype]), nans((C,), torch.float32)
+    dit.dit_rms_norm_backward(x, dy, dx, dtotal=res, weight=w, dweight=dw)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
