@@ -2,7 +2,8 @@
 // activations' type or into e4m3 with a scale for each row, and its gradient.
 //
 // Mathematics.  v = x + residual rounded to the type, r = (mean v^2 + eps)^-1/2,
-// y = v r w.  e4m3: scale = max |y| / 448, y / scale rounded to nearest even.
+// y = v r w, in this order: v w may vanish or overflow where v r, of size 1, does not.
+// e4m3: scale = max |y| / 448, y / scale rounded to nearest even.
 // Gradient: g = dy w, dx = dtotal + r (g - v r^2 mean(g v)), dw = sum dy v r: the two
 // row sums (v^2 and g v) are taken together.
 //
@@ -53,24 +54,29 @@ DIT_DEV float max_abs(float a, float2 b) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b.x), "f"(b.y));
   return d;
 }
+DIT_DEV float rcp_approx(float x) {  // within 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 DIT_DEV float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 
-// What an e4m3 row is held in: top is max |v w|, y = v r w.
+// What an e4m3 row is held in: top is max |y|.  v r comes before the weight: v w of a row of
+// 1e-37 has lost digits that y (of 1e-34 at eps 1e-6) has, and r over its scale is infinite.
 struct RowScale {
-  float scale, factor;  // out = v w factor
+  float scale, factor;  // out = y factor
   bool finite;
 };
-DIT_DEV RowScale row_scale(float top, float r) {
+DIT_DEV RowScale row_scale(float top) {
   RowScale q;
-  top *= r;
   q.finite = top <= 3.402823466e38f;
   // below 448 x 2^-126 the scale stays a normal number, so that its reciprocal is finite
   q.scale = !q.finite ? __int_as_float(0x7fffffff) : top > 0.f ? fmaxf(top / kE4M3Max, 1.17549435e-38f) : 1.f;
-  q.factor = q.finite ? r / q.scale : 0.f;
+  q.factor = q.finite ? rcp_approx(q.scale) : 0.f;
   return q;
 }
 
@@ -499,19 +505,20 @@ __global__ void __launch_bounds__(32 * RW * ROWS, ring_blocks(RW, NV, ROWS, Ring
           if (RESIDUAL == 0) row_sync<RW>();
         }
       }
-      float factor = r, top = 0.f;
+      float factor = 1.f, top = 0.f;
       bool finite = true;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
+        scale_by<T>(v[i], r);
         times_weight<T, WHOLE>(v[i], a.w, c, n, a.aligned & AL_W);
         if constexpr (MODE == E4M3)
 #pragma unroll
           for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[i][j]);
       }
       if constexpr (MODE == E4M3) {
-        const RowScale q = row_scale(row_max(top), r);
+        const RowScale q = row_scale(row_max(top));
         factor = q.factor, finite = q.finite;
         if (lane == 0) a.scale[row] = q.scale;
       }
@@ -522,8 +529,8 @@ __global__ void __launch_bounds__(32 * RW * ROWS, ring_blocks(RW, NV, ROWS, Ring
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + TPR * i) * E, n = WHOLE ? (C - c > 0 ? E : 0) : C - c;
         if (n <= 0) continue;
-        scale_by<T>(v[i], factor);
         if constexpr (MODE == E4M3) {
+          scale_by<T>(v[i], factor);
           const Pairs<T> q = finite ? v[i] : Pairs<T>{};
           if (direct) store_e4m3<T, WHOLE>(out8 + c, n, true, q);
           else store_e4m3<T, true>(out_slot + c, E, true, q);
@@ -630,6 +637,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
         }
         add_products<T>(square, v, v);
         const float r = rsqrtf(fmaf(row_sum(square.x + square.y), inv_c, a.eps));
+        scale_by<T>(v, r);
 #pragma unroll
         for (int j = 0; j < Pairs<T>::N; ++j) v[j] = fmul2(v[j], w[j]);
         if constexpr (MODE == E4M3) {
@@ -638,14 +646,13 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
           for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[j]);
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const RowScale q = row_scale(top, r);
+          const RowScale q = row_scale(top);
           if (!there[u]) continue;
           if (c == 0) a.scale[base + u * RPW + lane / LPR] = q.scale;
           scale_by<T>(v, q.factor);
           store_e4m3<T, false>(static_cast<uint8_t*>(a.out) + at_out, n, a.aligned & AL_OUT, q.finite ? v : Pairs<T>{});
         } else {
           if (!there[u]) continue;
-          scale_by<T>(v, r);
           store_chunk<T, false, WORDS>(static_cast<T*>(a.out) + at_out, n, a.aligned & AL_OUT, packed<T>(v));
         }
       }
@@ -671,11 +678,20 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) norm_narrow_kernel(const No
 }
 
 constexpr int kRowWarps = 8;
+// Blocks of e4m3 rows that an SM holds: without this bound the weights are fetched before r
+// is there, in registers that cost blocks (48828 rows of 2048 bf16 channels 77 us instead of
+// 68).  The other modes keep the compiler's own choice (0).
+constexpr int e4m3_blocks(int w, int nv, int esz) {
+  const int registers = esz == 2 ? (nv == 2 ? (w == 1 ? 64 : 48) : nv == 3 ? (w == 1 ? 80 : 64) : nv == 4 ? 80 : 128)
+                                 : (nv == 2 ? (w == 1 ? 48 : 40) : nv == 3 ? (w == 1 ? 64 : 48) : nv == 4 ? 64 : 80);
+  const int blocks = 65536 / (registers * 32 * (w == 1 ? kRowWarps : w));
+  return blocks > 1 ? blocks : 1;
+}
 
 // W warps hold a row in registers, NV chunks of 16 bytes a thread: chunk tid + 32 W i.
 // One warp a row: kRowWarps rows a block.
 template <typename T, int W, int NV, int MODE, bool WHOLE>
-__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W) norm_kernel(const Norm a) {
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W, MODE == E4M3 ? e4m3_blocks(W, NV, sizeof(T)) : 0) norm_kernel(const Norm a) {
   const int aligned = a.aligned | (WHOLE ? ~0 : 0);
   constexpr int E = 16 / sizeof(T), TPR = 32 * W, ROWS = W == 1 ? kRowWarps : 1;
   __shared__ float2 parts[2][W];
@@ -777,18 +793,19 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W) norm_kernel(
         add_products<T>(square, v[i], v[i]);
       }
       const float r = rsqrtf(fmaf(row_sum(make_float2(square.x + square.y, 0.f)).x, inv_c, a.eps));
-      float factor = r, top = 0.f;
+      float factor = 1.f, top = 0.f;
       bool finite = true;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
+        scale_by<T>(v[i], r);
         times_weight<T, WHOLE>(v[i], a.w, c, n, aligned & AL_W);
         if constexpr (MODE == E4M3)
 #pragma unroll
           for (int j = 0; j < Pairs<T>::N; ++j) top = max_abs(top, v[i][j]);
       }
       if constexpr (MODE == E4M3) {
-        const RowScale q = row_scale(row_max(top), r);
+        const RowScale q = row_scale(row_max(top));
         factor = q.factor, finite = q.finite;
         if (tid == 0) a.scale[row] = q.scale;
       }
@@ -796,7 +813,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W) norm_kernel(
       for (int i = 0; i < NV; ++i) {
         const int c = (tid + TPR * i) * E, n = WHOLE ? (a.C - c > 0 ? E : 0) : a.C - c;
         if (n <= 0) continue;
-        scale_by<T>(v[i], factor);
+        if constexpr (MODE == E4M3) scale_by<T>(v[i], factor);
         if constexpr (MODE == E4M3) store_e4m3<T, WHOLE>(static_cast<uint8_t*>(a.out) + at(a.sout) + c, n, aligned & AL_OUT, finite ? v[i] : Pairs<T>{});
         else store_chunk<T, WHOLE>(static_cast<T*>(a.out) + at(a.sout) + c, n, aligned & AL_OUT, packed<T>(v[i]));
       }

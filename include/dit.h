@@ -363,11 +363,12 @@ int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backwar
  *   total = x + residual, rounded once to the type (total = x without residual)
  *   y = total * weight / sqrt(mean(total^2) + eps), the mean over the channels
  * out holds y in the type of x, or in e4m3 with a scale for each row: scale =
- * max |y| / 448 (1 for a row of zeros), out = y / scale rounded to nearest even.
- * Such a row with a NaN or an infinity in it gets the scale NaN and zeros.  The
- * outputs total and out may be the very view of x or of residual (out only in
- * the type of x).  Arithmetic is fp32, the squares' sum too: a row with values
- * of 1e19 and more counts as one of infinite norm, its y is 0. */
+ * max |y| / 448 (1 for a row of zeros, at least 2^-126), out = y / scale rounded
+ * to nearest even.  Such a row with a NaN or an infinity in it gets the scale NaN
+ * and zeros.  The outputs total and out may be the very view of x or of residual
+ * (out only in the type of x).  Arithmetic is fp32, the squares' sum too: a row
+ * with values of 1e19 and more counts as one of infinite norm, its y is 0; squares
+ * of values below 1e-19 lose digits, which an eps as small does not hide. */
 enum { DIT_RMS_NORM_MAX_CHANNELS = 16384 };
 typedef struct {
   int64_t batch;

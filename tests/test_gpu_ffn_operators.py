@@ -1041,3 +1041,85 @@ def test_rms_norm_reads_no_weight_behind_the_last(dtype, C, residual):
     dy, dx, dw = rows(), nans((7, C), DT[dtype]), nans((C,), torch.float32)
     dit.dit_rms_norm_backward(x, dy, dx, dtotal=res, weight=w, dweight=dw)
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+# ------------------------------------------------------------------ tiny and huge rows of the norm
+TINY_WIDTHS = [24, 77, 255, 1536, 1535, 5000, 16384]   # several rows a warp, one, registers, rings, a whole block
+
+
+def tiny_rows(rng, C, dtype):
+    """Rows of 1e-39 to 1e-35, of unequal magnitudes and with zeros: their squares vanish, r is eps^-1/2.  And one of 1."""
+    size = 10.0 ** np.linspace(-39, -35, 12)[:, None]
+    x = rng.standard_normal((1, 12, C)) * size * 10.0 ** rng.uniform(-3, 0, (1, 12, C))
+    x[rng.random(x.shape) < 0.2] = 0
+    x[0, :, 0] = size[:, 0]
+    x[0, 5], x[0, 8] = 0, rng.standard_normal(C)
+    return torch.from_numpy(x).to(DT[dtype]).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", TINY_WIDTHS)
+@pytest.mark.parametrize("affine", [True, False])
+@pytest.mark.parametrize("eps", [1e-6, 1e-24])
+def test_rms_norm_of_tiny_rows_into_e4m3(C, dtype, affine, eps):
+    rng = np.random.default_rng(C + affine)
+    x = tiny_rows(rng, C, dtype)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(C)).float().cuda() if affine else None
+    q, scale = torch.empty(x.shape, dtype=E4M3, device="cuda"), nans((1, 12), torch.float32)
+    dit.dit_rms_norm_forward(x, q, weight=w, scale=scale, eps=eps)
+    ref = O.rms_norm_forward(n64(x), None if w is None else n64(w), eps)
+    s = np.maximum(O.e4m3_scale(ref), 2.0 ** -126)   # scales are normal numbers
+    near(scale, s, NSTEPS * ULP * s, "scale")
+    assert scale[0, 5] == 1
+    # v r is at most half a step of 2^-149 off, the weight is below 4, the scale at least 2^-126
+    near(q, ref / s[..., None], NSTEPS * ULP * np.abs(ref / s[..., None]) + 2.0 ** -20, "e4m3")
+
+
+@pytest.mark.parametrize("dtype,C,pad", [("bf16", 24, 0), ("f16", 77, 1), ("f32", 255, 3), ("bf16", 264, 0), ("bf16", 1536, 0), ("bf16", 1535, 1),
+                                         ("f16", 5000, 8), ("f32", 8196, 0), ("bf16", 16384, 0)])
+@pytest.mark.parametrize("kept", [None, "total", "x", "residual"])
+@pytest.mark.parametrize("size", [1e-30, 1e38])   # v w below 2^-90, and past fp32's largest number
+def test_rms_norm_of_extreme_weights_into_e4m3(dtype, C, pad, kept, size):
+    """The sum comes from where it is kept, or is formed again; y itself is an ordinary number."""
+    rng = np.random.default_rng(C)
+    shape, scales = (2, 9, C), 10.0 ** rng.uniform(0, 4, (2, 9, 1))
+    x, res = (padded(rng, shape, dtype, pad) for _ in range(2))
+    x.copy_(torch.from_numpy(n64(x) * scales).to(DT[dtype]))   # r of 1 and below: v w r is finite where v w is not
+    w = torch.from_numpy(rng.uniform(0.5, 1, C) * size / 8).float().cuda()
+    total = {None: None, "total": padded(rng, shape, dtype, pad, fill=False), "x": x, "residual": res}[kept]
+    v = n64((x.float() + res.float()).to(DT[dtype]))
+    q, scale = torch.empty((2, 9, C + pad), dtype=E4M3, device="cuda")[..., pad:], nans((2, 9), torch.float32)
+    dit.dit_rms_norm_forward(x, q, residual=res, total=total, weight=w, scale=scale)
+    if total is not None:
+        assert np.array_equal(n64(total), v)
+    ref = O.rms_norm_forward(v, n64(w))
+    s = O.e4m3_scale(ref)
+    near(scale, s, NSTEPS * ULP * s, "scale")
+    near(q, ref / s[..., None], NSTEPS * ULP * np.abs(ref / s[..., None]), "e4m3")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", TINY_WIDTHS)
+def test_rms_norm_of_tiny_rows_keeps_its_digits_under_small_weights(C, dtype):
+    # v w would be a subnormal number, v r and v r w are not
+    rng = np.random.default_rng(C)
+    x = torch.from_numpy(rng.uniform(1, 2, (2, 5, C)) * 1e-32).to(DT[dtype]).cuda()
+    w = torch.from_numpy(rng.uniform(1, 2, C) * 1e-12).float().cuda()
+    out = nans(x.shape, DT[dtype])
+    dit.dit_rms_norm_forward(x, out, weight=w, eps=1e-24)
+    ref = O.rms_norm_forward(n64(x), n64(w), 1e-24)
+    near(out, ref, NSTEPS * ULP * np.abs(ref), "out")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", TINY_WIDTHS)
+def test_rms_norm_of_huge_rows_is_zero_whatever_the_weight(C, dtype):
+    x = torch.full((1, 3, C), 1.0, dtype=DT[dtype], device="cuda")
+    x[0, 1] = 3e38
+    w, out = torch.full((C,), 4.0, device="cuda"), nans((1, 3, C), DT[dtype])
+    dit.dit_rms_norm_forward(x, out, weight=w)
+    assert (out[0, 1] == 0).all()
+    near(out[0, [0, 2]], np.full((2, C), 4 / np.sqrt(1 + 1e-6)), NSTEPS * ULP * 4)
+    q, scale = torch.ones(x.shape, device="cuda").to(E4M3), nans((1, 3), torch.float32)
+    dit.dit_rms_norm_forward(x, q, weight=w, scale=scale)
+    assert (q[0, 1].float() == 0).all() and scale[0, 1] == 1 and (q[0, [0, 2]].float() == 448).all()
