@@ -171,7 +171,8 @@ DIT_DEV void columns32(float (&v)[32], const float* p, int c, int n, float none)
     for (int j = 0; j < 32; ++j) v[j] = p && c + j < n ? __ldg(p + c + j) : none;
   }
 }
-// acc * (row_scale * scale) + bias over 32 columns
+// acc * scale * row_scale + bias over 32 columns.  The sum meets one scale, then the other:
+// their product may vanish (a row's scale may be 2^-126) where the value does not.
 template <bool SCALED>
 DIT_DEV void finish32(float (&v)[32], const Product& P, int side, float row_scale, int c0) {
   float w[32];
@@ -180,7 +181,7 @@ DIT_DEV void finish32(float (&v)[32], const Product& P, int side, float row_scal
     const float2 rs = make_float2(row_scale, row_scale);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const float2 x = fmul2(make_float2(v[j], v[j + 1]), fmul2(rs, make_float2(w[j], w[j + 1])));
+      const float2 x = fmul2(fmul2(make_float2(v[j], v[j + 1]), make_float2(w[j], w[j + 1])), rs);
       v[j] = x.x, v[j + 1] = x.y;
     }
   }
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, BLOCKS) few_rows_kernel(const 
       v[m] = sums[m][0][n][c][tok];
 #pragma unroll
       for (int w = 1; w < kFewWarps; ++w) v[m] += sums[m][w][n][c][tok];
-      if constexpr (F8) v[m] *= __ldg(a.x_scale + row) * __ldg(a.scale[m] + f);
+      if constexpr (F8) v[m] = v[m] * __ldg(a.scale[m] + f) * __ldg(a.x_scale + row);
       if (a.bias[m]) v[m] += __ldg(a.bias[m] + f);
       if (a.out[1]) a.out[1 + m][row * a.ldo[1 + m] + f] = (uint16_t)pack16(F16, v[m], 0.f);
     }
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Join J) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= n) continue;
-        if (J.scale[0]) g[j] *= rs * __ldg(J.scale[0] + c + j), v[j] *= rs * __ldg(J.scale[1] + c + j);
+        if (J.scale[0]) g[j] = g[j] * __ldg(J.scale[0] + c + j) * rs, v[j] = v[j] * __ldg(J.scale[1] + c + j) * rs;
         if (J.bias[0]) g[j] += __ldg(J.bias[0] + c + j);
         if (J.bias[1]) v[j] += __ldg(J.bias[1] + c + j);
       }

@@ -409,7 +409,9 @@ int64_t dit_rms_norm_workspace_bytes(const dit_rms_norm_args* a);
  * elements.  dtype is that of out, gate and up, and (operand_dtype ==
  * dtype) of x and the weights.  With operand_dtype DIT_DTYPE_E4M3, x and the
  * weights are e4m3, x * x_scale[row] and w * scale[channel] the values they
- * stand for; forward only.  Sums are fp32 on the tensor cores, every output is
+ * stand for; forward only.  A sum is multiplied by the channel's scale, then by
+ * the row's: any normal number as x_scale, 2^-100 to 2^90 as the others keep all
+ * its digits.  Sums are fp32 on the tensor cores, every output is
  * rounded once.  No output has a byte in common with an input.  Operands whose
  * pointer or stride is no multiple of 16 bytes are copied into the workspace
  * first, but for up to 32 rows in the forward call. */

@@ -1123,3 +1123,19 @@ def test_rms_norm_of_huge_rows_is_zero_whatever_the_weight(C, dtype):
     q, scale = torch.ones(x.shape, device="cuda").to(E4M3), nans((1, 3), torch.float32)
     dit.dit_rms_norm_forward(x, q, weight=w, scale=scale)
     assert (q[0, 1].float() == 0).all() and scale[0, 1] == 1 and (q[0, [0, 2]].float() == 448).all()
+
+
+@pytest.mark.parametrize("M,D,F", [(5, 256, 40), (40, 4096, 64), (300, 256, 136), (2600, 256, 1280)])  # few rows, K split, both tiles
+@pytest.mark.parametrize("bias", [False, True])
+def test_gated_ffn_of_rows_with_tiny_scales(M, D, F, bias):
+    """Scales whose product is no normal number where the sum times both is one."""
+    rng = np.random.default_rng(M)
+    x, wg, wu = (torch.from_numpy(rng.uniform(200, 448, s)).float().to(E4M3).cuda() for s in ((M, D), (F, D), (F, D)))
+    xs = torch.from_numpy(rng.uniform(1, 2, M) * 2.0 ** -126).float().cuda()
+    gs = torch.from_numpy(rng.uniform(1, 2, F) * 2.0 ** -22).float().cuda()
+    us = torch.from_numpy(rng.uniform(1, 2, F) * 2.0 ** 88).float().cuda()
+    bg, bu = (torch.from_numpy(rng.uniform(1, 2, F) * k).float().cuda() for k in (2.0 ** -126, 2.0 ** -14)) if bias else (None, None)
+    out, gate, up = (nans((M, F), torch.bfloat16) for _ in range(3))
+    dit.dit_gated_ffn_forward(x, wg, wu, out, gate=gate, up=up, bias_gate=bg, bias_up=bu, x_scale=xs, gate_scale=gs, up_scale=us)
+    assert (gate.float() >= 2.0 ** -126).all()
+    check_forward(out, gate, up, x, wg, wu, bg, bu, "silu", xs, gs, us)
