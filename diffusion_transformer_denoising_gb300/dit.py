@@ -665,7 +665,8 @@ def dit_gated_ffn_workspace_bytes(x, w_gate, *, backward=False) -> int:
     code, p = DTYPE_BF16 if operand == DTYPE_E4M3 else operand, 16 + 1  # a pointer that needs a copy
     scale = 16 if operand == DTYPE_E4M3 else 0
     F, D = w_gate.shape
-    for wanted in ((16, 16, 16), (0, 16, 0), (0, 16, 16)) if backward else ((0, 0, 0),):
+    # dx asks for its share beside the weights' gradients; one of these may split its rows where both would not
+    for wanted in ((16, 16, 16), (16, 16, 0)) if backward else ((0, 0, 0),):
         n = lib().dit_gated_ffn_workspace_bytes(_FFN_ARGS.pack(
             rows, D, F, code, operand, ACT_SILU, 0, p, D, p, D, p, D, scale, scale, scale, 0, 0, 16, F, 16, F, 16, F,
             *(v for w in wanted for v in (w, D)), 16 * backward, 16 * backward), int(backward))

@@ -272,3 +272,27 @@ def test_views_are_read_where_they_lie():
 def test_grad_norm_of_nothing_asks_for_some_workspace():
     assert dit.dit_grad_norm_workspace_bytes([]) == dit.dit_grad_norm_workspace_bytes([None, torch.zeros(0)]) == 8
     assert dit.dit_grad_norm_workspace_bytes([torch.zeros(2049)]) == 16
+
+
+# shapes whose products split K, for one weight's gradient where they do not for two, and for neither
+SPLITS = [(2048, 64, 2048), (4096, 512, 1024), (8192, 1024, 1024), (4096, 1000, 1000), (20000, 96, 96), (333, 1000, 2730),
+          (64, 32, 48), (33, 4096, 64), (1 << 20, 64, 64), (1, 128, 128)]
+
+
+@pytest.mark.parametrize("M,D,F", SPLITS, ids=str)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+def test_gated_ffn_workspace_by_shapes_is_enough_for_every_choice(L, M, D, F, dtype):
+    x, w = torch.empty(1, dtype=dtype).expand(M, D), torch.empty(1, dtype=dtype).expand(F, D)
+    most = dit.dit_gated_ffn_workspace_bytes(x, w, backward=True)
+    forward = dit.dit_gated_ffn_workspace_bytes(x, w)
+    code = dit.DTYPE_BF16 if dtype is torch.bfloat16 else dit.DTYPE_F16
+    base, needed = dict(rows=M, width=D, hidden=F, dtype=code), 0
+    for odd in (0, 1):
+        views = dict(x=(1 << 20) + 2, wg_s=D + 1, wu_s=D + 1) if odd else {}
+        assert L.dit_gated_ffn_workspace_bytes(ffn_args(**base, **views), 0) <= forward
+        for choice in range(16):
+            kept = {k: BWD[k] for i, k in enumerate(("dx", "dwg", "dwu", "dbg")) if choice >> i & 1}
+            n = L.dit_gated_ffn_workspace_bytes(ffn_args(**base, **views, gate=5 << 20, up=6 << 20, **kept), 1)
+            assert 0 <= n <= most, (odd, kept)
+            needed = max(needed, n)
+    assert needed == most
