@@ -704,9 +704,11 @@ def _grad_tensors(grads, clipped):
         outs = pointers
     else:
         made = [c for c in clipped if c is not None]
-        if (len(clipped) != len(grads) or len(made) != n or list(map(T.numel, made)) != sizes or
-                list(map(_dtype_of, made)) != dtypes or not all(map(T.is_contiguous, made))):
-            _refuse(DIT_ERR_SHAPE, "clipped must hold a contiguous tensor of the size and type of each gradient")
+        # None at the same places: an entry left out in only one list would shift all behind it
+        if (len(clipped) != len(grads) or
+                (n < len(grads) or len(made) < len(clipped)) and [g is None for g in grads] != [c is None for c in clipped] or
+                list(map(T.numel, made)) != sizes or list(map(_dtype_of, made)) != dtypes or not all(map(T.is_contiguous, made))):
+            _refuse(DIT_ERR_SHAPE, "clipped must hold a contiguous tensor of the size and type of each gradient at its place")
         outs = list(map(T.data_ptr, made))
     # structures of four 64-bit fields (the type and the reserved field as one)
     fields = array.array("q", bytes(32 * n))
@@ -719,9 +721,10 @@ def dit_grad_norm(grads, norm, *, max_norm=None, clipped=None, workspace=None, s
     """norm (a float32 CUDA tensor of one element) = the 2-norm of all tensors of
     the list `grads` together (None entries are left out).  With max_norm they
     are multiplied by max_norm / norm where norm is above it, in place or into
-    the list `clipped`; a norm that is not finite leaves the values as they
-    are.  workspace: a contiguous tensor of dit_grad_norm_workspace_bytes, or
-    None to take one from torch's allocator (only on torch's current stream)."""
+    the tensors at the same places of the list `clipped`; a norm that is not
+    finite leaves the values as they are.  workspace: a contiguous tensor of
+    dit_grad_norm_workspace_bytes, or None to take one from torch's allocator
+    (only on torch's current stream)."""
     torch = _torch or _use_torch()
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)

@@ -296,3 +296,13 @@ def test_gated_ffn_workspace_by_shapes_is_enough_for_every_choice(L, M, D, F, dt
             assert 0 <= n <= most, (odd, kept)
             needed = max(needed, n)
     assert needed == most
+
+
+def test_clipped_entries_belong_to_the_gradients_at_their_places():
+    a, b, c, d = (torch.ones(4) for _ in range(4))
+    norm = torch.zeros(())
+    refused(SHAPE, dit.dit_grad_norm, [None, a, b], norm, max_norm=1.0, clipped=[c, None, d])
+    refused(SHAPE, dit.dit_grad_norm, [a, None], norm, max_norm=1.0, clipped=[None, c])
+    refused(SHAPE, dit.dit_grad_norm, (g for g in (None, a)), norm, max_norm=1.0, clipped=(g for g in (c, None)))
+    # at the same places they are taken: the next check is the device's
+    assert "CUDA" in refused(INVALID, dit.dit_grad_norm, [None, a, b], norm, max_norm=1.0, clipped=[None, c, d])
