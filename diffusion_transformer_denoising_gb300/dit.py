@@ -594,7 +594,10 @@ def _ffn_args(x, w_gate, w_up, out, gate, up, act, x_scale=None, gate_scale=None
     _torch or _use_torch()
     if _grad_mode() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad or
                          bias_gate is not None and bias_gate.requires_grad or
-                         bias_up is not None and bias_up.requires_grad):
+                         bias_up is not None and bias_up.requires_grad or
+                         x_scale is not None and x_scale.requires_grad or
+                         gate_scale is not None and gate_scale.requires_grad or
+                         up_scale is not None and up_scale.requires_grad):
         _refuse_autograd()
     xs, ws = x.shape, w_gate.shape
     if len(xs) < 1 or len(ws) != 2 or ws[1] != xs[-1]:

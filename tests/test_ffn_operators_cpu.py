@@ -306,3 +306,14 @@ def test_clipped_entries_belong_to_the_gradients_at_their_places():
     refused(SHAPE, dit.dit_grad_norm, (g for g in (None, a)), norm, max_norm=1.0, clipped=(g for g in (c, None)))
     # at the same places they are taken: the next check is the device's
     assert "CUDA" in refused(INVALID, dit.dit_grad_norm, [None, a, b], norm, max_norm=1.0, clipped=[None, c, d])
+
+
+def test_scales_that_require_grad_are_refused():
+    x, g, u = (torch.zeros(s).to(torch.float8_e4m3fn) for s in ((3, 16), (6, 16), (6, 16)))
+    out = torch.zeros(3, 6, dtype=torch.bfloat16)
+    for bad in range(3):
+        xs, gs, us = (torch.ones(n).requires_grad_(i == bad) for i, n in enumerate((3, 6, 6)))
+        call = lambda: dit.dit_gated_ffn_forward(x, g, u, out, x_scale=xs, gate_scale=gs, up_scale=us)
+        assert "requires grad" in refused(INVALID, call)
+        with torch.no_grad():
+            assert "CUDA" in refused(INVALID, call)
