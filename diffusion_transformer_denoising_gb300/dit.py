@@ -204,13 +204,15 @@ _torch = None          # the module, its dtypes as dit.h names them and its grad
 _dtype_codes = {}
 _operand_codes = {}    # and e4m3
 _grad_mode = None
+_forward_ad = None
 
 
 def _use_torch():
-    global _torch, _grad_mode
+    global _torch, _grad_mode, _forward_ad
     if _torch is None:
         import torch
-        _grad_mode = torch.is_grad_enabled
+        import torch.autograd.forward_ad
+        _grad_mode, _forward_ad = torch.is_grad_enabled, torch.autograd.forward_ad
         _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
         _operand_codes.update(_dtype_codes)
         _operand_codes[torch.float8_e4m3fn] = DTYPE_E4M3
@@ -249,6 +251,14 @@ def _refuse_autograd():
     of are refused."""
     _refuse(DIT_ERR_INVALID_ARG, "a tensor requires grad: autograd does not see this call (run it under torch.no_grad(), "
                                  "or inside a torch.autograd.Function with the backward call)")
+
+
+def _refuse_tangents(*inputs):
+    """Inside a dual level of torch.autograd.forward_ad (whatever the grad mode is): inputs with a tangent are refused, for
+    the calls write values only."""
+    for t in inputs:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            _refuse(DIT_ERR_INVALID_ARG, "a tensor has a forward-mode tangent, which this call would lose (unpack the dual tensor)")
 
 
 def _raw_stream(t, stream):
@@ -320,6 +330,8 @@ def _rope_args(pos, axes, theta, style, eps, first, q, k):
             if (x is not None and x.requires_grad or weight is not None and weight.requires_grad or
                     dy is not None and dy.requires_grad):
                 _refuse_autograd()
+    if _forward_ad._current_level >= 0:
+        _refuse_tangents(pos, *q[:2], q[3], *k[:2], k[3])
     if first.dim() != 4:
         _refuse(DIT_ERR_SHAPE, "q must be [batch, tokens, heads, head_dim]")
     B, N, _, d = first.shape
@@ -352,7 +364,8 @@ def dit_rope_forward(pos, q, q_out, k=None, k_out=None, *, axes, theta=1e4, styl
     Views may have any strides with contiguous heads; k may have its own
     number of heads (see dit_rope_forward in include/dit.h).  Nothing is
     recorded for autograd, so with grad mode on an input that requires grad is
-    refused, here and in the calls below."""
+    refused, here and in the calls below; one with a forward-mode tangent is
+    always."""
     args = _rope_args(pos, axes, theta, style, eps, q, (q, None, q_out, q_weight, None),
                       (k, None, k_out, k_weight, None))
     status = lib().dit_rope_forward(args, _raw_stream(q, stream))
@@ -422,6 +435,8 @@ def _gn_args(x, dy, out, groups, weight, bias, mean, rstd, dweight, dbias, eps, 
                                              bias is not None and bias.requires_grad or
                                              dy is not None and dy.requires_grad):
         _refuse_autograd()
+    if out is not None and _forward_ad._current_level >= 0:
+        _refuse_tangents(x, weight, bias, dy, mean, rstd)
     shape, dtype = x.shape, x.dtype
     if len(shape) < 3:
         _refuse(DIT_ERR_SHAPE, "x must be [batch, ..., channels]")
@@ -507,6 +522,8 @@ def _norm_args(x, residual, total, dy, out, out_dtype, scale, weight, dweight, e
     if _grad_mode() and (x.requires_grad or residual is not None and residual.requires_grad or
                          weight is not None and weight.requires_grad or dy is not None and dy.requires_grad):
         _refuse_autograd()
+    if _forward_ad._current_level >= 0:
+        _refuse_tangents(x, residual, weight, dy)
     shape, dtype = x.shape, x.dtype
     B, N, C = _norm_rows(shape)
     code = _dtype_code(dtype)
@@ -599,6 +616,8 @@ def _ffn_args(x, w_gate, w_up, out, gate, up, act, x_scale=None, gate_scale=None
                          gate_scale is not None and gate_scale.requires_grad or
                          up_scale is not None and up_scale.requires_grad):
         _refuse_autograd()
+    if _forward_ad._current_level >= 0:
+        _refuse_tangents(x, w_gate, w_up, x_scale, gate_scale, up_scale, bias_gate, bias_up)
     xs, ws = x.shape, w_gate.shape
     if len(xs) < 1 or len(ws) != 2 or ws[1] != xs[-1]:
         _refuse(DIT_ERR_SHAPE, f"x is {list(xs)} and w_gate {list(ws)}: [..., width] and [hidden, width] are wanted")
@@ -648,10 +667,11 @@ def dit_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, *, dx=None, dw_gate=
     """Gradient of dit_gated_ffn_forward from the gate and up that it kept.  Each
     of dx, dw_gate, dw_up (of the inputs' type) and dbias_gate, dbias_up (float32
     [hidden]) is overwritten where given."""
-    if gate.requires_grad or up.requires_grad or dout.requires_grad:
-        _torch or _use_torch()
-        if _grad_mode():
-            _refuse_autograd()
+    _torch or _use_torch()
+    if (gate.requires_grad or up.requires_grad or dout.requires_grad) and _grad_mode():
+        _refuse_autograd()
+    if _forward_ad._current_level >= 0:
+        _refuse_tangents(gate, up, dout)
     args = _ffn_args(x, w_gate, w_up, dout, gate, up, act, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dbias_gate=dbias_gate,
                      dbias_up=dbias_up)
     L, s = lib(), _raw_stream(x, stream)
@@ -700,6 +720,8 @@ def _grad_tensors(grads, clipped):
         _refuse(DIT_ERR_SHAPE, "gradients must be contiguous")
     if _grad_mode() and any(map(_requires_grad_of, live)):
         _refuse_autograd()
+    if _forward_ad._current_level >= 0:
+        _refuse_tangents(*live)
     n = len(live)
     if clipped is None:
         outs = [0] * n

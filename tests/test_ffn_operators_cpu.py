@@ -317,3 +317,36 @@ def test_scales_that_require_grad_are_refused():
         assert "requires grad" in refused(INVALID, call)
         with torch.no_grad():
             assert "CUDA" in refused(INVALID, call)
+
+
+def test_forward_mode_tangents_are_refused():
+    """The calls write primal values only: a tangent would be lost without a word."""
+    import torch.autograd.forward_ad as fwd
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    f32 = lambda *s: torch.zeros(s)
+    ffn = (bf(3, 16), bf(6, 16), bf(6, 16))
+    calls = {  # inputs that a tangent may come with, and the call on them
+        "rope": ([bf(1, 4, 2, 8), f32(8), bf(1, 4, 2, 8)],
+                 lambda q, w, k: dit.dit_rope_forward(torch.zeros(4, 1, dtype=torch.int32), q, bf(1, 4, 2, 8), k, bf(1, 4, 2, 8),
+                                                      axes=(8,), q_weight=w, k_weight=f32(8))),
+        "group norm": ([bf(1, 4, 8), f32(8), f32(8)], lambda x, w, b: dit.dit_group_norm_forward(x, bf(1, 4, 8), 2, weight=w, bias=b)),
+        "rms norm": ([bf(3, 16), bf(3, 16), f32(16)], lambda x, r, w: dit.dit_rms_norm_forward(x, bf(3, 16), residual=r, weight=w)),
+        "rms norm gradient": ([bf(3, 16), bf(3, 16), bf(3, 16), f32(16)],
+                              lambda t, dy, dt, w: dit.dit_rms_norm_backward(t, dy, bf(3, 16), dtotal=dt, weight=w)),
+        "feed-forward": ([*ffn, f32(6), f32(6)],
+                         lambda x, g, u, bg, bu: dit.dit_gated_ffn_forward(x, g, u, bf(3, 6), bias_gate=bg, bias_up=bu)),
+        "feed-forward from e4m3": ([f32(3), f32(6), f32(6)],
+                                   lambda a, b, c: dit.dit_gated_ffn_forward(*(t.to(torch.float8_e4m3fn) for t in ffn), bf(3, 6),
+                                                                             x_scale=a, gate_scale=b, up_scale=c)),
+        "feed-forward gradient": ([*ffn, bf(3, 6), bf(3, 6), bf(3, 6)], lambda *a: dit.dit_gated_ffn_backward(*a, dx=bf(3, 16))),
+        "gradient norm": ([f32(4), bf(5)], lambda *g: dit.dit_grad_norm(list(g), torch.zeros(()))),
+    }
+    for name, (inputs, call) in calls.items():
+        with fwd.dual_level():
+            for i, t in enumerate(inputs):
+                args = [fwd.make_dual(t, torch.ones_like(t)) if i == j else v for j, v in enumerate(inputs)]
+                assert "tangent" in refused(INVALID, call, *args), (name, i)
+                with torch.no_grad():   # which leaves tangents alone
+                    assert "tangent" in refused(INVALID, call, *args), (name, i)
+            assert "CUDA" in refused(INVALID, call, *inputs), name   # without one
+        assert "CUDA" in refused(INVALID, call, *inputs), name
