@@ -15,7 +15,7 @@ struct ColumnSums {
   int n;
   int64_t second;       // floats from the first sum's columns to the second's
   float* out[2];
-  int late;             // the kernels before the previous one have written what is read
+  int late;             // the kernels before the previous one have written what is read (launch.cuh)
 };
 constexpr int kSumColumns = 8, kSumStrands = 64;
 template <int UNUSED = 0>
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kSumColumns * kSumStrands) column_sums_kernel(
     for (int64_t r = strand; r < a.rows; r += U * kSumStrands) {
       float v[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[i] = r + i * kSumStrands < a.rows ? p[(r + i * kSumStrands) * a.pitch] : 0.f;
+      for (int i = 0; i < U; ++i) v[i] = r + i * kSumStrands < a.rows ? __ldcg(p + (r + i * kSumStrands) * a.pitch) : 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i) s.add(v[i]);
     }

@@ -734,7 +734,7 @@ struct Join {
   int64_t M;
   int N;
   int f16, act;
-  int late;  // the kernels before the previous one have written what is read
+  int late;  // the kernels before the previous one have written what is read (launch.cuh)
 };
 
 DIT_DEV void store4(void* base, int64_t at, int n, int f16, const float (&v)[4]) {
@@ -750,10 +750,10 @@ DIT_DEV void store4(void* base, int64_t at, int n, int f16, const float (&v)[4])
   if (n > 3) p[3] = (uint16_t)(b >> 16);
 }
 DIT_DEV void sum_planes(const float* p, int64_t step, int n, float (&v)[4]) {
-  float4 s = *reinterpret_cast<const float4*>(p);
+  float4 s = __ldcg(reinterpret_cast<const float4*>(p));
 #pragma unroll 4
   for (int z = 1; z < n; ++z) {
-    const float4 t = *reinterpret_cast<const float4*>(p + z * step);
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(p + z * step));
     s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
   }
   v[0] = s.x, v[1] = s.y, v[2] = s.z, v[3] = s.w;

@@ -8,7 +8,13 @@ namespace dit {
 
 // Programmatic dependence between a kernel and the next of the same call: the
 // first lets the second start early, the second waits for the first's results
-// before it touches anything that kernel reads or writes.
+// before it touches anything that kernel reads or writes.  One that is marked late reads
+// before that wait, and only what the kernels before the previous one wrote: each block of
+// the previous one has waited for them (wait_previous) before it let this one start
+// (start_next), so they have ended.  It reads past L1 (__ldcg), which may hold what an
+// earlier launch found there, and waits before it ends, so that the call's end is that of
+// all its kernels.  (Without it the gradient of 64 x 256 x 1024 takes 14.8 us, with it 11.6;
+// of 333 x 1000 x 2730 32.3 and 30.5.)
 DIT_DEV void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 DIT_DEV void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
