@@ -857,7 +857,12 @@ DIT_DEV uint4 load8(const uint16_t* p, int n) {
   }
 }
 
-// 256 columns (8 a lane) x rows_per_block rows a block, 8 x ROWS rows at a time.
+// 256 columns (8 a lane) x rows_per_block rows a block, 8 x ROWS rows at a time.  dgate and
+// dup are rounded to the type: the tensor cores want both operands of a product in it, and
+// x and the weights are there.  That leaves dx and the weights' gradients 2.35e-3 of their
+// norm off in bf16 and 2.9e-4 in fp16, where their own rounding alone makes 1.66e-3 and
+// 2.1e-4; tf32 operands would keep all but run at half the rate on twice the bytes, of
+// widened copies of x and the weights too.  The bias sums take them unrounded.
 template <typename T, int ACT, int ALIGN>
 __global__ void __launch_bounds__(256) slopes_kernel(const Slopes a) {
   constexpr int ROWS = 2;
@@ -933,9 +938,10 @@ struct Split {
 // about 300 on 128 x 128 (256 at that rate); a launch fills and drains in about 4000,
 // and partial sums cost their traffic (written and read, fp32) and a launch.
 //
-// No split is longer than kLongest blocks: the tensor cores' fp32 sums lose up to 2^-23
-// of themselves at each step, to one side (16.8 M rows of terms of one sign, 1 M a
-// split: dW 6.6e-3 too small), and a wait for a tile has a limit in time.
+// No split is longer than kLongest blocks, 4096 steps of the tensor cores (65536 terms of 16
+// bits, 131072 of e4m3): their fp32 sums lose up to 2^-23 of themselves at each step, to
+// one side (16.8 M rows of terms of one sign, 1 M a split: dW 6.6e-3 too small), and a
+// wait for a tile has a limit in time.
 constexpr int64_t kLongest = 1024;
 Split choose(int64_t M, int64_t N, int64_t cols_per_n, int64_t k_blocks, int problems) {
   Split best{false, 1};

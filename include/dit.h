@@ -368,7 +368,9 @@ int64_t dit_group_norm_workspace_bytes(const dit_group_norm_args* a, int backwar
  * and zeros.  The outputs total and out may be the very view of x or of residual
  * (out only in the type of x).  Arithmetic is fp32, the squares' sum too: a row
  * with values of 1e19 and more counts as one of infinite norm, its y is 0; squares
- * of values below 1e-19 lose digits, which an eps as small does not hide. */
+ * of values below 1e-19 lose digits, which an eps as small does not hide.  The
+ * gradient of a row past 1e19 is dtotal alone, or NaN where the sum of weight *
+ * total * dy overflows. */
 enum { DIT_RMS_NORM_MAX_CHANNELS = 16384 };
 typedef struct {
   int64_t batch;
@@ -411,10 +413,10 @@ int64_t dit_rms_norm_workspace_bytes(const dit_rms_norm_args* a);
  * weights are e4m3, x * x_scale[row] and w * scale[channel] the values they
  * stand for; forward only.  A sum is multiplied by the channel's scale, then by
  * the row's: any normal number as x_scale, 2^-100 to 2^90 as the others keep all
- * its digits.  Sums are fp32 on the tensor cores, every output is
- * rounded once.  No output has a byte in common with an input.  Operands whose
- * pointer or stride is no multiple of 16 bytes are copied into the workspace
- * first, but for up to 32 rows in the forward call. */
+ * its digits.  Sums are fp32 on the tensor cores, every output is rounded once.  No
+ * output has a byte in common with an input.  Operands whose pointer or stride is
+ * no multiple of 16 bytes are copied into the workspace first, but for up to 32
+ * rows in the forward call. */
 typedef struct {
   int64_t rows;
   int32_t width;             /* 1 .. 2^17                                                   */
@@ -453,8 +455,10 @@ typedef struct {
 dit_status dit_gated_ffn_forward(const dit_gated_ffn_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 /* The gradient from the gate and up that the forward call kept.  The gradients
  * of gate and up are formed in fp32, summed into dbias_* as they are, and
- * rounded to dtype as operands of the products; dx, dw_gate and dw_up are fp32
- * sums rounded to dtype (overwritten; zero for no rows). */
+ * rounded to dtype as operands of the products (in fp16 those above 65504 become
+ * infinite and those below 6e-5 lose digits, as between separate calls: a scaled
+ * loss keeps them in range); dx, dw_gate and dw_up are fp32 sums rounded to dtype
+ * (overwritten; zero for no rows). */
 dit_status dit_gated_ffn_backward(const dit_gated_ffn_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 /* Bytes of workspace of the forward (backward == 0) or the backward call
  * (host-only query; pointers are read as present, NULL or aligned only);

@@ -1139,3 +1139,59 @@ def test_gated_ffn_of_rows_with_tiny_scales(M, D, F, bias):
     dit.dit_gated_ffn_forward(x, wg, wu, out, gate=gate, up=up, bias_gate=bg, bias_up=bu, x_scale=xs, gate_scale=gs, up_scale=us)
     assert (gate.float() >= 2.0 ** -126).all()
     check_forward(out, gate, up, x, wg, wu, bg, bu, "silu", xs, gs, us)
+
+
+def among_nans(t, left=16):
+    """t in the middle of a buffer of NaN, its rows `left` elements and 24 more apart."""
+    wide = nans((t.shape[0] + 2, t.shape[1] + left + 24), torch.float32).to(t.dtype) if t.dim() == 2 else nans((t.numel() + left + 24,), t.dtype)
+    view = wide[1:-1, left:left + t.shape[1]] if t.dim() == 2 else wide[left:left + t.numel()]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("operands", ["same", "e4m3"])
+@pytest.mark.parametrize("left", [16, 4, 3])   # rows of vectors, of words, of elements
+@pytest.mark.parametrize("M,D,F", [(1, 72, 40), (7, 65, 33), (19, 100, 17), (32, 256, 129), (33, 72, 64), (130, 65, 67), (300, 520, 264),
+                                   (40, 4096, 72), (2600, 264, 1288)])
+def test_gated_ffn_reads_nothing_beside_its_operands(M, D, F, left, operands):
+    rng = np.random.default_rng(M + D)
+    x, wg, wu = (randn(rng, s, "bf16", 0.3) for s in ((M, D), (F, D), (F, D)))
+    around = lambda t: among_nans(t, left)
+    vector = lambda n, lo: around(torch.from_numpy(rng.uniform(lo, 1, n)).float().cuda())
+    scales, kw = (None,) * 3, dict(bias_gate=vector(F, -1), bias_up=vector(F, -1))
+    if operands == "e4m3":
+        (x, xs), (wg, gs), (wu, us) = quantised(x), quantised(wg), quantised(wu)
+        xs, gs, us = (among_nans(s, 0) if s.numel() == M else around(s) for s in (xs, gs, us))
+        scales = xs, gs, us
+        kw.update(x_scale=xs, gate_scale=gs, up_scale=us)
+    x, wg, wu = around(x), around(wg), around(wu)
+    out, gate, up = (torch.zeros(M, F, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    dit.dit_gated_ffn_forward(x, wg, wu, out, gate=gate, up=up, **kw)
+    check_forward(out, gate, up, x, wg, wu, kw["bias_gate"], kw["bias_up"], "silu", *scales)
+    if operands == "e4m3":
+        return
+    gate, up, dout = around(gate), around(up), around(randn(rng, (M, F), "bf16"))
+    made = dict(dx=torch.zeros(M, D, dtype=torch.bfloat16, device="cuda"), dw_gate=torch.zeros(F, D, dtype=torch.bfloat16, device="cuda"),
+                dw_up=torch.zeros(F, D, dtype=torch.bfloat16, device="cuda"), dbias_gate=torch.zeros(F, device="cuda"), dbias_up=torch.zeros(F, device="cuda"))
+    dit.dit_gated_ffn_backward(x, wg, wu, gate, up, dout, **made)
+    plain = {k: torch.zeros_like(t) for k, t in made.items()}
+    alone = [t.contiguous() for t in (x, wg, wu, gate, up, dout)]
+    dit.dit_gated_ffn_backward(*alone, **plain)
+    for k, t in made.items():
+        assert torch.equal(t, plain[k]) and torch.isfinite(t).all(), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 7, 8, 2047, 2049, 16384, 16391, 40001])
+def test_grad_norm_reads_and_writes_nothing_beside_its_tensors(dtype, n):
+    rng = np.random.default_rng(n)
+    for left in range(9):
+        big, made = nans((n + 32,), DT[dtype]), nans((n + 32,), DT[dtype])
+        g, c = big[left:left + n], made[(3 * left) % 8:][:n]
+        g.copy_(torch.from_numpy(rng.standard_normal(n)))
+        norm = nans((), torch.float32)
+        dit.dit_grad_norm([g], norm, max_norm=0.5, clipped=[c])
+        ref = O.grad_norm([n64(g)])
+        assert abs(norm.item() - ref) <= 16 * ULP * ref
+        near(c, n64(g) * O.clip_factor(ref, 0.5), 24 * ULP * np.abs(n64(g) * O.clip_factor(ref, 0.5)))
+        assert int(torch.isnan(big).sum()) == 32 and int(torch.isnan(made).sum()) == 32
